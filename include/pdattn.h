@@ -335,6 +335,79 @@ pdattn_status pdattn_packed_attend(const pdattn_params* p, int32_t n_tokens, con
                                    size_t workspace_bytes, pdattn_stream stream);
 
 /*
+ * Coded cache: a paged KV cache held in 8 bits.  For every token and kv head
+ * the key and the value are D codes of one f32 scale,
+ *   scale = max(max_d |x_d| / qmax, 2^-126),  code_d = rne(x_d / scale),
+ *   x_d ~ code_d * scale,
+ * each step one f32 operation, with qmax 448 (e4m3) or 127 (int8, codes in
+ * [-127, 127]).  x is the f32 value: a key is coded after its rotation with
+ * no rounding to T in between.  A key or value that holds an infinity or a
+ * NaN gets the scale NaN and stands for NaN throughout; outputs that see
+ * such a token are NaN in every dimension, and no other output changes.
+ * Pages are shared and slots addressed as in the cache of T above.  The four
+ * calls below take T = bf16 or f32 (pdattn_coded_prefill: bf16) and the same
+ * head dims, groups, windows, scales, rope tables and sinks.  Codes and
+ * scales are 16-byte aligned.  Scales that no call has written may hold
+ * anything where no output sees them.
+ */
+typedef enum { PDATTN_E4M3 = 0, PDATTN_INT8 = 1 } pdattn_code;
+
+typedef struct {
+    void* k;                /* [num_pages, kv_heads, 64, head_dim] codes */
+    void* v;
+    float* k_scale;         /* [num_pages, kv_heads, 64] */
+    float* v_scale;
+    int32_t code;           /* pdattn_code */
+    int32_t reserved;       /* must be 0 */
+} pdattn_coded_cache;
+
+/*
+ * Bytes of workspace for the coded calls (0 if the parameters are invalid):
+ * pdattn_coded_decode of p->rows rows, pdattn_coded_prefill of up to n_tokens
+ * tokens, pdattn_coded_write and pdattn_coded_read of any number.  Zero-fill
+ * it once before first use.  Calls that share it must be ordered.
+ */
+size_t pdattn_coded_workspace_size(const pdattn_params* p, int32_t n_tokens);
+
+/*
+ * Codes n_tokens new keys (rotated at positions[i]) and values into slot
+ * slots[i] (page slots[i] / 64, offset slots[i] % 64) of the pools.  k_new,
+ * v_new [n_tokens, kv_heads, head_dim]; positions, slots [n_tokens] int32.
+ * The slots of one call must differ.  A slot outside the pools is recorded
+ * as PDATTN_EBADPAGE, a negative position or one past the rope table as
+ * PDATTN_EBADPOS; that token is not written.  Of the workspace only the
+ * status word is used (256 bytes are enough).  Of p, rows, pages_per_row,
+ * window, scale and sinks are not used.
+ */
+pdattn_status pdattn_coded_write(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,
+                                 const void* k_new, const void* v_new, const int32_t* positions,
+                                 const int32_t* slots, void* workspace, size_t workspace_bytes,
+                                 pdattn_stream stream);
+
+/*
+ * Reads slots back: k_out[i], v_out[i] [kv_heads, head_dim] of T are code *
+ * scale of slot slots[i] (one f32 product, one rounding to T).  Slots may
+ * repeat.  A slot outside the pools is recorded as PDATTN_EBADPAGE and that
+ * token's outputs stay as they were.  Workspace and p as in
+ * pdattn_coded_write; the cache is not written.
+ */
+pdattn_status pdattn_coded_read(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,
+                                const int32_t* slots, void* k_out, void* v_out, void* workspace,
+                                size_t workspace_bytes, pdattn_stream stream);
+
+/*
+ * pdattn_decode_fused over a coded cache: rotates q and k_new, codes k_new
+ * and v_new into the slot of position positions[r] through table[r], then
+ * attends over what the codes stand for.  Queries are not rounded to T
+ * (the kernels hold them, and the weights, in f16 with a scale of their own;
+ * for f32 in two f16 parts each); every sum is f32.
+ */
+pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cache* cache, const void* q,
+                                  const void* k_new, const void* v_new, const int32_t* positions,
+                                  const int32_t* table, void* out, void* workspace, size_t workspace_bytes,
+                                  pdattn_stream stream);
+
+/*
  * Synchronises `stream`, reads the workspace's device status word, clears
  * it and returns the first error it recorded (PDATTN_OK if none).  After
  * PDATTN_ETIMEOUT from decode attention the workspace's plan is withdrawn:

@@ -44,7 +44,16 @@ class Layer(ctypes.Structure):
     ]
 
 
+class CodedCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("code", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
 LAYERS_PER_LAUNCH = 32
+E4M3, INT8 = 0, 1
+_CODES = {torch.float8_e4m3fn: E4M3, torch.int8: INT8}
 
 
 def _load():
@@ -70,6 +79,10 @@ def _load():
         "pdattn_packed_workspace_size": (sz, [P, i32]),
         "pdattn_packed": (i32, [P, i32] + [vp] * 7 + [sz, vp]),
         "pdattn_packed_attend": (i32, [P, i32] + [vp] * 4 + [sz, vp]),
+        "pdattn_coded_workspace_size": (sz, [P, i32]),
+        "pdattn_coded_write": (i32, [P, ctypes.POINTER(CodedCache), i32] + [vp] * 5 + [sz, vp]),
+        "pdattn_coded_read": (i32, [P, ctypes.POINTER(CodedCache), i32] + [vp] * 4 + [sz, vp]),
+        "pdattn_coded_decode": (i32, [P, ctypes.POINTER(CodedCache)] + [vp] * 7 + [sz, vp]),
         "pdattn_check_status": (i32, [vp, vp]),
         "pdattn_last_error": (ctypes.c_char_p, []),
         "pdattn_last_launch_count": (i32, []),
@@ -326,6 +339,100 @@ def packed_attend(p, v, positions, out, ws, stream=None):
     _expect("out", out, (n, p.heads, p.head_dim), _dt(p))
     w, nb = _ws(ws)
     _check(lib.pdattn_packed_attend(ctypes.byref(p), n, _ptr(v), _ptr(positions), _ptr(out), w, nb, _stream(stream)))
+
+
+def make_coded_cache(p, k, v, k_scale, v_scale):
+    """Descriptor of a coded (8-bit) cache: codes k, v [num_pages, kv_heads, 64, D]
+    of torch.float8_e4m3fn or torch.int8 and their scales [num_pages, kv_heads, 64] f32."""
+    if not isinstance(k, torch.Tensor) or k.dtype not in _CODES:
+        raise ValueError("codes must be torch.float8_e4m3fn or torch.int8 tensors")
+    pool = (p.num_pages, p.kv_heads, 64, p.head_dim)
+    for name, t in (("k", k), ("v", v)):
+        _expect(name, t, pool, k.dtype)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _expect(name, t, pool[:3], torch.float32)
+    _same_device(k, v, k_scale, v_scale)
+    c = CodedCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _CODES[k.dtype], 0)
+    # the block holds raw pointers: keep the tensors alive as long as it lives
+    c._tensors = (k, v, k_scale, v_scale)
+    c._pool = pool
+    return c
+
+
+def new_coded_cache(p, code=torch.float8_e4m3fn, device="cuda"):
+    """An empty coded cache of p's pool shape (codes and scales zero); its tensors are
+    in cache._tensors: k, v, k_scale, v_scale."""
+    pool = (p.num_pages, p.kv_heads, 64, p.head_dim)
+    codes = [torch.zeros(pool, dtype=torch.uint8, device=device).view(code) for _ in range(2)]
+    return make_coded_cache(p, *codes, *(torch.zeros(pool[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def coded_workspace_size(p, n_tokens=0):
+    n = lib.pdattn_coded_workspace_size(ctypes.byref(p), n_tokens)
+    if n == 0:
+        raise PdattnError(EINVAL, lib.pdattn_last_error().decode() or "invalid parameters")
+    return n
+
+
+def new_coded_workspace(p, n_tokens=0, device="cuda"):
+    """A workspace for the coded calls: coded_decode of p.rows rows, coded_prefill of up to n_tokens tokens."""
+    return torch.zeros(coded_workspace_size(p, n_tokens), dtype=torch.uint8, device=device)
+
+
+def _same_device(*tensors):
+    """Every tensor on the current device: the calls launch there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def _check_coded(p, cache, ws, tokens, ints=(), table=None):
+    """Arguments of a coded call: tokens (name, tensor, heads) of [n, heads, D],
+    ints (name, tensor) of [n] int32.  Returns n and the workspace's arguments."""
+    if not isinstance(cache, CodedCache):
+        raise TypeError("cache must come from make_coded_cache or new_coded_cache")
+    if cache._pool != (p.num_pages, p.kv_heads, 64, p.head_dim):
+        raise ValueError(f"cache has pools {cache._pool}, the parameters another shape")
+    first = (tokens or ints)[0][1]
+    n = first.shape[0] if isinstance(first, torch.Tensor) and first.dim() else -1
+    for name, t, h in tokens:
+        _expect(name, t, (n, h, p.head_dim), _dt(p))
+    for name, t in ints:
+        _expect(name, t, (n,), torch.int32)
+    if table is not None:
+        _expect("table", table, (p.rows, p.pages_per_row), torch.int32)
+    w, nb = _ws(ws)
+    _same_device(cache._tensors[0], ws, *(t[1] for t in tokens), *(t[1] for t in ints),
+                 *(() if table is None else (table,)))
+    return n, w, nb
+
+
+def coded_write(p, cache, k_new, v_new, positions, slots, ws, stream=None):
+    """Codes of new keys (rotated at positions) and values [n, kv_heads, D] into pool slots [n] int32."""
+    n, w, nb = _check_coded(p, cache, ws, (("k_new", k_new, p.kv_heads), ("v_new", v_new, p.kv_heads)),
+                            (("positions", positions), ("slots", slots)))
+    _check(lib.pdattn_coded_write(ctypes.byref(p), ctypes.byref(cache), n, _ptr(k_new), _ptr(v_new), _ptr(positions),
+                                  _ptr(slots), w, nb, _stream(stream)))
+
+
+def coded_read(p, cache, slots, k_out, v_out, ws, stream=None):
+    """What the codes of pool slots [n] int32 stand for, as k_out, v_out [n, kv_heads, D]."""
+    n, w, nb = _check_coded(p, cache, ws, (("k_out", k_out, p.kv_heads), ("v_out", v_out, p.kv_heads)),
+                            (("slots", slots),))
+    _check(lib.pdattn_coded_read(ctypes.byref(p), ctypes.byref(cache), n, _ptr(slots), _ptr(k_out), _ptr(v_out), w, nb,
+                                 _stream(stream)))
+
+
+def coded_decode(p, cache, q, k_new, v_new, positions, table, out, ws, stream=None):
+    """decode_fused over a coded cache."""
+    _check_coded(p, cache, ws, (("q", q, p.heads), ("k_new", k_new, p.kv_heads), ("v_new", v_new, p.kv_heads),
+                                ("out", out, p.heads)), (("positions", positions),), table)
+    if q.shape[0] != p.rows:
+        raise ValueError(f"q has {q.shape[0]} rows, the parameters {p.rows}")
+    w, nb = _ws(ws)
+    _check(lib.pdattn_coded_decode(ctypes.byref(p), ctypes.byref(cache), _ptr(q), _ptr(k_new), _ptr(v_new),
+                                   _ptr(positions), _ptr(table), _ptr(out), w, nb, _stream(stream)))
 
 
 def check_status(ws, stream=None):

@@ -715,6 +715,206 @@ pdattn_status pdattn_packed_attend(const pdattn_params* p, int32_t n_tokens, con
                        false);
 }
 
+// ---------------------------------------------------------------------------
+// Coded (8-bit) cache
+// ---------------------------------------------------------------------------
+static pdattn_status check_coded(const pdattn_params* p, const pdattn_coded_cache* c) {
+    pdattn_status s = check_params(p);
+    if (s != PDATTN_OK) return s;
+    if (!c) return fail(PDATTN_EINVAL, "cache is NULL");
+    if (c->code != PDATTN_E4M3 && c->code != PDATTN_INT8) return fail(PDATTN_EINVAL, "unknown code type %d", c->code);
+    if (c->reserved != 0) return fail(PDATTN_EINVAL, "reserved field must be 0");
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(PDATTN_EINVAL, "NULL cache pointer");
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+        return fail(PDATTN_EINVAL, "the cache's codes and scales must be 16-byte aligned");
+    return PDATTN_OK;
+}
+
+// A workspace of which only the status word is used.
+static pdattn_status check_status_ws(const void* ws, size_t bytes) {
+    if (!ws) return fail(PDATTN_EINVAL, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return fail(PDATTN_EINVAL, "workspace must be 256-byte aligned");
+    if (bytes < sizeof(Ctrl))
+        return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", bytes, sizeof(Ctrl));
+    return PDATTN_OK;
+}
+
+static CodeArgs code_args(const pdattn_params* p, const pdattn_coded_cache* c, int32_t n_tokens, const void* k_new,
+                          const void* v_new, const int32_t* positions, void* ws) {
+    CodeArgs a = {};
+    a.n_tokens = n_tokens;
+    a.heads = p->heads;
+    a.kv_heads = p->kv_heads;
+    a.head_dim = p->head_dim;
+    a.pages_per_row = p->pages_per_row;
+    a.num_pages = p->num_pages;
+    a.rope_len = p->rope_len;
+    a.scale_log2 = scale_log2(p);
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.positions = positions;
+    a.rope_cos = p->rope_cos;
+    a.rope_sin = p->rope_sin;
+    a.k = static_cast<uint8_t*>(c->k);
+    a.v = static_cast<uint8_t*>(c->v);
+    a.k_scale = c->k_scale;
+    a.v_scale = c->v_scale;
+    a.ws = static_cast<char*>(ws);
+    return a;
+}
+
+// Blocks of the coding and read launches stay within a grid's 2^31 - 1.
+static pdattn_status check_tokens(const pdattn_params* p, int32_t n_tokens) {
+    if (n_tokens < 0) return fail(PDATTN_EINVAL, "n_tokens < 0");
+    if ((long long)n_tokens * (p->heads + 2ll * p->kv_heads) >= (1ll << 31))
+        return fail(PDATTN_EUNSUPPORTED, "too many tokens for one call");
+    return PDATTN_OK;
+}
+
+pdattn_status pdattn_coded_write(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,
+                                 const void* k_new, const void* v_new, const int32_t* positions, const int32_t* slots,
+                                 void* workspace, size_t workspace_bytes, pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_coded(p, cache);
+    if (s != PDATTN_OK) return s;
+    if ((s = check_tokens(p, n_tokens)) != PDATTN_OK) return s;
+    if (n_tokens == 0) return PDATTN_OK;
+    if (!k_new || !v_new || !positions || !slots) return fail(PDATTN_EINVAL, "NULL data pointer");
+    if (!aligned16(k_new) || !aligned16(v_new)) return fail(PDATTN_EINVAL, "k_new and v_new must be 16-byte aligned");
+    if ((s = check_status_ws(workspace, workspace_bytes)) != PDATTN_OK) return s;
+    CodeArgs a = code_args(p, cache, n_tokens, k_new, v_new, positions, workspace);
+    a.slots = slots;
+    cudaError_t e = launch_code(a, p->dtype, cache->code, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "coded write launch");
+    g_launches = 1;
+    return PDATTN_OK;
+}
+
+pdattn_status pdattn_coded_read(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,
+                                const int32_t* slots, void* k_out, void* v_out, void* workspace,
+                                size_t workspace_bytes, pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_coded(p, cache);
+    if (s != PDATTN_OK) return s;
+    if ((s = check_tokens(p, n_tokens)) != PDATTN_OK) return s;
+    if (n_tokens == 0) return PDATTN_OK;
+    if (!slots || !k_out || !v_out) return fail(PDATTN_EINVAL, "NULL data pointer");
+    if (!aligned16(k_out) || !aligned16(v_out)) return fail(PDATTN_EINVAL, "k_out and v_out must be 16-byte aligned");
+    if ((s = check_status_ws(workspace, workspace_bytes)) != PDATTN_OK) return s;
+    ReadArgs a = {};
+    a.n_tokens = n_tokens;
+    a.kv_heads = p->kv_heads;
+    a.head_dim = p->head_dim;
+    a.num_pages = p->num_pages;
+    a.k = static_cast<const uint8_t*>(cache->k);
+    a.v = static_cast<const uint8_t*>(cache->v);
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.slots = slots;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.ws = static_cast<char*>(workspace);
+    cudaError_t e = launch_read(a, p->dtype, cache->code, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "coded read launch");
+    g_launches = 1;
+    return PDATTN_OK;
+}
+
+// Codes [num_pages, kv_heads, 64, D] as rows of D bytes: boxes of a page's 64
+// rows, swizzled over the row's bytes.
+static pdattn_status make_code_map(CUtensorMap* map, const void* codes, const pdattn_params* p) {
+    auto fn = encode_fn();
+    if (!fn) return fail(PDATTN_ECUDA, "cuTensorMapEncodeTiled is not available");
+    cuuint64_t dims[2] = {(cuuint64_t)p->head_dim, (cuuint64_t)p->num_pages * p->kv_heads * kPageSize};
+    cuuint64_t strides[1] = {(cuuint64_t)p->head_dim};
+    cuuint32_t box[2] = {(cuuint32_t)p->head_dim, (cuuint32_t)kPageSize};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    p->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PDATTN_ECUDA, "cuTensorMapEncodeTiled (codes) failed (%d)", (int)r);
+    return PDATTN_OK;
+}
+
+// Decode: the split plan's regions, then the coded query rows (f16, with the
+// remainder row for f32 inputs, and 16 bytes for the factor).
+static int coded_q_row(const pdattn_params* p) { return (p->dtype == PDATTN_F32 ? 4 : 2) * p->head_dim + 16; }
+
+static WsLayout coded_layout(const pdattn_params* p, int grid) {
+    WsLayout L = ws_layout(p->rows, p->heads, p->kv_heads, p->head_dim, p->pages_per_row, 0, p->chunk_pages, grid);
+    L.total = align256(L.q_rot + (size_t)p->rows * p->heads * coded_q_row(p));
+    return L;
+}
+
+size_t pdattn_coded_workspace_size(const pdattn_params* p, int32_t n_tokens) {
+    if (check_params(p) != PDATTN_OK || check_tokens(p, n_tokens) != PDATTN_OK) return 0;
+    const int grid = sm_count();
+    if (grid <= 0) return 0;
+    return coded_layout(p, grid).total;
+}
+
+pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cache* cache, const void* q,
+                                  const void* k_new, const void* v_new, const int32_t* positions,
+                                  const int32_t* table, void* out, void* workspace, size_t workspace_bytes,
+                                  pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_coded(p, cache);
+    if (s != PDATTN_OK) return s;
+    if ((s = check_tokens(p, p->rows)) != PDATTN_OK) return s;
+    if (p->rows == 0) return PDATTN_OK;
+    if (!q || !k_new || !v_new || !positions || !table || !out) return fail(PDATTN_EINVAL, "NULL data pointer");
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))
+        return fail(PDATTN_EINVAL, "q, k_new, v_new and out must be 16-byte aligned");
+    const int grid = sm_count();
+    if (grid <= 0) return fail(PDATTN_ECUDA, "no CUDA device");
+    if ((s = check_status_ws(workspace, workspace_bytes)) != PDATTN_OK) return s;
+    const WsLayout L = coded_layout(p, grid);
+    if (workspace_bytes < L.total)
+        return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, L.total);
+    char* ws = static_cast<char*>(workspace);
+    CUtensorMap km, vm;
+    if ((s = make_code_map(&km, cache->k, p)) != PDATTN_OK) return s;
+    if ((s = make_code_map(&vm, cache->v, p)) != PDATTN_OK) return s;
+    PrepArgs pa = prep_args(p, positions, table, ws, L, grid);
+    pa.do_plan = 1;
+    int n = 0;
+    cudaError_t e = launch_prep(pa, p->dtype, (cudaStream_t)stream, &n);
+    if (e != cudaSuccess) return cuda_fail(e, "plan launch");
+    CodeArgs ca = code_args(p, cache, p->rows, k_new, v_new, positions, ws);
+    ca.q = q;
+    ca.table = table;
+    ca.after_plan = 1;
+    ca.q_row_bytes = coded_q_row(p);
+    ca.q_split = p->dtype == PDATTN_F32;
+    ca.q_out = reinterpret_cast<uint8_t*>(ws + L.q_rot);
+    e = launch_code(ca, p->dtype, cache->code, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "coded rope/write launch");
+    AttendArgs aa = {};
+    aa.rows = p->rows;
+    aa.heads = p->heads;
+    aa.kv_heads = p->kv_heads;
+    aa.group = p->heads / p->kv_heads;
+    aa.head_dim = p->head_dim;
+    aa.pages_per_row = p->pages_per_row;
+    aa.num_pages = p->num_pages;
+    aa.window = p->window;
+    aa.chunk_pages = p->chunk_pages;
+    aa.q = ws + L.q_rot;
+    aa.positions = positions;
+    aa.table = table;
+    aa.sinks = p->sinks;
+    aa.out = out;
+    aa.ws = ws;
+    aa.L = L;
+    aa.k_scale = cache->k_scale;
+    aa.v_scale = cache->v_scale;
+    e = launch_attend_coded(aa, km, vm, p->dtype, cache->code, grid, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "coded attention launch");
+    g_launches = n + 2;
+    return PDATTN_OK;
+}
+
 pdattn_status pdattn_check_status(void* workspace, pdattn_stream stream) {
     if (!workspace) return fail(PDATTN_EINVAL, "workspace is NULL");
     cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);

@@ -1,0 +1,23 @@
+// Launcher of the decode attention over a coded (8-bit) cache; the kernel is
+// in attend_kernel.cuh, its consumer Consumer<T, D, G, Code>.
+#include "attend_kernel.cuh"
+
+namespace pdattn {
+
+template <typename T, int D>
+static cudaError_t launch_code_type(const AttendArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int code,
+                                    int grid, cudaStream_t stream) {
+    if (code == 0) return launch_one<T, D, kMaxGroup, NoLayers, E4m3>(a, k_map, v_map, grid, true, stream);
+    return launch_one<T, D, kMaxGroup, NoLayers, Int8>(a, k_map, v_map, grid, true, stream);
+}
+
+cudaError_t launch_attend_coded(const AttendArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
+                                int code, int grid, cudaStream_t stream) {
+    if (dtype == 0)
+        return a.head_dim == 128 ? launch_code_type<__nv_bfloat16, 128>(a, k_map, v_map, code, grid, stream)
+                                 : launch_code_type<__nv_bfloat16, 64>(a, k_map, v_map, code, grid, stream);
+    return a.head_dim == 128 ? launch_code_type<float, 128>(a, k_map, v_map, code, grid, stream)
+                             : launch_code_type<float, 64>(a, k_map, v_map, code, grid, stream);
+}
+
+}  // namespace pdattn

@@ -66,6 +66,8 @@ struct AttendArgs {
     void* out;
     char* ws;
     WsLayout L;
+    const float* k_scale;   // coded cache: [num_pages, kv_heads, 64]; q then holds code_kernel's rows
+    const float* v_scale;
 };
 
 struct PrefillPrepArgs {
@@ -97,6 +99,44 @@ struct PrefillArgs {
     PfLayout L;
 };
 
+// Rotation, coding and cache write of n tokens (csrc/coded.cu).  With q the
+// queries are rotated too, as f16 rows of q_row_bytes: D elements, with
+// q_split D more that hold what the first round off, and the row's factor
+// (after them, or in q_factor).
+struct CodeArgs {
+    int n_tokens, heads, kv_heads, head_dim, pages_per_row, num_pages, rope_len;
+    int after_plan;         // 1: a programmatic dependent of a planner launch
+    int q_row_bytes, q_split;
+    float scale_log2;
+    const void* q;          // nullptr: keys and values only
+    const void* k_new;
+    const void* v_new;
+    const int* positions;
+    const int* slots;       // [n_tokens] page * 64 + offset; nullptr: through the table at the token's position
+    const int* table;
+    const void* rope_cos;   // nullptr: no rotation
+    const void* rope_sin;
+    uint8_t* k;             // codes [num_pages, kv_heads, 64, head_dim]
+    uint8_t* v;
+    float* k_scale;         // [num_pages, kv_heads, 64]
+    float* v_scale;
+    uint8_t* q_out;
+    float* q_factor;
+    char* ws;
+};
+
+struct ReadArgs {
+    int n_tokens, kv_heads, head_dim, num_pages;
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    const int* slots;
+    void* k_out;            // [n_tokens, kv_heads, head_dim] of T
+    void* v_out;
+    char* ws;
+};
+
 cudaError_t launch_rope_tables(float theta, int D, int S, int dtype, void* cos_out, void* sin_out,
                                cudaStream_t stream);
 // The split planner (one block, if a.do_plan), then the rope + cache write of
@@ -112,6 +152,9 @@ cudaError_t launch_attend(const AttendArgs& a, const CUtensorMap& k_map, const C
 // Multi-layer attention: one persistent launch over every layer's items.
 cudaError_t launch_attend_layers(const AttendArgs& a, const AttendLayers& lay, int dtype, int grid,
                                  cudaStream_t stream);
+// The same over a coded cache (code 0: e4m3, 1: int8); maps over the codes.
+cudaError_t launch_attend_coded(const AttendArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
+                                int code, int grid, cudaStream_t stream);
 size_t attend_smem_bytes(int dtype, int head_dim);
 // The tile list (one block), then the rope + write of every token at its
 // slot (programmatic launch that ends after the tile list): two launches.
@@ -127,5 +170,8 @@ cudaError_t launch_packed_prep(const PrefillPrepArgs& a, int dtype, cudaStream_t
 // v_map over v, both [n, kv_heads, D] as 3-D tensors.
 cudaError_t launch_packed(const PrefillArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map,
                           const CUtensorMap& v_map, int grid, cudaStream_t stream);
+
+cudaError_t launch_code(const CodeArgs& a, int dtype, int code, cudaStream_t stream);
+cudaError_t launch_read(const ReadArgs& a, int dtype, int code, cudaStream_t stream);
 
 }  // namespace pdattn
