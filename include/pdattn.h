@@ -408,6 +408,20 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
                                   pdattn_stream stream);
 
 /*
+ * pdattn_prefill_paged over a coded cache: a chunk of new tokens (a prompt,
+ * part of one, or drafted tokens to check) is rotated, coded into its slots
+ * and attends its row's positions up to its own, over what the codes stand
+ * for.  Layouts, errors and rules are those of pdattn_prefill_paged; bf16
+ * only.  The products run on f16 tensor-core tiles (codes times the ratio of
+ * their scale to a power of two, 11 bits); few tokens over long rows are
+ * split along the keys and merged.
+ */
+pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,
+                                   const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                                   const int32_t* rows, const int32_t* slots, const int32_t* table, void* out,
+                                   void* workspace, size_t workspace_bytes, pdattn_stream stream);
+
+/*
  * Synchronises `stream`, reads the workspace's device status word, clears
  * it and returns the first error it recorded (PDATTN_OK if none).  After
  * PDATTN_ETIMEOUT from decode attention the workspace's plan is withdrawn:

@@ -83,6 +83,7 @@ def _load():
         "pdattn_coded_write": (i32, [P, ctypes.POINTER(CodedCache), i32] + [vp] * 5 + [sz, vp]),
         "pdattn_coded_read": (i32, [P, ctypes.POINTER(CodedCache), i32] + [vp] * 4 + [sz, vp]),
         "pdattn_coded_decode": (i32, [P, ctypes.POINTER(CodedCache)] + [vp] * 7 + [sz, vp]),
+        "pdattn_coded_prefill": (i32, [P, ctypes.POINTER(CodedCache), i32] + [vp] * 9 + [sz, vp]),
         "pdattn_check_status": (i32, [vp, vp]),
         "pdattn_last_error": (ctypes.c_char_p, []),
         "pdattn_last_launch_count": (i32, []),
@@ -433,6 +434,16 @@ def coded_decode(p, cache, q, k_new, v_new, positions, table, out, ws, stream=No
     w, nb = _ws(ws)
     _check(lib.pdattn_coded_decode(ctypes.byref(p), ctypes.byref(cache), _ptr(q), _ptr(k_new), _ptr(v_new),
                                    _ptr(positions), _ptr(table), _ptr(out), w, nb, _stream(stream)))
+
+
+def coded_prefill(p, cache, q, k_new, v_new, positions, rows, slots, table, out, ws, stream=None):
+    """prefill_paged over a coded cache (bf16)."""
+    n, w, nb = _check_coded(p, cache, ws, (("q", q, p.heads), ("k_new", k_new, p.kv_heads),
+                                           ("v_new", v_new, p.kv_heads), ("out", out, p.heads)),
+                            (("positions", positions), ("rows", rows), ("slots", slots)), table)
+    _check(lib.pdattn_coded_prefill(ctypes.byref(p), ctypes.byref(cache), n, _ptr(q), _ptr(k_new), _ptr(v_new),
+                                    _ptr(positions), _ptr(rows), _ptr(slots), _ptr(table), _ptr(out), w, nb,
+                                    _stream(stream)))
 
 
 def check_status(ws, stream=None):

@@ -847,11 +847,38 @@ static WsLayout coded_layout(const pdattn_params* p, int grid) {
     return L;
 }
 
+// Prefill: the tile lists and rotated queries of a prefill call, the query
+// factors, the sub-tiles and the partials of split tiles (bounds: split_tiles
+// in prep.cu).  Every region grows with n_tokens, so a workspace for n_tokens
+// serves fewer.
+struct CodedPfLayout {
+    PfLayout base;
+    size_t factor, units, part_ml, part_o, total;
+    int slot_rows;
+};
+
+static CodedPfLayout coded_pf_layout(const pdattn_params* p, int n_tokens, int grid) {
+    CodedPfLayout L;
+    const int g = p->heads / p->kv_heads, tile_tokens = 2 * (kPfRows / g);
+    L.base = pf_layout(n_tokens, p->heads, p->head_dim, 2);
+    L.slot_rows = (n_tokens < tile_tokens ? n_tokens : tile_tokens) * g;
+    const size_t slots = 4 * (size_t)grid;
+    size_t off = L.base.total;
+    L.factor = off; off = align256(off + sizeof(float) * (size_t)n_tokens * p->heads);
+    L.units = off; off = align256(off + sizeof(PfTile) * ((size_t)n_tokens + slots));
+    L.part_ml = off; off = align256(off + sizeof(float2) * slots * L.slot_rows);
+    L.part_o = off; off = align256(off + sizeof(float) * slots * L.slot_rows * p->head_dim);
+    L.total = off;
+    return L;
+}
+
 size_t pdattn_coded_workspace_size(const pdattn_params* p, int32_t n_tokens) {
     if (check_params(p) != PDATTN_OK || check_tokens(p, n_tokens) != PDATTN_OK) return 0;
     const int grid = sm_count();
     if (grid <= 0) return 0;
-    return coded_layout(p, grid).total;
+    const size_t decode = coded_layout(p, grid).total;
+    const size_t prefill = n_tokens > 0 ? coded_pf_layout(p, n_tokens, grid).total : 0;
+    return decode > prefill ? decode : prefill;
 }
 
 pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cache* cache, const void* q,
@@ -912,6 +939,112 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
     e = launch_attend_coded(aa, km, vm, p->dtype, cache->code, grid, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded attention launch");
     g_launches = n + 2;
+    return PDATTN_OK;
+}
+
+pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,
+                                   const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                                   const int32_t* rows, const int32_t* slots, const int32_t* table, void* out,
+                                   void* workspace, size_t workspace_bytes, pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_coded(p, cache);
+    if (s != PDATTN_OK) return s;
+    if ((s = check_tokens(p, n_tokens)) != PDATTN_OK) return s;
+    if (p->dtype != PDATTN_BF16) return fail(PDATTN_EUNSUPPORTED, "prefill runs on the tensor cores: dtype must be bf16");
+    if (p->rows <= 0) return fail(PDATTN_EINVAL, "prefill needs at least one table row");
+    if (n_tokens == 0) return PDATTN_OK;
+    if (!q || !k_new || !v_new || !positions || !rows || !slots || !table || !out)
+        return fail(PDATTN_EINVAL, "NULL data pointer");
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))
+        return fail(PDATTN_EINVAL, "q, k_new, v_new and out must be 16-byte aligned");
+    const int grid = sm_count();
+    if (grid <= 0) return fail(PDATTN_ECUDA, "no CUDA device");
+    if ((s = check_status_ws(workspace, workspace_bytes)) != PDATTN_OK) return s;
+    const CodedPfLayout L = coded_pf_layout(p, n_tokens, grid);
+    if (workspace_bytes < L.total)
+        return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, L.total);
+    char* ws = static_cast<char*>(workspace);
+    const int g = p->heads / p->kv_heads, tile_tokens = 2 * (kPfRows / g);
+
+    // Query rows (f16) [n_tokens, heads, D]: boxes as in prefill_impl.
+    auto fn = encode_fn();
+    if (!fn) return fail(PDATTN_ECUDA, "cuTensorMapEncodeTiled is not available");
+    CUtensorMap qm;
+    cuuint64_t dims[3] = {(cuuint64_t)p->head_dim, (cuuint64_t)p->heads, (cuuint64_t)n_tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)p->head_dim * 2, (cuuint64_t)p->heads * p->head_dim * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)(tile_tokens / 2)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(&qm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ws + L.base.q_rot, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PDATTN_ECUDA, "cuTensorMapEncodeTiled (queries) failed (%d)", (int)r);
+
+    // With at least two tiles per CTA for certain (a tile holds at most
+    // tile_tokens) no tile is split.
+    const long long sure = ((long long)n_tokens + tile_tokens - 1) / tile_tokens * p->kv_heads;
+    const bool split = sure < 2ll * grid;
+    PrefillPrepArgs pa = {};
+    pa.n_tokens = n_tokens;
+    pa.rows = p->rows;
+    pa.heads = p->heads;
+    pa.kv_heads = p->kv_heads;
+    pa.head_dim = p->head_dim;
+    pa.pages_per_row = p->pages_per_row;
+    pa.num_pages = p->num_pages;
+    pa.window = p->window;
+    pa.rope_len = p->rope_len;
+    pa.tile_tokens = tile_tokens;
+    pa.positions = positions;
+    pa.row_of = rows;
+    pa.rope_cos = p->rope_cos;
+    pa.ws = ws;
+    pa.L = L.base;
+    pa.split_grid = split ? grid : 0;
+    pa.units = L.units;
+    cudaError_t e = launch_prefill_plan(pa, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "coded prefill plan launch");
+
+    CodeArgs ca = code_args(p, cache, n_tokens, k_new, v_new, positions, ws);
+    ca.q = q;
+    ca.slots = slots;
+    ca.after_plan = 1;
+    ca.q_row_bytes = 2 * p->head_dim;
+    ca.q_out = reinterpret_cast<uint8_t*>(ws + L.base.q_rot);
+    ca.q_factor = reinterpret_cast<float*>(ws + L.factor);
+    e = launch_code(ca, p->dtype, cache->code, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "coded rope/write launch");
+
+    CodedPrefillArgs aa = {};
+    aa.a.n_tokens = n_tokens;
+    aa.a.heads = p->heads;
+    aa.a.kv_heads = p->kv_heads;
+    aa.a.group = g;
+    aa.a.tile_tokens = tile_tokens;
+    aa.a.head_dim = p->head_dim;
+    aa.a.pages_per_row = p->pages_per_row;
+    aa.a.num_pages = p->num_pages;
+    aa.a.window = p->window;
+    aa.a.positions = positions;
+    aa.a.table = table;
+    aa.a.sinks = p->sinks;
+    aa.a.out = out;
+    aa.a.ws = ws;
+    aa.a.L = L.base;
+    aa.k = static_cast<const uint8_t*>(cache->k);
+    aa.v = static_cast<const uint8_t*>(cache->v);
+    aa.k_scale = cache->k_scale;
+    aa.v_scale = cache->v_scale;
+    aa.q_factor = ca.q_factor;
+    aa.units = split ? L.units : L.base.tiles;
+    aa.slot_rows = L.slot_rows;
+    aa.part_o = reinterpret_cast<float*>(ws + L.part_o);
+    aa.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
+    // a split tile has at least two of the 4 grid / kv_heads pieces
+    const int most = (2 * grid + p->kv_heads - 1) / p->kv_heads;
+    const int merge_tiles = split ? (n_tokens < most ? n_tokens : most) : 0;
+    e = launch_prefill_coded(aa, qm, cache->code, grid, merge_tiles, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "coded prefill attention launch");
+    g_launches = split ? 4 : 3;
     return PDATTN_OK;
 }
 

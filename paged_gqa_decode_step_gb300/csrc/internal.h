@@ -85,6 +85,8 @@ struct PrefillPrepArgs {
     void* v_pool;
     char* ws;
     PfLayout L;
+    int split_grid;         // > 0: also list sub-tiles at `units`, for about two units per CTA of this many
+    size_t units;
 };
 
 struct PrefillArgs {
@@ -137,6 +139,20 @@ struct ReadArgs {
     char* ws;
 };
 
+// Prefill attention over a coded cache (csrc/prefill_coded.cu).
+struct CodedPrefillArgs {
+    PrefillArgs a;
+    const uint8_t* k;       // codes and scales
+    const uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    const float* q_factor;  // [n_tokens, heads]
+    size_t units;           // offset of the tile list the units come from
+    int slot_rows;          // rows of a split piece's partial
+    float* part_o;          // [slot, kv head, slot_rows, D]
+    float2* part_ml;        // [slot, kv head, slot_rows] (maximum, sum)
+};
+
 cudaError_t launch_rope_tables(float theta, int D, int S, int dtype, void* cos_out, void* sin_out,
                                cudaStream_t stream);
 // The split planner (one block, if a.do_plan), then the rope + cache write of
@@ -171,6 +187,12 @@ cudaError_t launch_packed_prep(const PrefillPrepArgs& a, int dtype, cudaStream_t
 cudaError_t launch_packed(const PrefillArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map,
                           const CUtensorMap& v_map, int grid, cudaStream_t stream);
 
+// The tile list alone, with sub-tiles if a.split_grid > 0 (one block).
+cudaError_t launch_prefill_plan(const PrefillPrepArgs& a, cudaStream_t stream);
+// Attention of the units, then (merge_tiles > 0: an upper bound on split
+// tiles) the merge of split tiles.
+cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int code, int grid,
+                                 int merge_tiles, cudaStream_t stream);
 cudaError_t launch_code(const CodeArgs& a, int dtype, int code, cudaStream_t stream);
 cudaError_t launch_read(const ReadArgs& a, int dtype, int code, cudaStream_t stream);
 

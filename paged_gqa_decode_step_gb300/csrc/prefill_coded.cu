@@ -1,0 +1,830 @@
+// Prefill attention over a coded (8-bit) paged cache on the tensor cores.
+//
+// The dataflow is prefill.cu's: a unit is a tile of up to 256 / g tokens of
+// one row times one kv head, in two halves of 128 MMA rows; per block of 128
+// keys S = Q K^T, softmax with one thread per row, P over S's columns in
+// tensor memory, O += P V.  What differs:
+//
+//   * Codes.  Four converter warps read a block's codes straight from the
+//     cache (contiguous pages, one block ahead, in registers) and store
+//     K' = code * r as f16 where the MMA reads it; r = scale / ref in (0, 1]
+//     with ref a power of two.  For K ref is the block's largest scale
+//     rounded up, and the block's scores are multiplied by it; for V it is
+//     the largest so far in the unit, and O is rescaled when it grows (it
+//     then travels with the running maximum's rescale).  r and code * r
+//     round to f16's 11 bits (2^-12 of the value, against 2^-9 for bf16);
+//     values under 2^-14 ref round to a step of 2^-24 ref.  Converting once
+//     per unit and block costs each SM 12 codes per clock at full MMA rate.
+//     Multiplying the scales into S and P instead would put two more
+//     instructions per score into the softmax, which bounds the kernel.
+//   * Types.  Q comes as f16 rows with a factor each (code_kernel), P is f16
+//     kept 2^7 above the usual scale: f16's 11 bits hold all weights above
+//     2^-21 of the largest.
+//   * Long rows in few tiles are split along their keys (the planner's
+//     sub-tiles): a piece writes its unnormalised O, maximum and sum, and a
+//     second kernel merges them.
+//   * A key or value that stands for NaN makes its K' row NaN and its V' row
+//     zero: the weights of exactly the queries that see it become NaN.
+//
+// Warpgroups: 0 = warp 0 takes units and loads Q (TMA), warp 1 issues MMAs;
+// 1 = converters; 2 and 3 = softmax and epilogue of the halves.  Waits are
+// bounded as in prefill.cu.
+#include <climits>
+
+#include "coded.cuh"
+#include "internal.h"
+#include "umma.cuh"
+
+namespace pdattn {
+namespace {
+
+constexpr int kCpThreads = 512;
+constexpr float kRescale = 8.0f;    // lazy rescale threshold (log2 units)
+constexpr float kPBias = 7.0f;      // weights are kept 2^7 up: at most 2^(kRescale + kPBias) = 2^15
+constexpr int kRefs = 8;            // ring of (K ref, V ref) per block; longer than any stage ring
+
+template <int D>
+struct CpCfg {
+    static constexpr int kBoxes = D / 64;                 // 64-element column boxes
+    static constexpr int kQBytes = kBoxes * 16384;        // one half: 128 rows x 128 B per box
+    static constexpr int kKBytes = kBoxes * 16384;        // K' (or V') of a block: 128 keys x 128 B per box
+    static constexpr int kStageBytes = 2 * kKBytes;
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kOffStage = 2 * kQBytes;
+    static constexpr int kSmem = kOffStage + kStages * kStageBytes + 1024;   // + alignment slack
+    static constexpr uint32_t kTmemCols = 512;            // S of half h at 128 h, O at 256 + h D
+    static constexpr uint32_t kColO = 256;
+    static_assert(kStages < kRefs, "a block's refs outlive its stage");
+};
+
+// Registers: the launch gives 512 threads 128 each, which the converters keep;
+// the issuing warpgroup hands 48 to the two softmax warpgroups.
+constexpr uint32_t kRegsIssue = 80, kRegsConvert = 128, kRegsSoftmax = 152;
+static_assert(kRegsIssue + kRegsConvert + 2 * kRegsSoftmax <= 4 * 128, "register hand-over exceeds the launch");
+
+constexpr int kUnitSlots = 4;
+constexpr int kUnitReaders = 13;     // the issuing warp, four converter and eight softmax warps
+
+struct CpBars {
+    uint64_t q_full[2], q_empty[2];
+    uint64_t mma_done;
+    uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t k_ready[4], k_empty[4], v_ready[4], v_empty[4];   // [stage]
+    uint64_t ref_full[kRefs];
+};
+
+struct __align__(32) UnitSlot {
+    PfTile t;
+    int u;
+    int pad[7];
+};
+
+// The next unit from the producer's ring (whole warp) and its tile: -1 once
+// there is no more work, -2 on abort.
+__device__ __forceinline__ int take_unit(CpBars& bars, const UnitSlot* s_unit, uint32_t k, int lane,
+                                         volatile int* abort, Ctrl* ctrl, PfTile& t) {
+    const int slot = k % kUnitSlots;
+    if (!warp_wait(smem_u32(&bars.unit_full[slot]), (k / kUnitSlots) & 1, abort, ctrl)) return -2;
+    const volatile int4* src = reinterpret_cast<const volatile int4*>(&s_unit[slot]);
+    const int4 t0 = make_int4(src[0].x, src[0].y, src[0].z, src[0].w);
+    const int4 t1 = make_int4(src[1].x, src[1].y, src[1].z, src[1].w);
+    const int u = src[2].x;
+    t.t0 = t0.x; t.ntok = t0.y; t.row = t0.z; t.first_page = t0.w;
+    t.npg = t1.x; t.lo_min = t1.y; t.pos_max = t1.z; t.pad = t1.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.unit_empty[slot]));
+    return u;
+}
+
+// ---------------------------------------------------------------------------
+// Converters (four warps): codes of the unit stream's blocks to f16.
+// ---------------------------------------------------------------------------
+// A scale's power of two at or above it, as a biased exponent in [1, 252].
+__device__ __forceinline__ int exp_above(uint32_t bits) {
+    const int e = (int)(bits >> 23) + ((bits & 0x7fffffu) != 0);
+    return min(max(e, 1), 252);
+}
+
+template <int D, typename Code>
+__device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw, int lane, uint32_t st_s, CpBars& bars,
+                                             const UnitSlot* s_unit, uint32_t* s_ratio, volatile float* s_ref,
+                                             volatile int* abort, Ctrl* ctrl) {
+    using C = CpCfg<D>;
+    constexpr int kPieces = D / 16;             // 16-code pieces of a key
+    constexpr int kPer = D / 16;                // pieces per thread of a block's K (or V)
+    const PrefillArgs& a = ca.a;
+    const int Hk = a.kv_heads, tid = cw * 32 + lane;
+    PfTile t;
+    uint32_t k = 0;
+    int bk = -1, npg = 0, kvh = 0;
+    int pid_base = -32, pid_cur = 0, pid_nxt = 0;
+    bool fresh = false;                         // the block starts a unit
+    int y0 = 0, y1 = -1;                        // first rows of the block's pages in the pools; -1: no second page
+    const int* trow = nullptr;
+    auto page_row = [&](int pi) -> int {
+        if (pi - pid_base >= 32) {              // pages are visited in order, 32 ids at a time
+            if (pid_base < 0) pid_cur = lane < npg ? __ldg(trow + lane) : 0;
+            else pid_cur = pid_nxt;
+            pid_base += 32;
+            pid_nxt = pid_base + 32 + lane < npg ? __ldg(trow + pid_base + 32 + lane) : 0;
+        }
+        int page = __shfl_sync(0xffffffffu, pid_cur, pi & 31);
+        if (page < 0 || page >= a.num_pages) {
+            if (lane == 0) set_error(ctrl, kErrBadPage);
+            page = 0;
+        }
+        return (page * Hk + kvh) * kPageSize;
+    };
+    // The next block of the stream; false at its end.
+    auto advance = [&]() -> bool {
+        fresh = false;
+        if (2 * ++bk >= npg) {
+            const int u = take_unit(bars, s_unit, k++, lane, abort, ctrl, t);
+            if (u < 0) return false;
+            kvh = u % Hk;
+            npg = t.npg;
+            trow = a.table + (size_t)t.row * a.pages_per_row + t.first_page;
+            pid_base = -32;
+            bk = 0;
+            fresh = true;
+        }
+        y0 = page_row(2 * bk);
+        y1 = 2 * bk + 1 < npg ? page_row(2 * bk + 1) : -1;
+        return true;
+    };
+    uint4 kr[kPer], vr[kPer];
+    float4 ksc, vsc;
+    auto load = [&](uint4 (&r)[kPer], const uint8_t* pool) {
+        #pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int y = i < kPer / 2 ? y0 : y1;
+            if (y >= 0) r[i] = __ldg(reinterpret_cast<const uint4*>(pool + (size_t)y * D) + (i % (kPer / 2)) * 128 + tid);
+        }
+    };
+    auto load_scales = [&]() {
+        const int y = lane < 16 ? y0 : y1;
+        ksc = vsc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (y >= 0) {
+            ksc = __ldg(reinterpret_cast<const float4*>(ca.k_scale + y) + (lane & 15));
+            vsc = __ldg(reinterpret_cast<const float4*>(ca.v_scale + y) + (lane & 15));
+        }
+    };
+    // Widen, scale and store this thread's pieces of one operand.
+    auto store = [&](const uint4 (&r)[kPer], uint32_t base, bool is_v, bool two) {
+        #pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (i >= kPer / 2 && !two) break;
+            const int idx = i * 128 + tid, key = idx / kPieces, pc = idx % kPieces;
+            const uint32_t rr = s_ratio[key];
+            const uint32_t r2 = is_v ? __byte_perm(rr, rr, 0x3232) : __byte_perm(rr, rr, 0x1010);
+            uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w}, h[8];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // a V row outside the tile's keys may hold any codes, e4m3's NaN among them
+                if (is_v && r2 == 0) w[j] = 0;
+                widen4<Code>(w[j], h[2 * j], h[2 * j + 1]);
+                h[2 * j] = mul_f16x2(h[2 * j], r2);
+                h[2 * j + 1] = mul_f16x2(h[2 * j + 1], r2);
+            }
+            // two 16-byte chunks; at head dim 128 the upper half's lanes store
+            // them in the other order, so that eight lanes fill eight banks
+            const uint32_t row = base + (pc >> 2) * 16384 + key * 128;
+            const int c0 = (pc & 3) * 2, sw = D == 128 ? (pc >> 2) & 1 : 0;
+            const uint32_t at0 = row + (((c0 + sw) ^ (key & 7)) << 4), at1 = row + (((c0 + 1 - sw) ^ (key & 7)) << 4);
+            sts128(at0, sw ? h[4] : h[0], sw ? h[5] : h[1], sw ? h[6] : h[2], sw ? h[7] : h[3]);
+            sts128(at1, sw ? h[0] : h[4], sw ? h[1] : h[5], sw ? h[2] : h[6], sw ? h[3] : h[7]);
+        }
+    };
+    bool more = advance();
+    if (more) {
+        load(kr, ca.k);
+        load(vr, ca.v);
+        load_scales();
+    }
+    int v_exp = 1;                              // biased exponent of the unit's V ref
+    for (uint32_t it = 0; more; ++it) {
+        const int st = it % C::kStages;
+        const uint32_t par = (it / C::kStages) & 1;
+        const bool two = y1 >= 0;
+        // ---- ratios of the block's keys (each warp its own copy)
+        {
+            const int key0 = (t.first_page + 2 * bk) * kPageSize + 4 * lane;
+            const float ks[4] = {ksc.x, ksc.y, ksc.z, ksc.w}, vs[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
+            uint32_t kb[4], vb[4], kmax = 0, vmax = 0;
+            bool bad[4];
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = key0 + e >= t.lo_min && key0 + e <= t.pos_max;
+                kb[e] = in ? __float_as_uint(ks[e]) & 0x7fffffffu : 0u;
+                vb[e] = in ? __float_as_uint(vs[e]) & 0x7fffffffu : 0u;
+                bad[e] = kb[e] >= 0x7e000000u || vb[e] >= 0x7e000000u;   // no scale of a finite key or value
+                if (bad[e]) kb[e] = vb[e] = 0u;
+                kmax = max(kmax, kb[e]);
+                vmax = max(vmax, vb[e]);
+            }
+            kmax = __reduce_max_sync(0xffffffffu, kmax);
+            vmax = __reduce_max_sync(0xffffffffu, vmax);
+            const int k_exp = exp_above(kmax);
+            v_exp = fresh ? exp_above(vmax) : max(v_exp, exp_above(vmax));
+            const float k_down = __uint_as_float((uint32_t)(254 - k_exp) << 23);
+            const float v_down = __uint_as_float((uint32_t)(254 - v_exp) << 23);
+            uint32_t rr[4];
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                rr[e] = pack_f16x2(__uint_as_float(kb[e]) * k_down, __uint_as_float(vb[e]) * v_down);
+                if (bad[e]) rr[e] = 0x7e00u;                              // K ratio NaN, V ratio 0
+            }
+            __syncwarp();                       // the previous block's ratios are no longer read
+            *reinterpret_cast<uint4*>(s_ratio + 4 * lane) = make_uint4(rr[0], rr[1], rr[2], rr[3]);
+            __syncwarp();
+            // (K's stage is free only after the softmax has read the refs of
+            // the block kRefs - kStages before)
+            if (!warp_wait(smem_u32(&bars.k_empty[st]), par ^ 1, abort, ctrl)) return;
+            if (cw == 0 && lane == 0) {
+                s_ref[2 * (it % kRefs)] = __uint_as_float((uint32_t)k_exp << 23);
+                s_ref[2 * (it % kRefs) + 1] = __uint_as_float((uint32_t)v_exp << 23);
+                mbar_arrive(smem_u32(&bars.ref_full[it % kRefs]));
+            }
+        }
+        const uint32_t kb_s = st_s + st * C::kStageBytes;
+        store(kr, kb_s, false, two);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.k_ready[st]));
+        more = advance();
+        if (more) load(kr, ca.k);
+        if (!warp_wait(smem_u32(&bars.v_empty[st]), par ^ 1, abort, ctrl)) return;
+        store(vr, kb_s + C::kKBytes, true, two);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.v_ready[st]));
+        if (more) {
+            load(vr, ca.v);
+            load_scales();
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax and epilogue of one half (128 threads, one MMA row each).
+// ---------------------------------------------------------------------------
+// Max of 32 values as four short independent chains.
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+    float acc[4];
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float* v = reinterpret_cast<const float*>(&s[8 * k]);
+        float x = fmax3(v[0], v[1], v[2]);
+        x = fmax3(x, v[3], v[4]);
+        x = fmax3(x, v[5], v[6]);
+        acc[k] = fmaxf(x, v[7]);
+    }
+    return fmaxf(fmax3(acc[0], acc[1], acc[2]), acc[3]);
+}
+
+__device__ __forceinline__ float sink_scale(float mu, float l, bool has_sink, float sk) {
+    if (!has_sink) return l == 0.f ? 0.f : 1.f / l;
+    const float Mp = fmaxf(mu, sk);
+    const float f = exp2_approx(mu - Mp);
+    return f / (l * f + exp2_approx(sk - Mp));
+}
+
+template <int D>
+__device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int half, int quarter, int lane, uint32_t tmem,
+                                             CpBars& bars, const volatile float* s_ref, const UnitSlot* s_unit,
+                                             volatile int* abort, Ctrl* ctrl) {
+    using C = CpCfg<D>;
+    const PrefillArgs& a = ca.a;
+    const int W = a.window, Hk = a.kv_heads, g = a.group, Tq = a.tile_tokens / 2;
+    const int m = quarter * 32 + lane;                    // MMA row = TMEM lane
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + 128u * half, o_addr = tmem + lane_base + C::kColO + half * D;
+    const int tq = m / g, jh = m % g, tok = half * Tq + tq;
+    const __nv_bfloat16* sinks = static_cast<const __nv_bfloat16*>(a.sinks);
+    const bool out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+    const uint32_t s_full = smem_u32(&bars.s_full[half]), p_full = smem_u32(&bars.p_full[half]);
+    uint32_t it = 0, ch = 0, uh = 0, k = 0;
+    bool ok = true;
+    PfTile t;
+    int u = take_unit(bars, s_unit, k++, lane, abort, ctrl, t);
+    int pos_next = -1;
+    float f_next = 1.f;
+    auto row_inputs = [&](const PfTile& tt, int uu) {
+        pos_next = -1;
+        if (tq < Tq && tok < tt.ntok) {
+            pos_next = __ldg(a.positions + tt.t0 + tok);
+            f_next = __ldg(ca.q_factor + (size_t)(tt.t0 + tok) * a.heads + (uu % Hk) * g + jh);
+        }
+    };
+    if (u >= 0) row_inputs(t, u);
+    while (u >= 0) {
+        const int kvh = u % Hk, nb = (t.npg + 1) / 2;
+        if (half == 1 && t.ntok <= Tq) {
+            it += nb;
+            u = take_unit(bars, s_unit, k++, lane, abort, ctrl, t);
+            if (u >= 0) row_inputs(t, u);
+            continue;
+        }
+        const bool active = tq < Tq && tok < t.ntok;
+        const bool warp_active = __any_sync(0xffffffffu, active);
+        const int pos = active ? max(pos_next, 0) : -1;
+        const int lo = active && W > 0 && pos - W + 1 > 0 ? pos - W + 1 : 0;
+        const float qf = f_next;
+        float m_run = -INFINITY, l = 0.f, v_ref = 1.f;
+        for (int b = 0; b < nb; ++b) {
+            ok = warp_wait(s_full, (ch + b) & 1, abort, ctrl);
+            if (!ok) break;
+            tc_fence_after();
+            if (!warp_active) {                            // none of this warp's rows is a query
+                tc_fence_before();
+                if (lane == 0) mbar_arrive(p_full);
+                continue;
+            }
+            const int ri = (it + b) % kRefs;
+            ok = warp_wait(smem_u32(&bars.ref_full[ri]), ((it + b) / kRefs) & 1, abort, ctrl);
+            if (!ok) break;
+            const float v_new = s_ref[2 * ri + 1];
+            // a factor that underflows keeps -inf times it at -inf
+            const float f = fmaxf(qf * s_ref[2 * ri], kScaleMin);
+            const int pg0 = t.first_page + 2 * b, key0 = pg0 * kPageSize, npb = min(2, t.npg - 2 * b);
+            // keys c of this block visible to the row: c_lo <= c <= c_hi;
+            // 32-column chunks visible to every row of the warp skip the test
+            const int c_lo = lo - key0, c_hi = min(pos - key0, npb * kPageSize - 1);
+            const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 2 * kPageSize - 1);
+            auto mask = [&](uint32_t (&x)[32], int b0) {
+                if (!whole && !__all_sync(0xffffffffu, c_lo <= b0 && c_hi >= b0 + 31)) {
+                    #pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (b0 + c < c_lo || b0 + c > c_hi) x[c] = __float_as_uint(-INFINITY);
+                }
+            };
+            // The first 64 columns stay in registers; the others are read
+            // twice, once for the maximum (a 128-column row and its weights
+            // do not fit beside the converters' share of the registers).
+            uint32_t s0[32], s1[32], x[32];
+            tmem_ld32(s_addr, s0);
+            tmem_ld32(s_addr + 32, s1);
+            tmem_ld32(s_addr + 64, x);
+            tmem_wait_ld();
+            mask(s0, 0);
+            mask(s1, 32);
+            mask(x, 64);
+            float top = fmax3(max32(s0), max32(s1), max32(x));
+            tmem_ld32(s_addr + 96, x);
+            tmem_wait_ld();
+            mask(x, 96);
+            top = fmaxf(top, max32(x));
+            const float mx = top * f;
+            const bool need = mx > m_run + kRescale;
+            float alpha = 1.f;
+            if (need) {
+                alpha = exp2_approx(m_run - mx);
+                m_run = mx;
+                l *= alpha;
+            }
+            if (b > 0) alpha *= v_ref / v_new;             // powers of two: exact
+            v_ref = v_new;
+            if (b > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                #pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_addr + c0, o);
+                    tmem_wait_ld();
+                    #pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                    tmem_st32(o_addr + c0, o);
+                }
+            }
+            const float neg_mu = m_run == -INFINITY ? 0.f : kPBias - m_run;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            // weights of 32 columns over the first 64 columns of S, of which
+            // the registers hold what is still needed
+            auto weights = [&](const uint32_t (&y)[32], int q4) {
+                uint32_t pk[16];
+                #pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    float p0, p1;
+                    ffma2(p0, p1, __uint_as_float(y[c]), __uint_as_float(y[c + 1]), f, neg_mu);
+                    p0 = exp2_approx(p0);
+                    p1 = exp2_approx(p1);
+                    pk[c >> 1] = pack_f16x2(p0, p1);
+                    fadd2(acc[c & 2], acc[(c & 2) + 1], p0, p1);
+                }
+                tmem_st16(s_addr + 16 * q4, pk);
+            };
+            tmem_ld32(s_addr + 64, x);
+            weights(s0, 0);
+            weights(s1, 1);
+            tmem_wait_ld_of(x);
+            mask(x, 64);
+            tmem_ld32(s_addr + 96, s0);
+            weights(x, 2);
+            tmem_wait_ld_of(s0);
+            mask(s0, 96);
+            weights(s0, 3);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        }
+        if (!ok) break;
+        PfTile tn;
+        const int un = take_unit(bars, s_unit, k++, lane, abort, ctrl, tn);
+        if (un >= 0) row_inputs(tn, un);
+        ok = warp_wait(smem_u32(&bars.o_done[half]), uh & 1, abort, ctrl);
+        if (!ok) break;
+        tc_fence_after();
+        if (warp_active) {
+            const int h = kvh * g + jh;
+            const float mu = m_run == -INFINITY ? -1.0e30f : m_run - kPBias;
+            if (t.pad == 0) {
+                const float sk = sinks != nullptr && active ? __bfloat162float(sinks[h]) * 1.4426950408889634f : 0.f;
+                const float inv = sink_scale(mu, l, sinks != nullptr, sk) * v_ref;
+                __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + tok) * a.heads + h) * D;
+                #pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    uint32_t o[64];
+                    tmem_ld32(o_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+                    tmem_ld32(o_addr + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+                    tmem_wait_ld();
+                    if (active) {
+                        #pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            uint32_t w[8];
+                            #pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                w[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]) * inv,
+                                                   __uint_as_float(o[16 * v + 2 * e + 1]) * inv);
+                            __nv_bfloat16* dst = orow + c0 + 16 * v;
+                            if (out_wide) {
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                                             ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                                               "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                             : "memory");
+                            } else {
+                                reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
+                        }
+                    }
+                }
+            } else {
+                // a piece of a split tile: unnormalised O, maximum and sum
+                const size_t at = ((size_t)(t.pad - 1) * Hk + kvh) * ca.slot_rows + tok * g + jh;
+                float* orow = ca.part_o + at * D;
+                if (active) ca.part_ml[at] = make_float2(mu, l);
+                #pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_addr + c0, o);
+                    tmem_wait_ld();
+                    if (active) {
+                        #pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<float4*>(orow + c0 + c) =
+                                make_float4(__uint_as_float(o[c]) * v_ref, __uint_as_float(o[c + 1]) * v_ref,
+                                            __uint_as_float(o[c + 2]) * v_ref, __uint_as_float(o[c + 3]) * v_ref);
+                    }
+                }
+            }
+        }
+        // The next unit's first PV overwrites O only after this read (its
+        // p_full arrival follows in program order).
+        tc_fence_before();
+        ch += nb;
+        it += nb;
+        ++uh;
+        u = un;
+        t = tn;
+    }
+}
+
+template <int D, typename Code>
+__global__ void __launch_bounds__(kCpThreads, 1)
+    prefill_coded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CodedPrefillArgs ca) {
+    using C = CpCfg<D>;
+    const PrefillArgs& a = ca.a;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) CpBars bars;
+    __shared__ __align__(16) uint32_t s_ratio[4][128];
+    __shared__ float s_ref[2 * kRefs];
+    __shared__ UnitSlot s_unit[kUnitSlots];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    const uint32_t q_s = sb, st_s = sb + C::kOffStage;
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
+    volatile int* abort = &s_abort;
+
+    // Rows of the Q tiles that no token fills stay zero.
+    for (int i = tid; i < 2 * C::kQBytes / 16; i += kCpThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) {
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(smem_u32(&bars.k_ready[s]), 4);
+            mbar_init(smem_u32(&bars.k_empty[s]), 1);
+            mbar_init(smem_u32(&bars.v_ready[s]), 4);
+            mbar_init(smem_u32(&bars.v_empty[s]), 1);
+        }
+        for (int r = 0; r < kRefs; ++r) mbar_init(smem_u32(&bars.ref_full[r]), 1);
+        mbar_init(smem_u32(&bars.mma_done), 1);
+        for (int k = 0; k < kUnitSlots; ++k) {
+            mbar_init(smem_u32(&bars.unit_full[k]), 1);
+            mbar_init(smem_u32(&bars.unit_empty[k]), kUnitReaders);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(smem_u32(&bars.q_full[h]), 1);
+            mbar_init(smem_u32(&bars.q_empty[h]), 1);
+            mbar_init(smem_u32(&bars.s_full[h]), 1);
+            mbar_init(smem_u32(&bars.p_full[h]), 4);
+            mbar_init(smem_u32(&bars.o_done[h]), 1);
+        }
+        s_abort = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&q_map);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&s_tmem)), "r"(C::kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_proxy_async_shared();     // zeroed Q rows, before any MMA reads them
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    const int Hk = a.kv_heads, g = a.group, Tq = a.tile_tokens / 2;
+    const int n_units = (ctrl->magic == kPlanMagic ? ctrl->n_items : 0) * Hk;
+    const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + ca.units);
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        softmax_half<D>(ca, (warp - 8) >> 2, warp & 3, lane, tmem, bars, s_ref, s_unit, abort, ctrl);
+    } else if (warp >= 4) {
+        convert_warp<D, Code>(ca, warp - 4, lane, st_s, bars, s_unit, s_ratio[warp - 4], s_ref, abort, ctrl);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+      if (warp == 0) {
+        // ---------------- units and Q (whole warp, one lane issues) ----------------
+        uint32_t uq[2] = {0, 0};     // units whose Q half h was loaded
+        bool ok = true;
+        int u = blockIdx.x;
+        for (uint32_t k = 0; ok; ++k) {
+            if (k > 0) {
+                int v = 0;
+                if (lane == 0) v = (int)gridDim.x + atomicAdd(&ctrl->next_item, 1);
+                u = __shfl_sync(0xffffffffu, v, 0);
+            }
+            const int slot = k % kUnitSlots;
+            PfTile t = {};
+            if (u < n_units) t = tiles[u / Hk];
+            ok = warp_wait(smem_u32(&bars.unit_empty[slot]), ((k / kUnitSlots) & 1) ^ 1, abort, ctrl);
+            if (!ok) break;
+            if (lane == 0) {
+                int4* dst = reinterpret_cast<int4*>(&s_unit[slot]);
+                dst[0] = make_int4(t.t0, t.ntok, t.row, t.first_page);
+                dst[1] = make_int4(t.npg, t.lo_min, t.pos_max, t.pad);
+                dst[2] = make_int4(u < n_units ? u : -1, 0, 0, 0);
+                mbar_arrive(smem_u32(&bars.unit_full[slot]));
+            }
+            __syncwarp();
+            if (u >= n_units) break;
+            const int kvh = u % Hk, nh = uni(t.ntok > Tq ? 2 : 1), t0 = uni(t.t0);
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!ok || h >= nh) break;
+                ok = warp_wait(smem_u32(&bars.q_empty[h]), (uq[h] & 1) ^ 1, abort, ctrl);
+                if (!ok) break;
+                const uint32_t qf = smem_u32(&bars.q_full[h]);
+                elect_arrive_expect_tx(qf, C::kBoxes * 128 * g * Tq);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    elect_tma_3d(q_s + h * C::kQBytes + b * 16384, &q_map, b * 64, kvh * g, t0 + h * Tq, qf);
+                ++uq[h];
+            }
+        }
+        // Drain: every load issued has landed before exit.
+        #pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (uq[h] > 0) mbar_wait(smem_u32(&bars.q_full[h]), (uq[h] - 1) & 1, kPfTimeoutNs);
+      } else if (warp == 1) {
+        // ---------------- MMA issuer (as in prefill.cu) ----------------
+        constexpr uint32_t idesc_s = instr_desc(128, 128, 0, 0, 0);
+        constexpr uint32_t idesc_s64 = instr_desc(128, 64, 0, 0, 0);    // a block of one page
+        constexpr uint32_t idesc_o = instr_desc(128, D, 0, 1, 0);
+        bool issued = false;
+        bool ok = true;
+        const uint64_t dq = smem_desc(q_s, 16, 1024), dk = smem_desc(st_s, 16, 1024);
+        const uint64_t dv = smem_desc(st_s + C::kKBytes, 16384, 1024);
+        auto qk = [&](int h, int s, bool one_page) {
+            const uint32_t idesc = one_page ? idesc_s64 : idesc_s;
+            const uint64_t a0 = dq + (uint64_t)(h * (C::kQBytes >> 4));
+            const uint64_t b0 = dk + (uint64_t)(s * (C::kStageBytes >> 4));
+            #pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                umma_f16kind(tmem + 128u * h, a0 + (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2),
+                             b0 + (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2), idesc, ks > 0 ? 1u : 0u);
+            umma_commit(smem_u32(&bars.s_full[h]));
+        };
+        auto pv = [&](int h, uint32_t j, int s, bool first, bool one_page) -> bool {
+            if (!warp_wait(smem_u32(&bars.p_full[h]), j & 1, abort, ctrl)) return false;
+            tc_fence_after();
+            const uint64_t b0 = dv + (uint64_t)(s * (C::kStageBytes >> 4));
+            #pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                if (ks < 4 || !one_page)
+                    umma_f16kind_ts(tmem + C::kColO + h * D, tmem + 128u * h + ks * 8, b0 + (uint64_t)(ks * 128),
+                                    idesc_o, (first && ks == 0) ? 0u : 1u);
+            return true;
+        };
+        constexpr uint32_t kPend = 1, kPendFirst = 2, kPendLast = 4, kPendOne = 8, kPendB = 16, kEnd = 32;
+        uint32_t it = 0, uq0 = 0, uq1 = 0, cs0 = 0, cs1 = 0, f = 0;   // blocks; units / S per half; flags
+        int nh = 0, npg = 0, bk = 0;                                  // the current unit and block
+        for (uint32_t k = 0; ok;) {
+            if (2 * bk >= npg) {                                      // the unit is done: the next one
+                if (npg > 0) {
+                    ++uq0;
+                    if (nh == 2) ++uq1;
+                }
+                PfTile t;
+                const int u = take_unit(bars, s_unit, k++, lane, abort, ctrl, t);
+                if (u == -2) {
+                    ok = false;
+                    break;
+                }
+                nh = 0;
+                npg = 0;
+                bk = 0;
+                if (u < 0) {
+                    f |= kEnd;
+                } else {
+                    nh = uni(t.ntok > Tq ? 2 : 1);
+                    npg = uni(t.npg);
+                }
+            }
+            const int s = it % C::kStages;
+            const bool one = npg - 2 * bk == 1;
+            #pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if ((f & kPend) && (h == 0 || (f & kPendB))) {
+                    if (h == 0) {
+                        ok = warp_wait(smem_u32(&bars.v_ready[(it - 1) % C::kStages]), ((it - 1) / C::kStages) & 1, abort,
+                                       ctrl);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    ok = pv(h, (h ? cs1 : cs0) - 1, (it - 1) % C::kStages, f & kPendFirst, f & kPendOne);
+                    if (!ok) break;
+                    if (f & kPendLast) umma_commit(smem_u32(&bars.o_done[h]));
+                }
+                if (h < nh) {
+                    if (h == 0) {
+                        ok = warp_wait(smem_u32(&bars.k_ready[s]), (it / C::kStages) & 1, abort, ctrl);
+                        if (!ok) break;
+                    }
+                    if (bk == 0) {
+                        ok = warp_wait(smem_u32(&bars.q_full[h]), (h ? uq1 : uq0) & 1, abort, ctrl);
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+                    issued = true;
+                    qk(h, s, one);
+                }
+            }
+            if (!ok) break;
+            if (f & kPend) umma_commit(smem_u32(&bars.v_empty[(it - 1) % C::kStages]));
+            if (f & kEnd) break;
+            umma_commit(smem_u32(&bars.k_empty[s]));
+            const bool last = 2 * (bk + 1) >= npg;
+            if (last) {
+                umma_commit(smem_u32(&bars.q_empty[0]));
+                if (nh == 2) umma_commit(smem_u32(&bars.q_empty[1]));
+            }
+            f = kPend | (bk == 0 ? kPendFirst : 0) | (last ? kPendLast : 0) | (one ? kPendOne : 0) |
+                (nh == 2 ? kPendB : 0);
+            ++cs0;
+            if (nh == 2) ++cs1;
+            ++it;
+            ++bk;
+        }
+        // Drain: every MMA issued has finished before TMEM is freed.
+        if (issued) {
+            umma_commit(smem_u32(&bars.mma_done));
+            mbar_wait(smem_u32(&bars.mma_done), 0, kPfTimeoutNs);
+        }
+      }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0) {
+        // The last CTA out rewinds the unit cursor.
+        __threadfence();
+        if (atomicAdd(&ctrl->done_ctas, 1) == (int)gridDim.x - 1) {
+            ctrl->next_item = 0;
+            ctrl->done_ctas = 0;
+        }
+    }
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols)
+                     : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merge of split tiles: out = sum_c 2^(mu_c - M) o_c / sum_c 2^(mu_c - M) l_c
+// over a tile's pieces, with the sink's share of the denominator.  Block
+// (tile, kv head, 32 rows); a warp takes four rows, a lane D / 32 dimensions.
+// ---------------------------------------------------------------------------
+constexpr int kMergeRows = 32;
+
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ CodedPrefillArgs ca) {
+    constexpr int N = D / 32;
+    const PrefillArgs& a = ca.a;
+    const Ctrl* ctrl = reinterpret_cast<const Ctrl*>(a.ws + a.L.ctrl);
+    if (ctrl->n_items == 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kvh = blockIdx.y, g = a.group;
+    const __nv_bfloat16* sinks = static_cast<const __nv_bfloat16*>(a.sinks);
+    for (int j = blockIdx.x; j < ctrl->max_items; j += gridDim.x) {   // tiles up to the last split one
+        const PfTile t = reinterpret_cast<const PfTile*>(a.ws + a.L.tiles)[j];
+        const int nch = t.pad & 4095, slot0 = t.pad >> 12;
+        if (nch == 0) continue;
+        const int r1 = min((int)(blockIdx.z + 1) * kMergeRows, t.ntok * g);
+        for (int r = blockIdx.z * kMergeRows + warp; r < r1; r += 8) {
+            const size_t at0 = ((size_t)slot0 * a.kv_heads + kvh) * ca.slot_rows + r;
+            const size_t step = (size_t)a.kv_heads * ca.slot_rows;
+            float M = -1.0e30f, L = 0.f, O[N] = {};
+            #pragma unroll 4
+            for (int c = 0; c < nch; ++c) {
+                const float2 ml = __ldcg(ca.part_ml + at0 + c * step);
+                const float* src = ca.part_o + (at0 + c * step) * D + lane * N;
+                float x[N];
+                if constexpr (N == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                    x[0] = v.x; x[1] = v.y;
+                }
+                const float Mn = fmaxf(M, ml.x);
+                const float fa = exp2_approx(M - Mn), fc = exp2_approx(ml.x - Mn);
+                M = Mn;
+                L = L * fa + fc * ml.y;
+                #pragma unroll
+                for (int e = 0; e < N; ++e) O[e] = O[e] * fa + fc * x[e];
+            }
+            const int h = kvh * g + r % g;
+            const float sk = sinks != nullptr ? __bfloat162float(sinks[h]) * 1.4426950408889634f : 0.f;
+            const float inv = sink_scale(M, L, sinks != nullptr, sk);
+            __nv_bfloat16* dst =
+                static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + r / g) * a.heads + h) * D + lane * N;
+            if constexpr (N == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv),
+                                                            pack_bf16x2(O[2] * inv, O[3] * inv));
+            else
+                *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(O[0] * inv, O[1] * inv);
+        }
+    }
+}
+
+template <int D, typename Code>
+cudaError_t launch_d(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int grid, int merge_tiles,
+                     cudaStream_t stream) {
+    using C = CpCfg<D>;
+    auto kern = prefill_coded_kernel<D, Code>;
+    static int configured_mask = 0;   // bit per device id < 31
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 31 || !(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 31) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
+    }
+    kern<<<grid, kCpThreads, C::kSmem, stream>>>(q_map, ca);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || merge_tiles == 0) return e;
+    const dim3 mg((unsigned)merge_tiles, (unsigned)ca.a.kv_heads, (unsigned)((ca.slot_rows + kMergeRows - 1) / kMergeRows));
+    merge_kernel<D><<<mg, 256, 0, stream>>>(ca);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int code, int grid,
+                                 int merge_tiles, cudaStream_t stream) {
+    if (ca.a.head_dim == 128)
+        return code == 0 ? launch_d<128, E4m3>(ca, q_map, grid, merge_tiles, stream)
+                         : launch_d<128, Int8>(ca, q_map, grid, merge_tiles, stream);
+    return code == 0 ? launch_d<64, E4m3>(ca, q_map, grid, merge_tiles, stream)
+                     : launch_d<64, Int8>(ca, q_map, grid, merge_tiles, stream);
+}
+
+}  // namespace pdattn

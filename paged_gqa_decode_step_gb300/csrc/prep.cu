@@ -721,6 +721,79 @@ __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
     }
 }
 
+// Sub-tiles for a call with few tiles: tiles longer than Cb blocks of two
+// pages are cut along their keys into equal pieces, Cb = total blocks x kv
+// heads / (2 x grid) (about two units per CTA), at least kMinSplitBlocks (a
+// piece pays for its partial and the merge).  A sub-tile's pad is its partial
+// slot + 1 (0: the whole tile); a split tile's pad becomes first slot << 12 |
+// pieces.  Bounds: Cb >= blocks x Hk / (2 grid) makes the pieces of split
+// tiles at most 4 grid / Hk, so slots x Hk stay within 4 grid, and a tile's
+// pieces within 2 grid / Hk + 1.
+constexpr int kMinSplitBlocks = 4;
+
+__device__ void split_tiles(const PrefillPrepArgs& a) {
+    __shared__ int s_warp[32];
+    __shared__ int s_sub[kPrepThreads], s_slot[kPrepThreads];
+    __shared__ unsigned long long s_work;
+    __shared__ int s_last;
+    const int tid = threadIdx.x;
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
+    PfTile* tiles = reinterpret_cast<PfTile*>(a.ws + a.L.tiles);
+    PfTile* sub = reinterpret_cast<PfTile*>(a.ws + a.units);
+    if (tid == 0) { s_work = 0; s_last = 0; }
+    __syncthreads();
+    const int n_tiles = ctrl->n_items;
+    unsigned long long w = 0;
+    for (int j = tid; j < n_tiles; j += blockDim.x) w += (tiles[j].npg + 1) / 2;
+    if (w) atomicAdd(&s_work, w);
+    __syncthreads();
+    const unsigned long long per = 2ull * a.split_grid;
+    const long long Cb = max((long long)((s_work * a.kv_heads + per - 1) / per), (long long)kMinSplitBlocks);
+    int n_sub = 0, n_slot = 0;
+    for (int base = 0; base < n_tiles; base += kPrepThreads) {
+        const int j = base + tid;
+        const int nb = j < n_tiles ? (tiles[j].npg + 1) / 2 : 0;
+        const int nch = (int)((nb + Cb - 1) / Cb);
+        int subs, slots;
+        const int at = block_scan_excl<false>(nch, 0, s_warp, &subs);
+        const int slot = n_slot + block_scan_excl<false>(nch > 1 ? nch : 0, 0, s_warp, &slots);
+        s_sub[tid] = at;
+        s_slot[tid] = slot;
+        if (nch > 1) {
+            tiles[j].pad = slot << 12 | nch;
+            atomicMax(&s_last, j + 1);
+        }
+        __syncthreads();
+        for (int i = tid; i < subs; i += blockDim.x) {
+            int lo = 0, hi = kPrepThreads - 1;              // the last tile that starts at or before i
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (s_sub[mid] <= i) lo = mid;
+                else hi = mid - 1;
+            }
+            // (threads past the last tile all hold `subs`, which no i reaches)
+            const int4* src = reinterpret_cast<const int4*>(tiles + base + lo);
+            int4 d0 = src[0], d1 = src[1];
+            const int pages = d1.x, blocks = (pages + 1) / 2;
+            const int n = (int)((blocks + Cb - 1) / Cb), c = i - s_sub[lo];
+            const int b0 = (int)((long long)c * blocks / n), b1 = (int)((long long)(c + 1) * blocks / n);
+            d0.w += 2 * b0;
+            d1.x = min(2 * (b1 - b0), pages - 2 * b0);
+            d1.w = n > 1 ? s_slot[lo] + c + 1 : 0;
+            int4* dst = reinterpret_cast<int4*>(sub + n_sub + i);
+            dst[0] = d0;
+            dst[1] = d1;
+        }
+        n_sub += subs;
+        n_slot += slots;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        ctrl->n_items = n_sub;
+        ctrl->max_items = s_last;    // tiles up to the last split one
+    }
+}
+
 template <typename T>
 __device__ void rope_write_token(const PrefillPrepArgs& a, int i) {
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
@@ -950,6 +1023,14 @@ __global__ void __launch_bounds__(kPrepThreads) prefill_plan_kernel(const __grid
     build_prefill_plan(a);
 }
 
+// The tile list and its sub-tiles (coded prefill).
+__global__ void __launch_bounds__(kPrepThreads) prefill_split_kernel(const __grid_constant__ PrefillPrepArgs a) {
+    griddep_launch_dependents();
+    build_prefill_plan(a);
+    __syncthreads();
+    split_tiles(a);
+}
+
 // Block i rotates and writes token i.  The last block waits for the planner
 // before it exits, so that the completion of this grid (all the attention
 // kernel waits for) also covers the tile list; the other blocks do not wait,
@@ -1034,6 +1115,12 @@ cudaError_t launch_prefill_prep(const PrefillPrepArgs& a, int dtype, cudaStream_
     cfg.numAttrs = 1;
     if (dtype == 0) return cudaLaunchKernelEx(&cfg, prefill_rope_kernel<__nv_bfloat16>, a);
     return cudaLaunchKernelEx(&cfg, prefill_rope_kernel<float>, a);
+}
+
+cudaError_t launch_prefill_plan(const PrefillPrepArgs& a, cudaStream_t stream) {
+    if (a.split_grid > 0) prefill_split_kernel<<<1, kPrepThreads, 0, stream>>>(a);
+    else prefill_plan_kernel<<<1, kPrepThreads, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_packed_prep(const PrefillPrepArgs& a, int dtype, cudaStream_t stream) {
