@@ -107,14 +107,20 @@ __device__ __forceinline__ int exp_above(uint32_t bits) {
 }
 
 template <int D, typename Code>
-__device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw, int lane, uint32_t st_s, CpBars& bars,
+__device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw, int lane, uint8_t* stages, CpBars& bars,
                                              const UnitSlot* s_unit, uint32_t* s_ratio, volatile float* s_ref,
                                              volatile int* abort, Ctrl* ctrl) {
     using C = CpCfg<D>;
-    constexpr int kPieces = D / 16;             // 16-code pieces of a key
-    constexpr int kPer = D / 16;                // pieces per thread of a block's K (or V)
+    // A thread takes 16 codes of four keys (32 j + 8 cw + lane / 4, j = 0..3)
+    // from each 64-column box: eight lanes then store the even 16-byte chunks
+    // of one key and the odd ones of the next, which fill the eight bank
+    // groups, and every address is a constant away from two bases.
+    constexpr int kKeys = 4, kPer = kKeys * C::kBoxes;
     const PrefillArgs& a = ca.a;
-    const int Hk = a.kv_heads, tid = cw * 32 + lane;
+    const int Hk = a.kv_heads, kx = lane >> 2;
+    const size_t src_off = (size_t)(cw * 8 + kx) * D + (lane & 3) * 16;
+    const int dst0 = cw * 1024 + kx * 128 + (((2 * (lane & 3)) ^ kx) << 4);
+    const int dst1 = cw * 1024 + kx * 128 + (((2 * (lane & 3) + 1) ^ kx) << 4);
     PfTile t;
     uint32_t k = 0;
     int bk = -1, npg = 0, kvh = 0;
@@ -155,11 +161,14 @@ __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw,
     };
     uint4 kr[kPer], vr[kPer];
     float4 ksc, vsc;
+    // (index: key j, box)
     auto load = [&](uint4 (&r)[kPer], const uint8_t* pool) {
         #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int y = i < kPer / 2 ? y0 : y1;
-            if (y >= 0) r[i] = __ldg(reinterpret_cast<const uint4*>(pool + (size_t)y * D) + (i % (kPer / 2)) * 128 + tid);
+            const int j = i / C::kBoxes, y = j < kKeys / 2 ? y0 : y1;
+            if (y >= 0)
+                r[i] = __ldg(reinterpret_cast<const uint4*>(pool + (size_t)y * D + src_off + (j & 1) * 32 * D +
+                                                            (i % C::kBoxes) * 64));
         }
     };
     auto load_scales = [&]() {
@@ -170,52 +179,49 @@ __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw,
             vsc = __ldg(reinterpret_cast<const float4*>(ca.v_scale + y) + (lane & 15));
         }
     };
-    // Widen, scale and store this thread's pieces of one operand.
-    auto store = [&](const uint4 (&r)[kPer], uint32_t base, bool is_v, bool two) {
+    // Widen, scale and store this thread's codes of one operand; r2: the
+    // ratio of each of its keys, twice.
+    auto store = [&](const uint4 (&r)[kPer], uint8_t* base, const uint32_t (&r2)[kKeys], bool two) {
         #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            if (i >= kPer / 2 && !two) break;
-            const int idx = i * 128 + tid, key = idx / kPieces, pc = idx % kPieces;
-            const uint32_t rr = s_ratio[key];
-            const uint32_t r2 = is_v ? __byte_perm(rr, rr, 0x3232) : __byte_perm(rr, rr, 0x1010);
-            uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w}, h[8];
+            const int j = i / C::kBoxes;
+            if (j >= kKeys / 2 && !two) break;
+            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+            uint32_t h[8];
             #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // a V row outside the tile's keys may hold any codes, e4m3's NaN among them
-                if (is_v && r2 == 0) w[j] = 0;
-                widen4<Code>(w[j], h[2 * j], h[2 * j + 1]);
-                h[2 * j] = mul_f16x2(h[2 * j], r2);
-                h[2 * j + 1] = mul_f16x2(h[2 * j + 1], r2);
+            for (int e = 0; e < 4; ++e) {
+                widen4<Code>(w[e], h[2 * e], h[2 * e + 1]);
+                h[2 * e] = mul_f16x2(h[2 * e], r2[j]);
+                h[2 * e + 1] = mul_f16x2(h[2 * e + 1], r2[j]);
             }
-            // two 16-byte chunks; at head dim 128 the upper half's lanes store
-            // them in the other order, so that eight lanes fill eight banks
-            const uint32_t row = base + (pc >> 2) * 16384 + key * 128;
-            const int c0 = (pc & 3) * 2, sw = D == 128 ? (pc >> 2) & 1 : 0;
-            const uint32_t at0 = row + (((c0 + sw) ^ (key & 7)) << 4), at1 = row + (((c0 + 1 - sw) ^ (key & 7)) << 4);
-            sts128(at0, sw ? h[4] : h[0], sw ? h[5] : h[1], sw ? h[6] : h[2], sw ? h[7] : h[3]);
-            sts128(at1, sw ? h[0] : h[4], sw ? h[1] : h[5], sw ? h[2] : h[6], sw ? h[3] : h[7]);
+            uint8_t* to = base + (i % C::kBoxes) * 16384 + j * 4096;
+            *reinterpret_cast<uint4*>(to + dst0) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to + dst1) = make_uint4(h[4], h[5], h[6], h[7]);
         }
     };
     bool more = advance();
     if (more) {
+        load_scales();
         load(kr, ca.k);
         load(vr, ca.v);
-        load_scales();
     }
     int v_exp = 1;                              // biased exponent of the unit's V ref
     for (uint32_t it = 0; more; ++it) {
         const int st = it % C::kStages;
         const uint32_t par = (it / C::kStages) & 1;
         const bool two = y1 >= 0;
+        uint32_t rk[kKeys], rv[kKeys];
+        bool all_in;                            // every key of the block is one of the tile's
         // ---- ratios of the block's keys (each warp its own copy)
         {
             const int key0 = (t.first_page + 2 * bk) * kPageSize + 4 * lane;
             const float ks[4] = {ksc.x, ksc.y, ksc.z, ksc.w}, vs[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
             uint32_t kb[4], vb[4], kmax = 0, vmax = 0;
-            bool bad[4];
+            bool bad[4], in_range = true;
             #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool in = key0 + e >= t.lo_min && key0 + e <= t.pos_max;
+                in_range = in_range && in;
                 kb[e] = in ? __float_as_uint(ks[e]) & 0x7fffffffu : 0u;
                 vb[e] = in ? __float_as_uint(vs[e]) & 0x7fffffffu : 0u;
                 bad[e] = kb[e] >= 0x7e000000u || vb[e] >= 0x7e000000u;   // no scale of a finite key or value
@@ -238,6 +244,13 @@ __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw,
             __syncwarp();                       // the previous block's ratios are no longer read
             *reinterpret_cast<uint4*>(s_ratio + 4 * lane) = make_uint4(rr[0], rr[1], rr[2], rr[3]);
             __syncwarp();
+            #pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+                const uint32_t r = s_ratio[32 * j + cw * 8 + kx];
+                rk[j] = __byte_perm(r, r, 0x1010);
+                rv[j] = __byte_perm(r, r, 0x3232);
+            }
+            all_in = __all_sync(0xffffffffu, in_range);
             // (K's stage is free only after the softmax has read the refs of
             // the block kRefs - kStages before)
             if (!warp_wait(smem_u32(&bars.k_empty[st]), par ^ 1, abort, ctrl)) return;
@@ -247,22 +260,28 @@ __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw,
                 mbar_arrive(smem_u32(&bars.ref_full[it % kRefs]));
             }
         }
-        const uint32_t kb_s = st_s + st * C::kStageBytes;
-        store(kr, kb_s, false, two);
+        uint8_t* to = stages + st * C::kStageBytes;
+        store(kr, to, rk, two);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.k_ready[st]));
         more = advance();
-        if (more) load(kr, ca.k);
+        if (more) {
+            load_scales();
+            load(kr, ca.k);
+        }
+        if (!all_in) {
+            // a V row outside the tile's keys (ratio 0) may hold any codes, e4m3's NaN among them
+            #pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (rv[i / C::kBoxes] == 0) vr[i] = make_uint4(0, 0, 0, 0);
+        }
         if (!warp_wait(smem_u32(&bars.v_empty[st]), par ^ 1, abort, ctrl)) return;
-        store(vr, kb_s + C::kKBytes, true, two);
+        store(vr, to + C::kKBytes, rv, two);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.v_ready[st]));
-        if (more) {
-            load(vr, ca.v);
-            load_scales();
-        }
+        if (more) load(vr, ca.v);
     }
 }
 
@@ -566,7 +585,7 @@ __global__ void __launch_bounds__(kCpThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         softmax_half<D>(ca, (warp - 8) >> 2, warp & 3, lane, tmem, bars, s_ref, s_unit, abort, ctrl);
     } else if (warp >= 4) {
-        convert_warp<D, Code>(ca, warp - 4, lane, st_s, bars, s_unit, s_ratio[warp - 4], s_ref, abort, ctrl);
+        convert_warp<D, Code>(ca, warp - 4, lane, sm + C::kOffStage, bars, s_unit, s_ratio[warp - 4], s_ref, abort, ctrl);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
       if (warp == 0) {
