@@ -913,7 +913,6 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
     ca.table = table;
     ca.after_plan = 1;
     ca.q_row_bytes = coded_q_row(p);
-    ca.q_split = p->dtype == PDATTN_F32;
     ca.q_out = reinterpret_cast<uint8_t*>(ws + L.q_rot);
     e = launch_code(ca, p->dtype, cache->code, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded rope/write launch");

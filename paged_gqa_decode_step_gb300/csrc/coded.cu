@@ -2,9 +2,9 @@
 //
 // The write rotates keys as rope_write_kernel does (Llama example page,
 // "src/rope.linnet": separate f32 products and one f32 add) but codes the f32
-// value itself, with no rounding to T in between.  A group of D / 8 lanes
-// holds one head vector (4 elements of each half per lane, so a lane has
-// both elements of every pair it rotates), finds max|x| with shuffles and
+// value itself, with no rounding to T in between.  A group of D / 16 lanes
+// holds one head vector (8 elements of each half per lane, so a lane has both
+// elements of every pair it rotates), finds max|x| with shuffles and
 // divides by the scale (IEEE division: the codes are those of the formula in
 // coded.cuh, bit for bit).
 //
@@ -24,133 +24,163 @@ namespace pdattn {
 
 constexpr int kCodeThreads = 256;
 
+// Eight consecutive elements as f32.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&f)[4]);
+__device__ __forceinline__ void load8(const T* p, float (&f)[8]);
 template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[4]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
 }
 template <>
-__device__ __forceinline__ void load4<float>(const float* p, float (&f)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+__device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
+    #pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p) + k);
+        f[4 * k] = v.x; f[4 * k + 1] = v.y; f[4 * k + 2] = v.z; f[4 * k + 3] = v.w;
+    }
 }
 
-// One head vector per group of D / 8 lanes: vector v of token v / per, where
-// a token has `heads` query vectors (attention calls only), then its key and
-// its value vectors.
+// x / s rounded to nearest, for many x of one s: with r = RN(1 / s) and
+// q0 = RN(x r), the remainder x - s q0 is exact in one FMA and q0 + r * rem
+// rounds to the quotient (Markstein, IBM J. Res. Dev. 34, 1990).  Needs
+// quotient, remainder and s clear of the ends of the exponent range; a vector
+// whose largest magnitude lies outside [2^-60, 2^60] divides directly.  (The
+// remainder of a quotient below 2^-11 may then still be inexact; such a
+// quotient is under half of any code's smallest step.)
+struct Divider {
+    float s, r;
+    bool direct;
+    __device__ __forceinline__ Divider(float scale, uint32_t top) {
+        s = scale;
+        r = __fdiv_rn(1.f, scale);
+        direct = top < (uint32_t)(127 - 60) << 23 || top > (uint32_t)(127 + 60) << 23;
+    }
+    __device__ void apply(float (&x)[8]) const {
+        if (direct) {
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __fdiv_rn(x[k], s);
+        } else {
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float q0 = __fmul_rn(x[k], r);
+                x[k] = __fmaf_rn(__fmaf_rn(-s, q0, x[k]), r, q0);
+            }
+        }
+    }
+};
+
+// Block = one token; its vectors (`heads` queries in attention calls, then
+// keys, then values) are dealt to groups of D / 16 lanes, so that every lane
+// moves 16 bytes of bf16 at a time and position, slot and table rows are
+// found once per block.
 template <typename T, int D, typename Code>
 __global__ void __launch_bounds__(kCodeThreads) code_kernel(const __grid_constant__ CodeArgs a) {
     griddep_launch_dependents();
-    constexpr int kLanes = D / 8, kHalf = D / 2;
+    constexpr int kLanes = D / 16, kHalf = D / 2;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws);
-    const int Hk = a.kv_heads, Hq = a.q ? a.heads : 0, per = Hq + 2 * Hk;
-    const long long v = (long long)blockIdx.x * (kCodeThreads / kLanes) + threadIdx.x / kLanes;
-    const int lane = threadIdx.x % kLanes, e0 = 4 * lane;
-    if (v < (long long)a.n_tokens * per) {
-        const int i = (int)(v / per), j = (int)(v - (long long)i * per);
+    const int Hk = a.kv_heads, Hq = a.q ? a.heads : 0, per = Hq + 2 * Hk, i = blockIdx.x;
+    const int lane = threadIdx.x % kLanes, e0 = 8 * lane;
+    const int pos = __ldg(a.positions + i);
+    // a token's position must lie in the rope table, and for the attention
+    // calls in the page table
+    const bool pos_ok = pos >= 0 && (!a.rope_cos || pos < a.rope_len) && (!a.q || pos < a.pages_per_row * kPageSize);
+    int slot = -1;
+    if (pos_ok) {
+        if (a.slots) {
+            slot = __ldg(a.slots + i);
+        } else {
+            const int page = __ldg(a.table + (size_t)i * a.pages_per_row + pos / kPageSize);
+            slot = page >= 0 && page < a.num_pages ? page * kPageSize + pos % kPageSize : -1;
+        }
+    }
+    const bool slot_ok = slot >= 0 && slot / kPageSize < a.num_pages;
+    if (threadIdx.x == 0) {
+        if (!pos_ok) set_error(ctrl, kErrBadPos);
+        else if (!slot_ok) set_error(ctrl, kErrBadPage);
+    }
+    const int end = !pos_ok ? 0 : slot_ok ? per : Hq;
+    for (int j = threadIdx.x / kLanes; j < end; j += blockDim.x / kLanes) {
         const bool is_q = j < Hq, is_v = j >= Hq + Hk;
         const int h = is_q ? j : (is_v ? j - Hq - Hk : j - Hq);
-        const int pos = __ldg(a.positions + i);
-        // a token's position must lie in the rope table, and for the
-        // attention calls in the page table
-        const bool pos_ok = pos >= 0 && (!a.rope_cos || pos < a.rope_len) && (!a.q || pos < a.pages_per_row * kPageSize);
-        int slot = -1;
-        if (pos_ok && !is_q) {
-            if (a.slots) {
-                slot = __ldg(a.slots + i);
-            } else {
-                const int page = __ldg(a.table + (size_t)i * a.pages_per_row + pos / kPageSize);
-                slot = page >= 0 && page < a.num_pages ? page * kPageSize + pos % kPageSize : -1;
+        const T* src = static_cast<const T*>(is_q ? a.q : (is_v ? a.v_new : a.k_new)) +
+                       ((size_t)i * (is_q ? Hq : Hk) + h) * D;
+        float lo[8], hi[8];
+        load8<T>(src + e0, lo);
+        load8<T>(src + kHalf + e0, hi);
+        if (a.rope_cos && !is_v) {
+            const T* cr = static_cast<const T*>(a.rope_cos) + (size_t)pos * D;
+            const T* sr = static_cast<const T*>(a.rope_sin) + (size_t)pos * D;
+            float cl[8], ch[8], sl[8], sh[8];
+            load8<T>(cr + e0, cl);
+            load8<T>(cr + kHalf + e0, ch);
+            load8<T>(sr + e0, sl);
+            load8<T>(sr + kHalf + e0, sh);
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float x = lo[k], y = hi[k];
+                lo[k] = __fsub_rn(__fmul_rn(x, cl[k]), __fmul_rn(y, sl[k]));
+                hi[k] = __fadd_rn(__fmul_rn(y, ch[k]), __fmul_rn(x, sh[k]));
             }
         }
-        const bool slot_ok = slot >= 0 && slot / kPageSize < a.num_pages;
-        if (lane == 0) {
-            if (!pos_ok) set_error(ctrl, kErrBadPos);
-            else if (!is_q && !slot_ok) set_error(ctrl, kErrBadPage);
-        }
-        if (pos_ok && (is_q || slot_ok)) {
-            const T* src = static_cast<const T*>(is_q ? a.q : (is_v ? a.v_new : a.k_new)) +
-                           ((size_t)i * (is_q ? Hq : Hk) + h) * D;
-            float lo[4], hi[4];
-            load4<T>(src + e0, lo);
-            load4<T>(src + kHalf + e0, hi);
-            if (a.rope_cos && !is_v) {
-                const T* cr = static_cast<const T*>(a.rope_cos) + (size_t)pos * D;
-                const T* sr = static_cast<const T*>(a.rope_sin) + (size_t)pos * D;
-                float cl[4], ch[4], sl[4], sh[4];
-                load4<T>(cr + e0, cl);
-                load4<T>(cr + kHalf + e0, ch);
-                load4<T>(sr + e0, sl);
-                load4<T>(sr + kHalf + e0, sh);
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = lo[k], y = hi[k];
-                    lo[k] = __fsub_rn(__fmul_rn(x, cl[k]), __fmul_rn(y, sl[k]));
-                    hi[k] = __fadd_rn(__fmul_rn(y, ch[k]), __fmul_rn(x, sh[k]));
-                }
+        // the largest magnitude as its bits (they order like the value), so
+        // that an infinity or a NaN anywhere shows in the result
+        uint32_t top = 0;
+        #pragma unroll
+        for (int k = 0; k < 8; ++k)
+            top = max(top, max(__float_as_uint(lo[k]) & 0x7fffffffu, __float_as_uint(hi[k]) & 0x7fffffffu));
+        const uint32_t group = ((1u << kLanes) - 1) << ((threadIdx.x & 31) / kLanes * kLanes);
+        #pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(group, top, d));
+        const bool finite = top < 0x7f800000u;
+        if (is_q) {
+            // 2^-e scales the largest element into [1, 2)
+            const int ex = min(max((int)(top >> 23), 1), 253);      // biased exponent
+            const float down = finite ? __uint_as_float((uint32_t)(254 - ex) << 23) : __uint_as_float(0x7fc00000u);
+            const float factor = (finite ? __uint_as_float((uint32_t)ex << 23) : 1.f) * a.scale_log2;
+            uint8_t* row = a.q_out + ((size_t)i * Hq + h) * a.q_row_bytes;
+            uint32_t w[8], r[8];
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float x0 = (k < 4 ? lo : hi)[2 * (k & 3)] * down, x1 = (k < 4 ? lo : hi)[2 * (k & 3) + 1] * down;
+                w[k] = pack_f16x2(x0, x1);
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                r[k] = pack_f16x2(x0 - back.x, x1 - back.y);
             }
-            // the largest magnitude as its bits (they order like the value),
-            // so that an infinity or a NaN anywhere shows in the result
-            uint32_t top = 0;
-            #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                top = max(top, max(__float_as_uint(lo[k]) & 0x7fffffffu, __float_as_uint(hi[k]) & 0x7fffffffu));
-            const uint32_t group = kLanes == 32 ? 0xffffffffu
-                                                : ((1u << kLanes) - 1) << ((threadIdx.x & 31) / kLanes * kLanes);
-            #pragma unroll
-            for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(group, top, d));
-            const bool finite = top < 0x7f800000u;
-            if (is_q) {
-                // 2^-e scales the largest element into [1, 2)
-                const int ex = min(max((int)(top >> 23), 1), 253);      // biased exponent
-                const float down = finite ? __uint_as_float((uint32_t)(254 - ex) << 23) : __uint_as_float(0x7fc00000u);
-                const float factor = (finite ? __uint_as_float((uint32_t)ex << 23) : 1.f) * a.scale_log2;
-                uint8_t* row = a.q_out + ((size_t)i * Hq + h) * a.q_row_bytes;
-                uint32_t w[4], r[4];
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float* x = k < 2 ? lo : hi;
-                    const int o = 2 * (k & 1);
-                    const float x0 = x[o] * down, x1 = x[o + 1] * down;
-                    w[k] = pack_f16x2(x0, x1);
-                    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                    r[k] = pack_f16x2(x0 - back.x, x1 - back.y);
-                }
-                *reinterpret_cast<uint2*>(row + e0 * 2) = make_uint2(w[0], w[1]);
-                *reinterpret_cast<uint2*>(row + (kHalf + e0) * 2) = make_uint2(w[2], w[3]);
-                if (a.q_split) {
-                    *reinterpret_cast<uint2*>(row + 2 * D + e0 * 2) = make_uint2(r[0], r[1]);
-                    *reinterpret_cast<uint2*>(row + 2 * D + (kHalf + e0) * 2) = make_uint2(r[2], r[3]);
-                }
-                if (lane == 0) {
-                    if (a.q_factor) a.q_factor[(size_t)i * Hq + h] = factor;
-                    else *reinterpret_cast<float*>(row + (a.q_split ? 4 : 2) * D) = factor;
-                }
+            *reinterpret_cast<uint4*>(row + e0 * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(row + (kHalf + e0) * 2) = make_uint4(w[4], w[5], w[6], w[7]);
+            if (sizeof(T) == 4) {     // f32: the second row (see attend_kernel.cuh)
+                *reinterpret_cast<uint4*>(row + 2 * D + e0 * 2) = make_uint4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<uint4*>(row + 2 * D + (kHalf + e0) * 2) = make_uint4(r[4], r[5], r[6], r[7]);
+            }
+            if (lane == 0) {
+                if (a.q_factor) a.q_factor[(size_t)i * Hq + h] = factor;
+                else *reinterpret_cast<float*>(row + (int)sizeof(T) * D) = factor;
+            }
+        } else {
+            // a vector that holds an infinity or a NaN stands for NaN throughout
+            float scale = fmaxf(__fdiv_rn(__uint_as_float(top), Code::kQMax), kScaleMin);
+            if (finite) {
+                const Divider by(scale, top);
+                by.apply(lo);
+                by.apply(hi);
             } else {
-                // a vector that holds an infinity or a NaN stands for NaN throughout
-                const float scale = finite ? fmaxf(__fdiv_rn(__uint_as_float(top), Code::kQMax), kScaleMin)
-                                           : __uint_as_float(0x7fc00000u);
-                if (!finite) {
-                    #pragma unroll
-                    for (int k = 0; k < 4; ++k) lo[k] = hi[k] = 0.f;
-                }
-                const float by = finite ? scale : 1.f;
+                scale = __uint_as_float(0x7fc00000u);
                 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    lo[k] = __fdiv_rn(lo[k], by);
-                    hi[k] = __fdiv_rn(hi[k], by);
-                }
-                const size_t at = ((size_t)(slot / kPageSize) * Hk + h) * kPageSize + slot % kPageSize;
-                uint8_t* dst = (is_v ? a.v : a.k) + at * D;
-                *reinterpret_cast<uint32_t*>(dst + e0) = encode4<Code>(lo[0], lo[1], lo[2], lo[3]);
-                *reinterpret_cast<uint32_t*>(dst + kHalf + e0) = encode4<Code>(hi[0], hi[1], hi[2], hi[3]);
-                if (lane == 0) (is_v ? a.v_scale : a.k_scale)[at] = scale;
+                for (int k = 0; k < 8; ++k) lo[k] = hi[k] = 0.f;
             }
+            const size_t at = ((size_t)(slot / kPageSize) * Hk + h) * kPageSize + slot % kPageSize;
+            uint8_t* dst = (is_v ? a.v : a.k) + at * D;
+            *reinterpret_cast<uint2*>(dst + e0) = make_uint2(encode4<Code>(lo[0], lo[1], lo[2], lo[3]),
+                                                             encode4<Code>(lo[4], lo[5], lo[6], lo[7]));
+            *reinterpret_cast<uint2*>(dst + kHalf + e0) = make_uint2(encode4<Code>(hi[0], hi[1], hi[2], hi[3]),
+                                                                     encode4<Code>(hi[4], hi[5], hi[6], hi[7]));
+            if (lane == 0) (is_v ? a.v_scale : a.k_scale)[at] = scale;
         }
     }
     // With a planner launched before it, the last block exits only after the
@@ -222,11 +252,11 @@ static cudaError_t by_types(int dtype, int D, int code, F f) {
 }
 
 cudaError_t launch_code(const CodeArgs& a, int dtype, int code, cudaStream_t stream) {
-    const long long vectors = (long long)a.n_tokens * ((a.q ? a.heads : 0) + 2 * a.kv_heads);
-    const long long lanes = vectors * (a.head_dim / 8);
+    // as many lanes as the token's vectors can use, in whole warps
+    const long long lanes = (long long)((a.q ? a.heads : 0) + 2 * a.kv_heads) * (a.head_dim / 16);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((lanes + kCodeThreads - 1) / kCodeThreads));
-    cfg.blockDim = dim3(kCodeThreads);
+    cfg.gridDim = dim3((unsigned)a.n_tokens);
+    cfg.blockDim = dim3((unsigned)(lanes >= kCodeThreads ? kCodeThreads : (lanes + 31) / 32 * 32));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

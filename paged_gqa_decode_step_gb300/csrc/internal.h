@@ -102,13 +102,13 @@ struct PrefillArgs {
 };
 
 // Rotation, coding and cache write of n tokens (csrc/coded.cu).  With q the
-// queries are rotated too, as f16 rows of q_row_bytes: D elements, with
-// q_split D more that hold what the first round off, and the row's factor
-// (after them, or in q_factor).
+// queries are rotated too, as f16 rows of q_row_bytes: D elements, for f32
+// D more that hold what the first round off, and the row's factor (after
+// them, or in q_factor).
 struct CodeArgs {
     int n_tokens, heads, kv_heads, head_dim, pages_per_row, num_pages, rope_len;
     int after_plan;         // 1: a programmatic dependent of a planner launch
-    int q_row_bytes, q_split;
+    int q_row_bytes;
     float scale_log2;
     const void* q;          // nullptr: keys and values only
     const void* k_new;

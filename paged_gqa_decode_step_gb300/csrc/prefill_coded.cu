@@ -23,12 +23,17 @@
 //   * Long rows in few tiles are split along their keys (the planner's
 //     sub-tiles): a piece writes its unnormalised O, maximum and sum, and a
 //     second kernel merges them.
+//   * A tile that fits one half (up to 128 / g tokens: drafted tokens, the
+//     end of a prompt) alternates: both halves hold its queries, half A takes
+//     the even blocks and half B the odd ones, so that one softmax still runs
+//     under the other half's MMAs; half A's epilogue merges the two sums.
 //   * A key or value that stands for NaN makes its K' row NaN and its V' row
 //     zero: the weights of exactly the queries that see it become NaN.
 //
-// Warpgroups: 0 = warp 0 takes units and loads Q (TMA), warp 1 issues MMAs;
-// 1 = converters; 2 and 3 = softmax and epilogue of the halves.  Waits are
-// bounded as in prefill.cu.
+// Warps: 0 takes units (with their page ids, some blocks ahead), 1 issues
+// MMAs, 2 loads Q (TMA), 3 describes the blocks (pages, refs, ratios) a few
+// ahead of their use; 4 to 7 convert; 8 to 11 and 12 to 15 are the softmax and
+// epilogue of the halves.  Waits are bounded as in prefill.cu.
 #include <climits>
 
 #include "coded.cuh"
@@ -41,7 +46,7 @@ namespace {
 constexpr int kCpThreads = 512;
 constexpr float kRescale = 8.0f;    // lazy rescale threshold (log2 units)
 constexpr float kPBias = 7.0f;      // weights are kept 2^7 up: at most 2^(kRescale + kPBias) = 2^15
-constexpr int kRefs = 8;            // ring of (K ref, V ref) per block; longer than any stage ring
+constexpr int kDescs = 8;           // ring of block descriptors, longer than any stage ring
 
 template <int D>
 struct CpCfg {
@@ -54,51 +59,80 @@ struct CpCfg {
     static constexpr int kSmem = kOffStage + kStages * kStageBytes + 1024;   // + alignment slack
     static constexpr uint32_t kTmemCols = 512;            // S of half h at 128 h, O at 256 + h D
     static constexpr uint32_t kColO = 256;
-    static_assert(kStages < kRefs, "a block's refs outlive its stage");
+    static_assert(kStages < kDescs, "a block's descriptor outlives its stage");
 };
 
-// Registers: the launch gives 512 threads 128 each, which the converters keep;
-// the issuing warpgroup hands 48 to the two softmax warpgroups.
-constexpr uint32_t kRegsIssue = 80, kRegsConvert = 128, kRegsSoftmax = 152;
-static_assert(kRegsIssue + kRegsConvert + 2 * kRegsSoftmax <= 4 * 128, "register hand-over exceeds the launch");
-
 constexpr int kUnitSlots = 4;
-constexpr int kUnitReaders = 13;     // the issuing warp, four converter and eight softmax warps
+constexpr int kUnitReaders = 11;     // the issuing, the Q and the block warp, and eight softmax warps
+constexpr int kBlocksAhead = 6;      // blocks queued before the next unit is taken: short units queue up, long ones
+                                     // do not hold back work that other CTAs could take
+
+// warp_wait with its polling loop out of line: some thirty waits with the loop
+// in place would crowd the instruction cache.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, Ctrl* ctrl) {
+    return warp_wait(bar, parity, abort, ctrl);
+}
+
+__device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, volatile int* abort, Ctrl* ctrl) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return wait_slow(bar, parity, abort, ctrl);
+}
 
 struct CpBars {
+    uint64_t alt_full, alt_free;     // alternating units: half B's sums written / half A has merged them
     uint64_t q_full[2], q_empty[2];
     uint64_t mma_done;
     uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t k_ready[4], k_empty[4], v_ready[4], v_empty[4];   // [stage]
-    uint64_t ref_full[kRefs];
+    uint64_t desc_full[kDescs], desc_empty[kDescs];
 };
 
 struct __align__(32) UnitSlot {
     PfTile t;
     int u;
     int pad[7];
+    int pids[32];                    // the unit's first page ids
 };
+
+// A block of 128 keys: the first rows of its two pages in the pools (y1 -1: one
+// page; y0 -1: the end of the work), whether the tile sees every key, the refs
+// and per key the K ratio (low half) and the V ratio.
+struct __align__(16) BlockDesc {
+    int y0, y1, all_in, pad;
+    float k_ref, v_ref, pad2[2];
+    uint32_t ratio[128];
+};
+
+// Half B's (maximum, sum, V ref) of an alternating unit, by row.
+struct AltSums {
+    float mu[128], l[128], v_ref[128];
+};
+
+// Blocks and halves of a unit: an alternating unit's half h takes blocks h,
+// h + 2, ...; otherwise each present half takes all of them.
+__device__ __forceinline__ bool alternates(const PfTile& t, int Tq) { return t.ntok <= Tq && t.npg > 2; }
 
 // The next unit from the producer's ring (whole warp) and its tile: -1 once
 // there is no more work, -2 on abort.
 __device__ __forceinline__ int take_unit(CpBars& bars, const UnitSlot* s_unit, uint32_t k, int lane,
-                                         volatile int* abort, Ctrl* ctrl, PfTile& t) {
+                                         volatile int* abort, Ctrl* ctrl, PfTile& t, int* pid = nullptr) {
     const int slot = k % kUnitSlots;
-    if (!warp_wait(smem_u32(&bars.unit_full[slot]), (k / kUnitSlots) & 1, abort, ctrl)) return -2;
+    if (!cwait(smem_u32(&bars.unit_full[slot]), (k / kUnitSlots) & 1, abort, ctrl)) return -2;
     const volatile int4* src = reinterpret_cast<const volatile int4*>(&s_unit[slot]);
     const int4 t0 = make_int4(src[0].x, src[0].y, src[0].z, src[0].w);
     const int4 t1 = make_int4(src[1].x, src[1].y, src[1].z, src[1].w);
     const int u = src[2].x;
     t.t0 = t0.x; t.ntok = t0.y; t.row = t0.z; t.first_page = t0.w;
     t.npg = t1.x; t.lo_min = t1.y; t.pos_max = t1.z; t.pad = t1.w;
+    if (pid) *pid = reinterpret_cast<const volatile int*>(s_unit[slot].pids)[lane];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars.unit_empty[slot]));
     return u;
 }
 
 // ---------------------------------------------------------------------------
-// Converters (four warps): codes of the unit stream's blocks to f16.
+// The block warp: descriptors of the unit stream's blocks.
 // ---------------------------------------------------------------------------
 // A scale's power of two at or above it, as a biased exponent in [1, 252].
 __device__ __forceinline__ int exp_above(uint32_t bits) {
@@ -106,116 +140,58 @@ __device__ __forceinline__ int exp_above(uint32_t bits) {
     return min(max(e, 1), 252);
 }
 
-template <int D, typename Code>
-__device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw, int lane, uint8_t* stages, CpBars& bars,
-                                             const UnitSlot* s_unit, uint32_t* s_ratio, volatile float* s_ref,
-                                             volatile int* abort, Ctrl* ctrl) {
-    using C = CpCfg<D>;
-    // A thread takes 16 codes of four keys (32 j + 8 cw + lane / 4, j = 0..3)
-    // from each 64-column box: eight lanes then store the even 16-byte chunks
-    // of one key and the odd ones of the next, which fill the eight bank
-    // groups, and every address is a constant away from two bases.
-    constexpr int kKeys = 4, kPer = kKeys * C::kBoxes;
+template <int D>
+__device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane, CpBars& bars, const UnitSlot* s_unit,
+                                           BlockDesc* s_desc, volatile int* abort, Ctrl* ctrl) {
+    // Descriptor n goes where n - kDescs was.  The softmax may read that one
+    // until its block's PV is issued, which the conversion of the V kStages
+    // blocks later has waited for.
+    constexpr uint32_t kAhead = kDescs - CpCfg<D>::kStages;
     const PrefillArgs& a = ca.a;
-    const int Hk = a.kv_heads, kx = lane >> 2;
-    const size_t src_off = (size_t)(cw * 8 + kx) * D + (lane & 3) * 16;
-    const int dst0 = cw * 1024 + kx * 128 + (((2 * (lane & 3)) ^ kx) << 4);
-    const int dst1 = cw * 1024 + kx * 128 + (((2 * (lane & 3) + 1) ^ kx) << 4);
-    PfTile t;
-    uint32_t k = 0;
-    int bk = -1, npg = 0, kvh = 0;
-    int pid_base = -32, pid_cur = 0, pid_nxt = 0;
-    bool fresh = false;                         // the block starts a unit
-    int y0 = 0, y1 = -1;                        // first rows of the block's pages in the pools; -1: no second page
-    const int* trow = nullptr;
-    auto page_row = [&](int pi) -> int {
-        if (pi - pid_base >= 32) {              // pages are visited in order, 32 ids at a time
-            if (pid_base < 0) pid_cur = lane < npg ? __ldg(trow + lane) : 0;
-            else pid_cur = pid_nxt;
-            pid_base += 32;
-            pid_nxt = pid_base + 32 + lane < npg ? __ldg(trow + pid_base + 32 + lane) : 0;
-        }
-        int page = __shfl_sync(0xffffffffu, pid_cur, pi & 31);
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) set_error(ctrl, kErrBadPage);
-            page = 0;
-        }
-        return (page * Hk + kvh) * kPageSize;
-    };
-    // The next block of the stream; false at its end.
-    auto advance = [&]() -> bool {
-        fresh = false;
-        if (2 * ++bk >= npg) {
-            const int u = take_unit(bars, s_unit, k++, lane, abort, ctrl, t);
-            if (u < 0) return false;
-            kvh = u % Hk;
-            npg = t.npg;
-            trow = a.table + (size_t)t.row * a.pages_per_row + t.first_page;
-            pid_base = -32;
-            bk = 0;
-            fresh = true;
-        }
-        y0 = page_row(2 * bk);
-        y1 = 2 * bk + 1 < npg ? page_row(2 * bk + 1) : -1;
-        return true;
-    };
-    uint4 kr[kPer], vr[kPer];
-    float4 ksc, vsc;
-    // (index: key j, box)
-    auto load = [&](uint4 (&r)[kPer], const uint8_t* pool) {
-        #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int j = i / C::kBoxes, y = j < kKeys / 2 ? y0 : y1;
-            if (y >= 0)
-                r[i] = __ldg(reinterpret_cast<const uint4*>(pool + (size_t)y * D + src_off + (j & 1) * 32 * D +
-                                                            (i % C::kBoxes) * 64));
-        }
-    };
-    auto load_scales = [&]() {
-        const int y = lane < 16 ? y0 : y1;
-        ksc = vsc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (y >= 0) {
-            ksc = __ldg(reinterpret_cast<const float4*>(ca.k_scale + y) + (lane & 15));
-            vsc = __ldg(reinterpret_cast<const float4*>(ca.v_scale + y) + (lane & 15));
-        }
-    };
-    // Widen, scale and store this thread's codes of one operand; r2: the
-    // ratio of each of its keys, twice.
-    auto store = [&](const uint4 (&r)[kPer], uint8_t* base, const uint32_t (&r2)[kKeys], bool two) {
-        #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int j = i / C::kBoxes;
-            if (j >= kKeys / 2 && !two) break;
-            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-            uint32_t h[8];
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                widen4<Code>(w[e], h[2 * e], h[2 * e + 1]);
-                h[2 * e] = mul_f16x2(h[2 * e], r2[j]);
-                h[2 * e + 1] = mul_f16x2(h[2 * e + 1], r2[j]);
+    const int Hk = a.kv_heads;
+    uint32_t n = 0;
+    for (uint32_t k = 0;; ++k) {
+        PfTile t;
+        int pid_cur = 0;
+        const int u = take_unit(bars, s_unit, k, lane, abort, ctrl, t, &pid_cur);
+        if (u == -2) return;
+        const int npg = u < 0 ? 1 : t.npg, kvh = u < 0 ? 0 : u % Hk;
+        const int* trow = u < 0 ? nullptr : a.table + (size_t)t.row * a.pages_per_row + t.first_page;
+        int pid_base = 0, pid_nxt = u >= 0 && 32 + lane < npg ? __ldg(trow + 32 + lane) : 0;
+        auto page_row = [&](int pi) -> int {
+            if (pi - pid_base >= 32) {          // pages are visited in order, 32 ids at a time
+                pid_cur = pid_nxt;
+                pid_base += 32;
+                pid_nxt = pid_base + 32 + lane < npg ? __ldg(trow + pid_base + 32 + lane) : 0;
             }
-            uint8_t* to = base + (i % C::kBoxes) * 16384 + j * 4096;
-            *reinterpret_cast<uint4*>(to + dst0) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(to + dst1) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
-    };
-    bool more = advance();
-    if (more) {
-        load_scales();
-        load(kr, ca.k);
-        load(vr, ca.v);
-    }
-    int v_exp = 1;                              // biased exponent of the unit's V ref
-    for (uint32_t it = 0; more; ++it) {
-        const int st = it % C::kStages;
-        const uint32_t par = (it / C::kStages) & 1;
-        const bool two = y1 >= 0;
-        uint32_t rk[kKeys], rv[kKeys];
-        bool all_in;                            // every key of the block is one of the tile's
-        // ---- ratios of the block's keys (each warp its own copy)
-        {
+            int page = __shfl_sync(0xffffffffu, pid_cur, pi & 31);
+            if (page < 0 || page >= a.num_pages) {
+                if (lane == 0) set_error(ctrl, kErrBadPage);
+                page = 0;
+            }
+            return (page * Hk + kvh) * kPageSize;
+        };
+        int v_exp = 1;                          // biased exponent of the unit's V ref so far
+        #pragma unroll 1
+        for (int bk = 0; 2 * bk < npg; ++bk, ++n) {
+            int y0 = -1, y1 = -1;
+            float ks[4] = {}, vs[4] = {};
+            if (u >= 0) {
+                y0 = page_row(2 * bk);
+                if (2 * bk + 1 < npg) y1 = page_row(2 * bk + 1);
+                const int y = lane < 16 ? y0 : y1;
+                if (y >= 0) {
+                    const float4 kq = __ldg(reinterpret_cast<const float4*>(ca.k_scale + y) + (lane & 15));
+                    const float4 vq = __ldg(reinterpret_cast<const float4*>(ca.v_scale + y) + (lane & 15));
+                    ks[0] = kq.x; ks[1] = kq.y; ks[2] = kq.z; ks[3] = kq.w;
+                    vs[0] = vq.x; vs[1] = vq.y; vs[2] = vq.z; vs[3] = vq.w;
+                }
+            }
+            if (n >= kAhead) {
+                const uint32_t m = n - kAhead;
+                if (!cwait(smem_u32(&bars.desc_empty[m % kDescs]), (m / kDescs) & 1, abort, ctrl)) return;
+            }
             const int key0 = (t.first_page + 2 * bk) * kPageSize + 4 * lane;
-            const float ks[4] = {ksc.x, ksc.y, ksc.z, ksc.w}, vs[4] = {vsc.x, vsc.y, vsc.z, vsc.w};
             uint32_t kb[4], vb[4], kmax = 0, vmax = 0;
             bool bad[4], in_range = true;
             #pragma unroll
@@ -232,56 +208,128 @@ __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw,
             kmax = __reduce_max_sync(0xffffffffu, kmax);
             vmax = __reduce_max_sync(0xffffffffu, vmax);
             const int k_exp = exp_above(kmax);
-            v_exp = fresh ? exp_above(vmax) : max(v_exp, exp_above(vmax));
+            v_exp = max(v_exp, exp_above(vmax));
             const float k_down = __uint_as_float((uint32_t)(254 - k_exp) << 23);
             const float v_down = __uint_as_float((uint32_t)(254 - v_exp) << 23);
-            uint32_t rr[4];
+            uint32_t own[4];
             #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                rr[e] = pack_f16x2(__uint_as_float(kb[e]) * k_down, __uint_as_float(vb[e]) * v_down);
-                if (bad[e]) rr[e] = 0x7e00u;                              // K ratio NaN, V ratio 0
+                own[e] = pack_f16x2(__uint_as_float(kb[e]) * k_down, __uint_as_float(vb[e]) * v_down);
+                if (bad[e]) own[e] = 0x7e00u;                             // K ratio NaN, V ratio 0
             }
-            __syncwarp();                       // the previous block's ratios are no longer read
-            *reinterpret_cast<uint4*>(s_ratio + 4 * lane) = make_uint4(rr[0], rr[1], rr[2], rr[3]);
+            const bool all_in = __all_sync(0xffffffffu, in_range);
+            BlockDesc& d = s_desc[n % kDescs];
+            *reinterpret_cast<uint4*>(d.ratio + 4 * lane) = make_uint4(own[0], own[1], own[2], own[3]);
+            if (lane == 0) {
+                *reinterpret_cast<int4*>(&d) = make_int4(y0, y1, all_in ? 1 : 0, 0);
+                *reinterpret_cast<float2*>(&d.k_ref) =
+                    make_float2(__uint_as_float((uint32_t)k_exp << 23), __uint_as_float((uint32_t)v_exp << 23));
+            }
             __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.desc_full[n % kDescs]));
+        }
+        if (u < 0) return;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Converters (four warps): codes of the unit stream's blocks to f16.
+// ---------------------------------------------------------------------------
+template <int D, typename Code>
+__device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw, int lane, uint8_t* stages, CpBars& bars,
+                                             const BlockDesc* s_desc, volatile int* s_blocks, volatile int* abort,
+                                             Ctrl* ctrl) {
+    using C = CpCfg<D>;
+    // A thread takes 16 codes of four keys (32 j + 8 cw + lane / 4, j = 0..3)
+    // from each 64-column box: eight lanes then store the even 16-byte chunks
+    // of one key and the odd ones of the next, which fill the eight bank
+    // groups, and every address is a constant away from two bases.
+    constexpr int kKeys = 4, kPer = kKeys * C::kBoxes;
+    const int kx = lane >> 2;
+    const size_t src_off = (size_t)(cw * 8 + kx) * D + (lane & 3) * 16;
+    const int dst0 = cw * 1024 + kx * 128 + (((2 * (lane & 3)) ^ kx) << 4);
+    const int dst1 = cw * 1024 + kx * 128 + (((2 * (lane & 3) + 1) ^ kx) << 4);
+    uint4 r[kPer];                              // codes of the next operand to convert: key i / boxes, box i % boxes
+    int y0 = -1, y1 = -1;                       // pages of the next codes to load
+    auto take_desc = [&](uint32_t n, int* all_in) -> bool {
+        if (!cwait(smem_u32(&bars.desc_full[n % kDescs]), (n / kDescs) & 1, abort, ctrl)) return false;
+        const uint4 d = lds128(smem_u32(&s_desc[n % kDescs]));
+        y0 = (int)d.x;
+        y1 = (int)d.y;
+        *all_in = (int)d.z;
+        return y0 >= 0;
+    };
+    int all_in = 1, next_in = 1;
+    if (!take_desc(0, &all_in)) return;
+    const uint8_t* p0 = ca.k + (size_t)y0 * D + src_off;
+    const uint8_t* p1 = ca.k + (size_t)max(y1, 0) * D + src_off;
+    #pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int j = i / C::kBoxes;
+        if (j < kKeys / 2 || y1 >= 0)
+            r[i] = __ldg(reinterpret_cast<const uint4*>((j < kKeys / 2 ? p0 : p1) + (j & 1) * 32 * D + (i % C::kBoxes) * 64));
+    }
+    #pragma unroll 1
+    for (uint32_t it = 0;; ++it) {
+        const int st = it % C::kStages;
+        const uint32_t par = (it / C::kStages) & 1;
+        const bool two = y1 >= 0;
+        bool more = true;
+        // K, then V, through one copy of the code.  Each register is refilled
+        // as soon as it is converted, a whole operand ahead of its use.
+        #pragma unroll 1
+        for (int op = 0; op < 2; ++op) {
+            if (op == 1) {
+                more = take_desc(it + 1, &next_in);
+                if (!more && *abort) return;
+            }
+            const uint8_t* pool = op == 0 ? ca.v : ca.k;
+            p0 = pool + (size_t)max(y0, 0) * D + src_off;
+            p1 = pool + (size_t)max(y1, 0) * D + src_off;
+            uint32_t r2[kKeys];
             #pragma unroll
             for (int j = 0; j < kKeys; ++j) {
-                const uint32_t r = s_ratio[32 * j + cw * 8 + kx];
-                rk[j] = __byte_perm(r, r, 0x1010);
-                rv[j] = __byte_perm(r, r, 0x3232);
+                const uint32_t rr = s_desc[it % kDescs].ratio[32 * j + cw * 8 + kx];
+                r2[j] = __byte_perm(rr, rr, op == 0 ? 0x1010 : 0x3232);
             }
-            all_in = __all_sync(0xffffffffu, in_range);
-            // (K's stage is free only after the softmax has read the refs of
-            // the block kRefs - kStages before)
-            if (!warp_wait(smem_u32(&bars.k_empty[st]), par ^ 1, abort, ctrl)) return;
-            if (cw == 0 && lane == 0) {
-                s_ref[2 * (it % kRefs)] = __uint_as_float((uint32_t)k_exp << 23);
-                s_ref[2 * (it % kRefs) + 1] = __uint_as_float((uint32_t)v_exp << 23);
-                mbar_arrive(smem_u32(&bars.ref_full[it % kRefs]));
+            if (!all_in) {
+                // a row outside the tile's keys (ratio 0) may hold any codes, e4m3's NaN among them
+                #pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (r2[i / C::kBoxes] == 0) r[i] = make_uint4(0, 0, 0, 0);
             }
-        }
-        uint8_t* to = stages + st * C::kStageBytes;
-        store(kr, to, rk, two);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.k_ready[st]));
-        more = advance();
-        if (more) {
-            load_scales();
-            load(kr, ca.k);
-        }
-        if (!all_in) {
-            // a V row outside the tile's keys (ratio 0) may hold any codes, e4m3's NaN among them
+            if (!cwait(smem_u32(op == 0 ? &bars.k_empty[st] : &bars.v_empty[st]), par ^ 1, abort, ctrl)) return;
+            uint8_t* base = stages + st * C::kStageBytes + op * C::kKBytes;
             #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (rv[i / C::kBoxes] == 0) vr[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kPer; ++i) {
+                const int j = i / C::kBoxes;
+                if (j < kKeys / 2 || two) {
+                    const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+                    uint32_t h[8];
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        widen4<Code>(w[e], h[2 * e], h[2 * e + 1]);
+                        h[2 * e] = mul_f16x2(h[2 * e], r2[j]);
+                        h[2 * e + 1] = mul_f16x2(h[2 * e + 1], r2[j]);
+                    }
+                    uint8_t* to = base + (i % C::kBoxes) * 16384 + j * 4096;
+                    *reinterpret_cast<uint4*>(to + dst0) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(to + dst1) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                if (more && (j < kKeys / 2 || y1 >= 0))
+                    r[i] = __ldg(reinterpret_cast<const uint4*>((j < kKeys / 2 ? p0 : p1) + (j & 1) * 32 * D +
+                                                                (i % C::kBoxes) * 64));
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(op == 0 ? &bars.k_ready[st] : &bars.v_ready[st]));
         }
-        if (!warp_wait(smem_u32(&bars.v_empty[st]), par ^ 1, abort, ctrl)) return;
-        store(vr, to + C::kKBytes, rv, two);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.v_ready[st]));
-        if (more) load(vr, ca.v);
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&bars.desc_empty[it % kDescs]));
+            if (cw == 0) *s_blocks = (int)it + 1;   // progress, for the scheduler
+        }
+        if (!more) return;
+        all_in = next_in;
     }
 }
 
@@ -311,25 +359,27 @@ __device__ __forceinline__ float sink_scale(float mu, float l, bool has_sink, fl
 
 template <int D>
 __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int half, int quarter, int lane, uint32_t tmem,
-                                             CpBars& bars, const volatile float* s_ref, const UnitSlot* s_unit,
-                                             volatile int* abort, Ctrl* ctrl) {
+                                             CpBars& bars, const BlockDesc* s_desc, volatile AltSums& s_alt,
+                                             const UnitSlot* s_unit, volatile int* abort, Ctrl* ctrl) {
     using C = CpCfg<D>;
     const PrefillArgs& a = ca.a;
     const int W = a.window, Hk = a.kv_heads, g = a.group, Tq = a.tile_tokens / 2;
     const int m = quarter * 32 + lane;                    // MMA row = TMEM lane
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_addr = tmem + lane_base + 128u * half, o_addr = tmem + lane_base + C::kColO + half * D;
-    const int tq = m / g, jh = m % g, tok = half * Tq + tq;
+    const int tq = m / g, jh = m % g;
     const __nv_bfloat16* sinks = static_cast<const __nv_bfloat16*>(a.sinks);
     const bool out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     const uint32_t s_full = smem_u32(&bars.s_full[half]), p_full = smem_u32(&bars.p_full[half]);
-    uint32_t it = 0, ch = 0, uh = 0, k = 0;
+    uint32_t it = 0, ch = 0, uh = 0, uh_b = 0, ua = 0, k = 0;   // blocks; this half's blocks, units; half B's units; alternating units
     bool ok = true;
     PfTile t;
     int u = take_unit(bars, s_unit, k++, lane, abort, ctrl, t);
     int pos_next = -1;
     float f_next = 1.f;
+    auto token_of = [&](const PfTile& tt) { return alternates(tt, Tq) ? tq : half * Tq + tq; };
     auto row_inputs = [&](const PfTile& tt, int uu) {
+        const int tok = token_of(tt);
         pos_next = -1;
         if (tq < Tq && tok < tt.ntok) {
             pos_next = __ldg(a.positions + tt.t0 + tok);
@@ -339,61 +389,77 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
     if (u >= 0) row_inputs(t, u);
     while (u >= 0) {
         const int kvh = u % Hk, nb = (t.npg + 1) / 2;
-        if (half == 1 && t.ntok <= Tq) {
+        const bool alt = alternates(t, Tq);
+        if (half == 1 && t.ntok <= Tq && !alt) {
             it += nb;
             u = take_unit(bars, s_unit, k++, lane, abort, ctrl, t);
             if (u >= 0) row_inputs(t, u);
             continue;
         }
+        const int tok = token_of(t);
         const bool active = tq < Tq && tok < t.ntok;
         const bool warp_active = __any_sync(0xffffffffu, active);
-        const int pos = active ? max(pos_next, 0) : -1;
+        // (a row that holds no query must not keep its warp from skipping masks)
+        const int pos = active ? max(pos_next, 0) : INT_MAX;
         const int lo = active && W > 0 && pos - W + 1 > 0 ? pos - W + 1 : 0;
         const float qf = f_next;
         float m_run = -INFINITY, l = 0.f, v_ref = 1.f;
-        for (int b = 0; b < nb; ++b) {
-            ok = warp_wait(s_full, (ch + b) & 1, abort, ctrl);
+        const int first = alt ? half : 0, stride = alt ? 2 : 1;
+        for (int b = first; b < nb; b += stride) {
+            ok = cwait(s_full, ch & 1, abort, ctrl);
             if (!ok) break;
+            ++ch;
             tc_fence_after();
             if (!warp_active) {                            // none of this warp's rows is a query
                 tc_fence_before();
                 if (lane == 0) mbar_arrive(p_full);
                 continue;
             }
-            const int ri = (it + b) % kRefs;
-            ok = warp_wait(smem_u32(&bars.ref_full[ri]), ((it + b) / kRefs) & 1, abort, ctrl);
+            const int di = (it + b) % kDescs;
+            ok = cwait(smem_u32(&bars.desc_full[di]), ((it + b) / kDescs) & 1, abort, ctrl);
             if (!ok) break;
-            const float v_new = s_ref[2 * ri + 1];
+            const float v_new = *reinterpret_cast<const volatile float*>(&s_desc[di].v_ref);
             // a factor that underflows keeps -inf times it at -inf
-            const float f = fmaxf(qf * s_ref[2 * ri], kScaleMin);
+            const float f = fmaxf(qf * *reinterpret_cast<const volatile float*>(&s_desc[di].k_ref), kScaleMin);
             const int pg0 = t.first_page + 2 * b, key0 = pg0 * kPageSize, npb = min(2, t.npg - 2 * b);
             // keys c of this block visible to the row: c_lo <= c <= c_hi;
-            // 32-column chunks visible to every row of the warp skip the test
+            // 32-column chunks visible to every row of the warp skip the test, and
+            // those visible to none the exponentials too
             const int c_lo = lo - key0, c_hi = min(pos - key0, npb * kPageSize - 1);
-            const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 2 * kPageSize - 1);
-            auto mask = [&](uint32_t (&x)[32], int b0) {
-                if (!whole && !__all_sync(0xffffffffu, c_lo <= b0 && c_hi >= b0 + 31)) {
+            // (per chunk: 0 wholly visible to the warp, 1 not, 2 wholly hidden)
+            int state = 0;
+            if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 2 * kPageSize - 1)) {
+                #pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const int b0 = 32 * q4;
+                    const bool in = __all_sync(0xffffffffu, c_lo <= b0 && c_hi >= b0 + 31);
+                    const bool out = __all_sync(0xffffffffu, !active || c_lo > b0 + 31 || c_hi < b0);
+                    state |= (out ? 2 : in ? 0 : 1) << (2 * q4);
+                }
+            }
+            auto mask = [&](uint32_t (&y)[32], int q4) {
+                if (state >> (2 * q4) & 3) {
+                    const int from = min(max(c_lo - 32 * q4, 0), 32), to = min(max(c_hi + 1 - 32 * q4, 0), 32);
+                    const uint32_t vis = (uint32_t)((1ull << to) - 1) & ~(uint32_t)((1ull << from) - 1);
                     #pragma unroll
                     for (int c = 0; c < 32; ++c)
-                        if (b0 + c < c_lo || b0 + c > c_hi) x[c] = __float_as_uint(-INFINITY);
+                        if (!(vis >> c & 1)) y[c] = __float_as_uint(-INFINITY);
                 }
             };
-            // The first 64 columns stay in registers; the others are read
-            // twice, once for the maximum (a 128-column row and its weights
-            // do not fit beside the converters' share of the registers).
-            uint32_t s0[32], s1[32], x[32];
-            tmem_ld32(s_addr, s0);
-            tmem_ld32(s_addr + 32, s1);
-            tmem_ld32(s_addr + 64, x);
-            tmem_wait_ld();
-            mask(s0, 0);
-            mask(s1, 32);
-            mask(x, 64);
-            float top = fmax3(max32(s0), max32(s1), max32(x));
-            tmem_ld32(s_addr + 96, x);
-            tmem_wait_ld();
-            mask(x, 96);
-            top = fmaxf(top, max32(x));
+            // Both passes are rolled loops over 32 columns: a scheduler's warps
+            // run two softmax halves and a converter, and code that outgrows
+            // its instruction cache cost 7 to 15 clocks per instruction
+            // (unrolled passes: 1.5 times the kernel's time).  Reading S twice
+            // costs 30 clocks per chunk.
+            float top = -INFINITY;
+            #pragma unroll 1
+            for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t x[32];
+                tmem_ld32(s_addr + 32 * q4, x);
+                tmem_wait_ld();
+                if (state != 0) mask(x, q4);
+                top = fmaxf(top, max32(x));
+            }
             const float mx = top * f;
             const bool need = mx > m_run + kRescale;
             float alpha = 1.f;
@@ -402,9 +468,9 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
                 m_run = mx;
                 l *= alpha;
             }
-            if (b > 0) alpha *= v_ref / v_new;             // powers of two: exact
+            if (b > first) alpha *= v_ref / v_new;         // powers of two: exact
             v_ref = v_new;
-            if (b > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (b > first && __any_sync(0xffffffffu, alpha != 1.f)) {
                 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
@@ -417,10 +483,16 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             }
             const float neg_mu = m_run == -INFINITY ? 0.f : kPBias - m_run;
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            // weights of 32 columns over the first 64 columns of S, of which
-            // the registers hold what is still needed
+            // weights of 32 columns over the first 64 columns of S: chunk q's go
+            // over columns that chunks 0 .. q / 2 held, which have been read
             auto weights = [&](const uint32_t (&y)[32], int q4) {
                 uint32_t pk[16];
+                if ((state >> (2 * q4) & 3) == 2) {
+                    #pragma unroll
+                    for (int c = 0; c < 16; ++c) pk[c] = 0;
+                    tmem_st16(s_addr + 16 * q4, pk);
+                    return;
+                }
                 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                     float p0, p1;
@@ -432,16 +504,14 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
                 }
                 tmem_st16(s_addr + 16 * q4, pk);
             };
-            tmem_ld32(s_addr + 64, x);
-            weights(s0, 0);
-            weights(s1, 1);
-            tmem_wait_ld_of(x);
-            mask(x, 64);
-            tmem_ld32(s_addr + 96, s0);
-            weights(x, 2);
-            tmem_wait_ld_of(s0);
-            mask(s0, 96);
-            weights(s0, 3);
+            #pragma unroll 1
+            for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t x[32];
+                tmem_ld32(s_addr + 32 * q4, x);
+                tmem_wait_ld();
+                if (state != 0) mask(x, q4);
+                weights(x, q4);
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -452,69 +522,102 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
         PfTile tn;
         const int un = take_unit(bars, s_unit, k++, lane, abort, ctrl, tn);
         if (un >= 0) row_inputs(tn, un);
-        ok = warp_wait(smem_u32(&bars.o_done[half]), uh & 1, abort, ctrl);
+        ok = cwait(smem_u32(&bars.o_done[half]), uh & 1, abort, ctrl);
         if (!ok) break;
         tc_fence_after();
-        if (warp_active) {
-            const int h = kvh * g + jh;
-            const float mu = m_run == -INFINITY ? -1.0e30f : m_run - kPBias;
-            if (t.pad == 0) {
-                const float sk = sinks != nullptr && active ? __bfloat162float(sinks[h]) * 1.4426950408889634f : 0.f;
-                const float inv = sink_scale(mu, l, sinks != nullptr, sk) * v_ref;
-                __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + tok) * a.heads + h) * D;
-                #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t o[64];
-                    tmem_ld32(o_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-                    tmem_ld32(o_addr + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
-                    tmem_wait_ld();
-                    if (active) {
-                        #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint32_t w[8];
-                            #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                w[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]) * inv,
-                                                   __uint_as_float(o[16 * v + 2 * e + 1]) * inv);
-                            __nv_bfloat16* dst = orow + c0 + 16 * v;
-                            if (out_wide) {
-                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                                             ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-                                               "r"(w[5]), "r"(w[6]), "r"(w[7])
-                                             : "memory");
-                            } else {
-                                reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                            }
-                        }
-                    }
+        const float mu = m_run == -INFINITY ? -1.0e30f : m_run - kPBias;
+        if (alt && half == 1) {
+            // hand the sums to half A, whose epilogue merges both; O stays
+            // until it has (this half's next weights come after alt_free)
+            s_alt.mu[m] = mu;
+            s_alt.l[m] = l;
+            s_alt.v_ref[m] = v_ref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.alt_full));
+            ok = cwait(smem_u32(&bars.alt_free), ua & 1, abort, ctrl);
+            if (!ok) break;
+        } else {
+            float M = mu, L = l, fa = v_ref, fb = 0.f;     // O = fa O_A + fb O_B
+            if (alt) {
+                ok = cwait(smem_u32(&bars.o_done[1]), uh_b & 1, abort, ctrl) &&
+                     cwait(smem_u32(&bars.alt_full), ua & 1, abort, ctrl);
+                if (!ok) break;
+                tc_fence_after();
+                const float mu_b = s_alt.mu[m];
+                M = fmaxf(mu, mu_b);
+                const float ea = exp2_approx(mu - M), eb = exp2_approx(mu_b - M);
+                L = l * ea + s_alt.l[m] * eb;
+                fa = v_ref * ea;
+                fb = s_alt.v_ref[m] * eb;
+            }
+            if (warp_active) {
+                const int h = kvh * g + jh;
+                float sk = 0.f;
+                if (sinks != nullptr && active && t.pad == 0) sk = __bfloat162float(sinks[h]) * 1.4426950408889634f;
+                if (t.pad == 0) {
+                    const float inv = sink_scale(M, L, sinks != nullptr, sk);
+                    fa *= inv;
+                    fb *= inv;
                 }
-            } else {
-                // a piece of a split tile: unnormalised O, maximum and sum
+                // a piece of a split tile leaves its unnormalised O, maximum and sum
                 const size_t at = ((size_t)(t.pad - 1) * Hk + kvh) * ca.slot_rows + tok * g + jh;
-                float* orow = ca.part_o + at * D;
-                if (active) ca.part_ml[at] = make_float2(mu, l);
+                if (t.pad != 0 && active) ca.part_ml[at] = make_float2(M, L);
+                __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + tok) * a.heads + h) * D;
                 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_addr + c0, o);
                     tmem_wait_ld();
-                    if (active) {
+                    #pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * fa);
+                    if (alt) {
+                        uint32_t ob[32];
+                        tmem_ld32(o_addr + D + c0, ob);
+                        tmem_wait_ld();
+                        #pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            o[c] = __float_as_uint(fmaf(__uint_as_float(ob[c]), fb, __uint_as_float(o[c])));
+                    }
+                    if (!active) continue;
+                    if (t.pad != 0) {
+                        float4* dst = reinterpret_cast<float4*>(ca.part_o + at * D + c0);
                         #pragma unroll
                         for (int c = 0; c < 32; c += 4)
-                            *reinterpret_cast<float4*>(orow + c0 + c) =
-                                make_float4(__uint_as_float(o[c]) * v_ref, __uint_as_float(o[c + 1]) * v_ref,
-                                            __uint_as_float(o[c + 2]) * v_ref, __uint_as_float(o[c + 3]) * v_ref);
+                            dst[c / 4] = make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]),
+                                                     __uint_as_float(o[c + 2]), __uint_as_float(o[c + 3]));
+                        continue;
+                    }
+                    #pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        uint32_t w[8];
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]), __uint_as_float(o[16 * v + 2 * e + 1]));
+                        __nv_bfloat16* dst = orow + c0 + 16 * v;
+                        if (out_wide) {
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                                         ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                                           "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                         : "memory");
+                        } else {
+                            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 }
             }
+            // The next unit's first PV overwrites O only after this read (its
+            // p_full arrival follows in program order; half B's, after alt_free).
+            tc_fence_before();
+            if (alt) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.alt_free));
+            }
         }
-        // The next unit's first PV overwrites O only after this read (its
-        // p_full arrival follows in program order).
-        tc_fence_before();
-        ch += nb;
         it += nb;
         ++uh;
+        if (alt) ++ua;
+        if (alt || t.ntok > Tq) ++uh_b;
         u = un;
         t = tn;
     }
@@ -527,11 +630,11 @@ __global__ void __launch_bounds__(kCpThreads, 1)
     const PrefillArgs& a = ca.a;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) CpBars bars;
-    __shared__ __align__(16) uint32_t s_ratio[4][128];
-    __shared__ float s_ref[2 * kRefs];
+    __shared__ BlockDesc s_desc[kDescs];
     __shared__ UnitSlot s_unit[kUnitSlots];
+    __shared__ AltSums s_alt;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_blocks;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -549,7 +652,10 @@ __global__ void __launch_bounds__(kCpThreads, 1)
             mbar_init(smem_u32(&bars.v_ready[s]), 4);
             mbar_init(smem_u32(&bars.v_empty[s]), 1);
         }
-        for (int r = 0; r < kRefs; ++r) mbar_init(smem_u32(&bars.ref_full[r]), 1);
+        for (int r = 0; r < kDescs; ++r) {
+            mbar_init(smem_u32(&bars.desc_full[r]), 1);
+            mbar_init(smem_u32(&bars.desc_empty[r]), 4);
+        }
         mbar_init(smem_u32(&bars.mma_done), 1);
         for (int k = 0; k < kUnitSlots; ++k) {
             mbar_init(smem_u32(&bars.unit_full[k]), 1);
@@ -562,7 +668,10 @@ __global__ void __launch_bounds__(kCpThreads, 1)
             mbar_init(smem_u32(&bars.p_full[h]), 4);
             mbar_init(smem_u32(&bars.o_done[h]), 1);
         }
+        mbar_init(smem_u32(&bars.alt_full), 4);
+        mbar_init(smem_u32(&bars.alt_free), 4);
         s_abort = 0;
+        s_blocks = 0;
         fence_barrier_init();
         prefetch_tensormap(&q_map);
     }
@@ -582,47 +691,75 @@ __global__ void __launch_bounds__(kCpThreads, 1)
     const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + ca.units);
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        softmax_half<D>(ca, (warp - 8) >> 2, warp & 3, lane, tmem, bars, s_ref, s_unit, abort, ctrl);
+        softmax_half<D>(ca, (warp - 8) >> 2, warp & 3, lane, tmem, bars, s_desc, s_alt, s_unit, abort, ctrl);
     } else if (warp >= 4) {
-        convert_warp<D, Code>(ca, warp - 4, lane, sm + C::kOffStage, bars, s_unit, s_ratio[warp - 4], s_ref, abort, ctrl);
+        convert_warp<D, Code>(ca, warp - 4, lane, sm + C::kOffStage, bars, s_desc, &s_blocks, abort, ctrl);
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
       if (warp == 0) {
-        // ---------------- units and Q (whole warp, one lane issues) ----------------
-        uint32_t uq[2] = {0, 0};     // units whose Q half h was loaded
+        // ---------------- units ----------------
         bool ok = true;
-        int u = blockIdx.x;
+        int u = blockIdx.x, queued = 0;
         for (uint32_t k = 0; ok; ++k) {
             if (k > 0) {
                 int v = 0;
-                if (lane == 0) v = (int)gridDim.x + atomicAdd(&ctrl->next_item, 1);
+                if (lane == 0) {
+                    uint64_t t0 = 0;
+                    while (queued - *reinterpret_cast<volatile int*>(&s_blocks) > kBlocksAhead && !*abort) {
+                        __nanosleep(256);
+                        const uint64_t now = globaltimer_ns();
+                        if (t0 == 0) {
+                            t0 = now;
+                        } else if (now - t0 > kPfTimeoutNs) {
+                            *abort = 1;
+                            set_error(ctrl, kErrTimeout);
+                        }
+                    }
+                    v = (int)gridDim.x + atomicAdd(&ctrl->next_item, 1);
+                }
                 u = __shfl_sync(0xffffffffu, v, 0);
             }
             const int slot = k % kUnitSlots;
             PfTile t = {};
-            if (u < n_units) t = tiles[u / Hk];
-            ok = warp_wait(smem_u32(&bars.unit_empty[slot]), ((k / kUnitSlots) & 1) ^ 1, abort, ctrl);
+            int pid = 0;
+            if (u < n_units) {
+                t = tiles[u / Hk];
+                if (lane < t.npg) pid = __ldg(a.table + (size_t)t.row * a.pages_per_row + t.first_page + lane);
+            }
+            ok = cwait(smem_u32(&bars.unit_empty[slot]), ((k / kUnitSlots) & 1) ^ 1, abort, ctrl);
             if (!ok) break;
             if (lane == 0) {
                 int4* dst = reinterpret_cast<int4*>(&s_unit[slot]);
                 dst[0] = make_int4(t.t0, t.ntok, t.row, t.first_page);
                 dst[1] = make_int4(t.npg, t.lo_min, t.pos_max, t.pad);
                 dst[2] = make_int4(u < n_units ? u : -1, 0, 0, 0);
-                mbar_arrive(smem_u32(&bars.unit_full[slot]));
             }
+            s_unit[slot].pids[lane] = pid;
             __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.unit_full[slot]));
             if (u >= n_units) break;
-            const int kvh = u % Hk, nh = uni(t.ntok > Tq ? 2 : 1), t0 = uni(t.t0);
+            queued += (t.npg + 1) / 2;
+        }
+      } else if (warp == 3) {
+        block_warp<D>(ca, lane, bars, s_unit, s_desc, abort, ctrl);
+      } else if (warp == 2) {
+        // ---------------- Q (whole warp, one lane issues) ----------------
+        uint32_t uq[2] = {0, 0};     // units whose Q half h was loaded
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            PfTile t;
+            const int u = take_unit(bars, s_unit, k, lane, abort, ctrl, t);
+            if (u < 0) break;
+            const bool alt = alternates(t, Tq);
+            const int kvh = uni(u % Hk), nh = uni(alt || t.ntok > Tq ? 2 : 1), t0 = uni(t.t0), step = uni(alt ? 0 : Tq);
             #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (!ok || h >= nh) break;
-                ok = warp_wait(smem_u32(&bars.q_empty[h]), (uq[h] & 1) ^ 1, abort, ctrl);
+                ok = cwait(smem_u32(&bars.q_empty[h]), (uq[h] & 1) ^ 1, abort, ctrl);
                 if (!ok) break;
                 const uint32_t qf = smem_u32(&bars.q_full[h]);
                 elect_arrive_expect_tx(qf, C::kBoxes * 128 * g * Tq);
                 for (int b = 0; b < C::kBoxes; ++b)
-                    elect_tma_3d(q_s + h * C::kQBytes + b * 16384, &q_map, b * 64, kvh * g, t0 + h * Tq, qf);
+                    elect_tma_3d(q_s + h * C::kQBytes + b * 16384, &q_map, b * 64, kvh * g, t0 + h * step, qf);
                 ++uq[h];
             }
         }
@@ -650,8 +787,9 @@ __global__ void __launch_bounds__(kCpThreads, 1)
             umma_commit(smem_u32(&bars.s_full[h]));
         };
         auto pv = [&](int h, uint32_t j, int s, bool first, bool one_page) -> bool {
-            if (!warp_wait(smem_u32(&bars.p_full[h]), j & 1, abort, ctrl)) return false;
+            if (!cwait(smem_u32(&bars.p_full[h]), j & 1, abort, ctrl)) return false;
             tc_fence_after();
+            issued = true;
             const uint64_t b0 = dv + (uint64_t)(s * (C::kStageBytes >> 4));
             #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
@@ -660,11 +798,20 @@ __global__ void __launch_bounds__(kCpThreads, 1)
                                     idesc_o, (first && ks == 0) ? 0u : 1u);
             return true;
         };
-        constexpr uint32_t kPend = 1, kPendFirst = 2, kPendLast = 4, kPendOne = 8, kPendB = 16, kEnd = 32;
-        uint32_t it = 0, uq0 = 0, uq1 = 0, cs0 = 0, cs1 = 0, f = 0;   // blocks; units / S per half; flags
-        int nh = 0, npg = 0, bk = 0;                                  // the current unit and block
+        // Blocks of successive units form one stream.  A step takes one block:
+        // for each half that works on it, the half's pending PV (of its
+        // previous block), then S of this block.  A pending PV of the unit
+        // before goes out at the next unit's first step in any case.  The
+        // half loop stays rolled so that each MMA sequence is issued from one
+        // place; per-half state is selected by value.
+        constexpr uint32_t kPend = 1, kFirst = 2, kLast = 4, kOne = 8, kFrees = 16;
+        uint32_t it = 0, uq0 = 0, uq1 = 0;               // blocks; units per half
+        uint32_t cs0 = 0, cs1 = 0, f0 = 0, f1 = 0;       // S issued per half; flags of the pending PV
+        uint32_t pit0 = 0, pit1 = 0;                     // its block
+        int nh = 0, npg = 0, bk = 0;                     // the current unit and block
+        bool alt = false, end = false;
         for (uint32_t k = 0; ok;) {
-            if (2 * bk >= npg) {                                      // the unit is done: the next one
+            if (2 * bk >= npg) {                         // the unit is done: the next one
                 if (npg > 0) {
                     ++uq0;
                     if (nh == 2) ++uq1;
@@ -678,55 +825,64 @@ __global__ void __launch_bounds__(kCpThreads, 1)
                 nh = 0;
                 npg = 0;
                 bk = 0;
-                if (u < 0) {
-                    f |= kEnd;
-                } else {
-                    nh = uni(t.ntok > Tq ? 2 : 1);
+                alt = false;
+                end = u < 0;
+                if (u >= 0) {
+                    alt = uni(alternates(t, Tq) ? 1 : 0);
+                    nh = uni(alt || t.ntok > Tq ? 2 : 1);
                     npg = uni(t.npg);
                 }
             }
             const int s = it % C::kStages;
             const bool one = npg - 2 * bk == 1;
+            bool k_waited = false;
             #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                if ((f & kPend) && (h == 0 || (f & kPendB))) {
-                    if (h == 0) {
-                        ok = warp_wait(smem_u32(&bars.v_ready[(it - 1) % C::kStages]), ((it - 1) / C::kStages) & 1, abort,
-                                       ctrl);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    ok = pv(h, (h ? cs1 : cs0) - 1, (it - 1) % C::kStages, f & kPendFirst, f & kPendOne);
+                const bool here = alt ? h == (bk & 1) : h < nh;
+                const uint32_t f = h ? f1 : f0;
+                if ((f & kPend) && (here || bk == 0)) {
+                    const uint32_t pit = h ? pit1 : pit0;
+                    ok = cwait(smem_u32(&bars.v_ready[pit % C::kStages]), (pit / C::kStages) & 1, abort, ctrl);
                     if (!ok) break;
-                    if (f & kPendLast) umma_commit(smem_u32(&bars.o_done[h]));
+                    ok = pv(h, (h ? cs1 : cs0) - 1, pit % C::kStages, f & kFirst, f & kOne);
+                    if (!ok) break;
+                    if (f & kFrees) umma_commit(smem_u32(&bars.v_empty[pit % C::kStages]));
+                    if (f & kLast) umma_commit(smem_u32(&bars.o_done[h]));
+                    if (h) f1 = 0;
+                    else f0 = 0;
                 }
-                if (h < nh) {
-                    if (h == 0) {
-                        ok = warp_wait(smem_u32(&bars.k_ready[s]), (it / C::kStages) & 1, abort, ctrl);
+                if (here) {
+                    if (!k_waited) {
+                        ok = cwait(smem_u32(&bars.k_ready[s]), (it / C::kStages) & 1, abort, ctrl);
                         if (!ok) break;
+                        k_waited = true;
                     }
-                    if (bk == 0) {
-                        ok = warp_wait(smem_u32(&bars.q_full[h]), (h ? uq1 : uq0) & 1, abort, ctrl);
+                    const bool first = alt ? bk < 2 : bk == 0;
+                    if (first) {
+                        ok = cwait(smem_u32(&bars.q_full[h]), (h ? uq1 : uq0) & 1, abort, ctrl);
                         if (!ok) break;
                     }
                     tc_fence_after();
                     issued = true;
                     qk(h, s, one);
+                    // the half's last block of the unit
+                    const bool last = 2 * (bk + (alt ? 2 : 1)) >= npg;
+                    if (last) umma_commit(smem_u32(&bars.q_empty[h]));
+                    const uint32_t nf = kPend | (first ? kFirst : 0) | (last ? kLast : 0) | (one ? kOne : 0) |
+                                        (alt || h == nh - 1 ? kFrees : 0);
+                    if (h) {
+                        f1 = nf;
+                        pit1 = it;
+                        ++cs1;
+                    } else {
+                        f0 = nf;
+                        pit0 = it;
+                        ++cs0;
+                    }
                 }
             }
-            if (!ok) break;
-            if (f & kPend) umma_commit(smem_u32(&bars.v_empty[(it - 1) % C::kStages]));
-            if (f & kEnd) break;
-            umma_commit(smem_u32(&bars.k_empty[s]));
-            const bool last = 2 * (bk + 1) >= npg;
-            if (last) {
-                umma_commit(smem_u32(&bars.q_empty[0]));
-                if (nh == 2) umma_commit(smem_u32(&bars.q_empty[1]));
-            }
-            f = kPend | (bk == 0 ? kPendFirst : 0) | (last ? kPendLast : 0) | (one ? kPendOne : 0) |
-                (nh == 2 ? kPendB : 0);
-            ++cs0;
-            if (nh == 2) ++cs1;
+            if (!ok || end) break;
+            umma_commit(smem_u32(&bars.k_empty[s]));     // this block's S issued
             ++it;
             ++bk;
         }
