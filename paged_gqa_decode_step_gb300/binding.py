@@ -356,7 +356,7 @@ def make_coded_cache(p, k, v, k_scale, v_scale):
     c = CodedCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _CODES[k.dtype], 0)
     # the block holds raw pointers: keep the tensors alive as long as it lives
     c._tensors = (k, v, k_scale, v_scale)
-    c._pool = pool
+    c._pool, c._device = pool, k.get_device()
     return c
 
 
@@ -384,66 +384,87 @@ def _same_device(*tensors):
     """Every tensor on the current device: the calls launch there."""
     here = torch.cuda.current_device()
     for t in tensors:
-        if t.device.index != here:
+        if t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+    return here
 
 
-def _check_coded(p, cache, ws, tokens, ints=(), table=None):
-    """Arguments of a coded call: tokens (name, tensor, heads) of [n, heads, D],
-    ints (name, tensor) of [n] int32.  Returns n and the workspace's arguments."""
+def _check_coded(p, cache, ws, n, heads, ints, table, **named):
+    """Arguments of a coded call: `named` of [n, heads, D] (heads by name), ints of [n] int32."""
     if not isinstance(cache, CodedCache):
         raise TypeError("cache must come from make_coded_cache or new_coded_cache")
     if cache._pool != (p.num_pages, p.kv_heads, 64, p.head_dim):
         raise ValueError(f"cache has pools {cache._pool}, the parameters another shape")
-    first = (tokens or ints)[0][1]
-    n = first.shape[0] if isinstance(first, torch.Tensor) and first.dim() else -1
-    for name, t, h in tokens:
-        _expect(name, t, (n, h, p.head_dim), _dt(p))
-    for name, t in ints:
-        _expect(name, t, (n,), torch.int32)
+    here = torch.cuda.current_device()
+    dt, D, Hk, Hq = _dt(p), p.head_dim, p.kv_heads, p.heads
+    kv, qs = (n, Hk, D), (n, Hq, D)
+    # one pass over each tensor's attributes; _expect names what is wrong
+    for name, t in named.items():
+        shape = qs if name in heads else kv
+        if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.get_device() == here
+                and t.is_contiguous()):
+            _expect(name, t, shape, dt)
+            _same_device(t)
+    for name, t in ints.items():
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == (n,) and t.get_device() == here
+                and t.is_contiguous()):
+            _expect(name, t, (n,), torch.int32)
+            _same_device(t)
     if table is not None:
-        _expect("table", table, (p.rows, p.pages_per_row), torch.int32)
-    w, nb = _ws(ws)
-    _same_device(cache._tensors[0], ws, *(t[1] for t in tokens), *(t[1] for t in ints),
-                 *(() if table is None else (table,)))
-    return n, w, nb
+        shape = (p.rows, p.pages_per_row)
+        if not (isinstance(table, torch.Tensor) and table.dtype is torch.int32 and table.shape == shape
+                and table.get_device() == here and table.is_contiguous()):
+            _expect("table", table, shape, torch.int32)
+            _same_device(table)
+    if cache._device != here or ws.get_device() != here or not ws.is_contiguous():
+        _ws(ws)
+        _same_device(cache._tensors[0], ws)
+
+
+def _tokens(t):
+    return t.shape[0] if isinstance(t, torch.Tensor) and t.dim() else -1
+
+
+def _raw_stream(stream):
+    # the current stream's handle without the Stream object, whose making takes
+    # longer (3 us) than the rest of a call's checks
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def coded_write(p, cache, k_new, v_new, positions, slots, ws, stream=None):
     """Codes of new keys (rotated at positions) and values [n, kv_heads, D] into pool slots [n] int32."""
-    n, w, nb = _check_coded(p, cache, ws, (("k_new", k_new, p.kv_heads), ("v_new", v_new, p.kv_heads)),
-                            (("positions", positions), ("slots", slots)))
-    _check(lib.pdattn_coded_write(ctypes.byref(p), ctypes.byref(cache), n, _ptr(k_new), _ptr(v_new), _ptr(positions),
-                                  _ptr(slots), w, nb, _stream(stream)))
+    n = _tokens(k_new)
+    _check_coded(p, cache, ws, n, (), dict(positions=positions, slots=slots), None, k_new=k_new, v_new=v_new)
+    _check(lib.pdattn_coded_write(p, cache, n, k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(),
+                                  slots.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 def coded_read(p, cache, slots, k_out, v_out, ws, stream=None):
     """What the codes of pool slots [n] int32 stand for, as k_out, v_out [n, kv_heads, D]."""
-    n, w, nb = _check_coded(p, cache, ws, (("k_out", k_out, p.kv_heads), ("v_out", v_out, p.kv_heads)),
-                            (("slots", slots),))
-    _check(lib.pdattn_coded_read(ctypes.byref(p), ctypes.byref(cache), n, _ptr(slots), _ptr(k_out), _ptr(v_out), w, nb,
-                                 _stream(stream)))
+    n = _tokens(slots)
+    _check_coded(p, cache, ws, n, (), dict(slots=slots), None, k_out=k_out, v_out=v_out)
+    _check(lib.pdattn_coded_read(p, cache, n, slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), ws.data_ptr(),
+                                 ws.nbytes, _raw_stream(stream)))
 
 
 def coded_decode(p, cache, q, k_new, v_new, positions, table, out, ws, stream=None):
     """decode_fused over a coded cache."""
-    _check_coded(p, cache, ws, (("q", q, p.heads), ("k_new", k_new, p.kv_heads), ("v_new", v_new, p.kv_heads),
-                                ("out", out, p.heads)), (("positions", positions),), table)
-    if q.shape[0] != p.rows:
-        raise ValueError(f"q has {q.shape[0]} rows, the parameters {p.rows}")
-    w, nb = _ws(ws)
-    _check(lib.pdattn_coded_decode(ctypes.byref(p), ctypes.byref(cache), _ptr(q), _ptr(k_new), _ptr(v_new),
-                                   _ptr(positions), _ptr(table), _ptr(out), w, nb, _stream(stream)))
+    _check_coded(p, cache, ws, p.rows, ("q", "out"), dict(positions=positions), table, q=q, k_new=k_new, v_new=v_new,
+                 out=out)
+    _check(lib.pdattn_coded_decode(p, cache, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(),
+                                   table.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 def coded_prefill(p, cache, q, k_new, v_new, positions, rows, slots, table, out, ws, stream=None):
     """prefill_paged over a coded cache (bf16)."""
-    n, w, nb = _check_coded(p, cache, ws, (("q", q, p.heads), ("k_new", k_new, p.kv_heads),
-                                           ("v_new", v_new, p.kv_heads), ("out", out, p.heads)),
-                            (("positions", positions), ("rows", rows), ("slots", slots)), table)
-    _check(lib.pdattn_coded_prefill(ctypes.byref(p), ctypes.byref(cache), n, _ptr(q), _ptr(k_new), _ptr(v_new),
-                                    _ptr(positions), _ptr(rows), _ptr(slots), _ptr(table), _ptr(out), w, nb,
-                                    _stream(stream)))
+    n = _tokens(q)
+    _check_coded(p, cache, ws, n, ("q", "out"), dict(positions=positions, rows=rows, slots=slots), table, q=q,
+                 k_new=k_new, v_new=v_new, out=out)
+    _check(lib.pdattn_coded_prefill(p, cache, n, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                    positions.data_ptr(), rows.data_ptr(), slots.data_ptr(), table.data_ptr(),
+                                    out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 def check_status(ws, stream=None):

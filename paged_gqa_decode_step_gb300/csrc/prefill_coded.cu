@@ -218,6 +218,12 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
                 if (bad[e]) own[e] = 0x7e00u;                             // K ratio NaN, V ratio 0
             }
             const bool all_in = __all_sync(0xffffffffu, in_range);
+            // The converters load one operand ahead, 16 KB: enough for L2's
+            // latency but not for HBM's, so the pages go to L2 from here.
+            if (lane < 4) {
+                const int y = lane & 1 ? y1 : y0;
+                if (y >= 0) prefetch_l2_bulk((lane < 2 ? ca.k : ca.v) + (size_t)y * D, kPageSize * D);
+            }
             BlockDesc& d = s_desc[n % kDescs];
             *reinterpret_cast<uint4*>(d.ratio + 4 * lane) = make_uint4(own[0], own[1], own[2], own[3]);
             if (lane == 0) {
