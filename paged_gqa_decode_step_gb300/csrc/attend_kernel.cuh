@@ -36,6 +36,7 @@
 
 #include "coded.cuh"
 #include "internal.h"
+#include "umma.cuh"
 
 namespace pdattn {
 
@@ -423,7 +424,9 @@ struct Consumer {
         // V scale = mantissa * 2^exponent
         const uint32_t vsa = __float_as_uint(lds_f32(scales + 256 + ta * 4));
         const uint32_t vsb = __float_as_uint(lds_f32(scales + 256 + tb * 4));
-        const float ea = (float)((int)(vsa >> 23) - 127), eb = (float)((int)(vsb >> 23) - 127);
+        // (the exponent's bits under 2^23's read 2^23 + exponent)
+        const float ea = __uint_as_float(0x4b000000u | vsa >> 23) - (8388608.f + 127.f);
+        const float eb = __uint_as_float(0x4b000000u | vsb >> 23) - (8388608.f + 127.f);
         // (an infinity or a NaN, exponent 255, makes the token's weight a NaN)
         const float ma = __uint_as_float((vsa >> 23) == 255 ? 0x7fc00000u : (vsa & 0x7fffffu) | 0x3f800000u);
         const float mb = __uint_as_float((vsb >> 23) == 255 ? 0x7fc00000u : (vsb & 0x7fffffu) | 0x3f800000u);
@@ -969,7 +972,23 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         // One lane runs the page loop: per page it waits for a free stage,
         // writes the stage's meta, arms the full barrier and issues the TMA
         // copies.  No warp-wide collectives sit in the loop.
-        if (lane == 0) {
+        // Coded cache: the whole warp runs it in step and an elected lane
+        // issues (a stage takes 12 copies, or 24 at head dim 64, which cost a
+        // diverged lane 100 clocks each: more than the stage's time in HBM).
+        const bool lead = !kCoded || lane == 0;
+        auto copy_tile = [](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+            if constexpr (kCoded) elect_tma_2d(dst, map, x, y, bar);
+            else tma_load_2d(dst, map, x, y, bar);
+        };
+        auto copy_bulk = [](uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+            if constexpr (kCoded) elect_bulk_load(dst, src, bytes, bar);
+            else bulk_load(dst, src, bytes, bar);
+        };
+        auto wait_for = [](uint32_t bar, uint32_t parity) {
+            if constexpr (kCoded) return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+            else return mbar_wait(bar, parity);
+        };
+        if (kCoded || lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             int islot = 0;
@@ -992,7 +1011,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             bool first_item = true;
             auto issue_q = [&](uint32_t qdst, const uint8_t* qsrc, uint32_t fb) {
                 if constexpr (C::kQRow == C::kQSrcRow) {
-                    bulk_load(qdst, qsrc, g * C::kQRow, fb);
+                    copy_bulk(qdst, qsrc, g * C::kQRow, fb);
                 } else {
                     for (int h = 0; h < g; ++h)
                         bulk_load(qdst + h * C::kQRow, qsrc + h * C::kQSrcRow, C::kQSrcRow, fb);
@@ -1011,7 +1030,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 q_pending = false;
             };
             while (ok && !aborted) {
-                if (!mbar_wait(bar_ifull + 8 * islot, iphase)) { ok = false; break; }
+                if (!wait_for(bar_ifull + 8 * islot, iphase)) { ok = false; break; }
                 const uint8_t* slotp = item_q + islot * C::kItemBytes;
                 const int4 d0 = reinterpret_cast<const int4*>(slotp)[0];
                 const int4 d1 = reinterpret_cast<const int4*>(slotp)[1];
@@ -1038,7 +1057,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                     const int np = min(P, npg - j);
                     if (!dep && (pre_stages >= S || first_page + j + np - 1 >= last_page)) resolve();
                     if (aborted) break;
-                    if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1)) { ok = false; break; }
+                    if (!wait_for(bar_empty + 8 * stage, phase ^ 1)) { ok = false; break; }
                     if (hold) {
                         // test hook: this stage is never armed nor filled
                         hold = false;
@@ -1061,27 +1080,30 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                             flags |= 1 << (kValidShift + p);
                             bytes += 2 * C::kTileBytes + C::kScaleBytes;
                         } else if (p < np) {
-                            set_error(ctrl, kErrBadPage);
+                            if (lead) set_error(ctrl, kErrBadPage);
                         }
                     }
                     int4* mp = reinterpret_cast<int4*>(meta + stage);
-                    mp[0] = make_int4(row, kvh, nch, slot);
-                    mp[1] = make_int4(t_lo, t_hi, flags, chunk);
-                    mbar_arrive_expect_tx(fb, bytes);
+                    if (lead) {
+                        mp[0] = make_int4(row, kvh, nch, slot);
+                        mp[1] = make_int4(t_lo, t_hi, flags, chunk);
+                        mbar_arrive_expect_tx(fb, bytes);
+                    }
+                    __syncwarp(kCoded ? 0xffffffffu : 1u);
                     #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         if (flags & (1 << (kValidShift + p))) {
                             const int y = pidv[p] * Hk * kPageSize + y_kv;
                             #pragma unroll
                             for (int bx = 0; bx < C::kBoxes; ++bx) {
-                                tma_load_2d(dst + p * C::kTileBytes + bx * C::kBoxBytes, km, bx * C::kBoxCols, y, fb);
-                                tma_load_2d(dst + (P + p) * C::kTileBytes + bx * C::kBoxBytes, vm, bx * C::kBoxCols, y,
-                                            fb);
+                                copy_tile(dst + p * C::kTileBytes + bx * C::kBoxBytes, km, bx * C::kBoxCols, y, fb);
+                                copy_tile(dst + (P + p) * C::kTileBytes + bx * C::kBoxBytes, vm, bx * C::kBoxCols, y,
+                                          fb);
                             }
                             if constexpr (kCoded) {
                                 const uint32_t sdst = sbase + C::kOffScale + (stage * P + p) * C::kScaleBytes;
-                                bulk_load(sdst, a.k_scale + y, kPageSize * 4, fb);
-                                bulk_load(sdst + kPageSize * 4, a.v_scale + y, kPageSize * 4, fb);
+                                copy_bulk(sdst, a.k_scale + y, kPageSize * 4, fb);
+                                copy_bulk(sdst + kPageSize * 4, a.v_scale + y, kPageSize * 4, fb);
                             }
                         }
                     }
@@ -1100,26 +1122,29 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                     armed |= 1u << stage;
                     armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
                     issued += np;
-                    *s_issued = issued;
+                    if (lead) *s_issued = issued;
                     if (++stage == S) { stage = 0; phase ^= 1; }
                 }
                 if (!ok || aborted) break;
                 resolve();   // later items come after the wait
                 if (aborted) break;
-                mbar_arrive(bar_iempty + 8 * islot);
+                __syncwarp(kCoded ? 0xffffffffu : 1u);
+                if (lead) mbar_arrive(bar_iempty + 8 * islot);
                 if (++islot == kItemSlots) { islot = 0; iphase ^= 1; }
             }
             if (ok && !aborted) {
                 // Terminator: the next stage carries no data, only the end flag.
-                if (mbar_wait(bar_empty + 8 * stage, phase ^ 1)) {
-                    meta[stage].flags = kTerm;
-                    mbar_arrive(bar_full + 8 * stage);
+                if (wait_for(bar_empty + 8 * stage, phase ^ 1)) {
+                    if (lead) {
+                        meta[stage].flags = kTerm;
+                        mbar_arrive(bar_full + 8 * stage);
+                    }
                 } else {
                     ok = false;
                 }
             }
             if (!ok || aborted) {
-                if (!ok) fail_timeout(ctrl);
+                if (!ok && lead) fail_timeout(ctrl);
                 resolve();   // issues a pending query copy, so that its stage completes
                 // Let the copies in flight land before the CTA's shared memory
                 // goes away (after a refused plan the consumers have left and
