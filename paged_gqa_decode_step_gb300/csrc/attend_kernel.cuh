@@ -311,27 +311,28 @@ struct Consumer<__nv_bfloat16, D, G, Uncoded> {
 // so that neither K's nor V's reads meet in a bank.
 //
 //   scores   c . q, times the query's factor and the token's K scale: f32
-//   weights  e^s, times the token's V scale, as f16 for the PV product
+//   weights  e^(s - m), times the token's V scale, as f16 for the PV product
 //
-// V scales differ by token and may differ by orders of magnitude, so the
-// weights carry a running maximum of their own (w, of s plus the scale's
-// exponent), apart from the softmax's (m); the sums meet in stash().  Both
-// maxima are raised lazily, when some score passes them by 2^kLazyCoded (one
-// vote instead of the reductions), and the weights are kept 2^kBias above
-// the usual so that f16 holds 11 bits of all but the smallest: at most
-// 2^(kLazyCoded + kBias + 1) = 2^15, under f16's largest.
+// The V scales enter relative to a power of two, r = 2^(kBias - e) with e the
+// exponent of the largest V scale the warp has seen: O is kept in units of
+// 1 / r.  m and e are raised lazily, when a score passes m by more than
+// kLazyCoded or a scale passes 2^(e + 1) (one vote for both instead of the
+// reductions), so a weight stays under 2^(kLazyCoded + kBias + 1) = 2^15 and
+// f16 holds 11 bits of all weights down to 2^-22 of the largest possible.
 // For f32 inputs the products take a second pass with what f16 rounded off
 // the query and off the weights.
 template <typename T, int D, int G, typename Code>
 struct Consumer {
     static constexpr bool kSplit = sizeof(T) == 4;
     static constexpr int KS = D / 16;
-    static constexpr float kLazyCoded = 6.f, kBias = 8.f;
+    static constexpr float kLazyCoded = 6.f;
+    static constexpr int kBias = 8;
+    static constexpr float kRMax = 1.7014118e38f;   // 2^127: scales down to 2^(kBias - 127) count in full
     uint32_t qf[KS][2];
     uint32_t ql[kSplit ? KS : 1][2];
     float o[KS][4];
     float f0, f1;                         // factors of heads 2*(lane%4) and +1
-    float m0, m1, w0, w1, l0, l1;
+    float m0, m1, l0, l1, r;
 
     // Token of the tile's row i (0..7; row i + 8 holds token perm(i) + 8).
     // K: rows 2j and 2j + 1 are read together (D 128: their 16-byte chunks
@@ -371,8 +372,9 @@ struct Consumer {
         f1 = lds_f32(qbuf + (2 * t + 1) * kRow + (kSplit ? 4 : 2) * D);
         #pragma unroll
         for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        m0 = m1 = w0 = w1 = kNegBig;
+        m0 = m1 = kNegBig;
         l0 = l1 = 0.f;
+        r = kRMax;
     }
 
     // One page's tokens tok0 .. tok0 + 15; scales: the page's 64 K scales, then 64 V scales.
@@ -421,61 +423,68 @@ struct Consumer {
         }
         const bool va = ta >= t_lo && ta < t_hi, vb = tb >= t_lo && tb < t_hi;
         const float ksa = lds_f32(scales + ta * 4), ksb = lds_f32(scales + tb * 4);
-        // V scale = mantissa * 2^exponent
-        const uint32_t vsa = __float_as_uint(lds_f32(scales + 256 + ta * 4));
-        const uint32_t vsb = __float_as_uint(lds_f32(scales + 256 + tb * 4));
-        // (the exponent's bits under 2^23's read 2^23 + exponent)
-        const float ea = __uint_as_float(0x4b000000u | vsa >> 23) - (8388608.f + 127.f);
-        const float eb = __uint_as_float(0x4b000000u | vsb >> 23) - (8388608.f + 127.f);
-        // (an infinity or a NaN, exponent 255, makes the token's weight a NaN)
-        const float ma = __uint_as_float((vsa >> 23) == 255 ? 0x7fc00000u : (vsa & 0x7fffffu) | 0x3f800000u);
-        const float mb = __uint_as_float((vsb >> 23) == 255 ? 0x7fc00000u : (vsb & 0x7fffffu) | 0x3f800000u);
-        const float s0 = va ? (c[0] + c2[0]) * (f0 * ksa) : -INFINITY;
-        const float s1 = va ? (c[1] + c2[1]) * (f1 * ksa) : -INFINITY;
-        const float s2 = vb ? (c[2] + c2[2]) * (f0 * ksb) : -INFINITY;
-        const float s3 = vb ? (c[3] + c2[3]) * (f1 * ksb) : -INFINITY;
-        const float x0 = fmaxf(s0, s2), x1 = fmaxf(s1, s3);
-        const float y0 = fmaxf(s0 + ea, s2 + eb), y1 = fmaxf(s1 + ea, s3 + eb);
-        const bool over = x0 > m0 + kLazyCoded || x1 > m1 + kLazyCoded || y0 > w0 + kLazyCoded || y1 > w1 + kLazyCoded;
-        if (__any_sync(0xffffffffu, over)) {
-            float r[4] = {x0, x1, y0, y1};
-            #pragma unroll
-            for (int sh = 4; sh < 32; sh <<= 1)
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) r[k] = fmaxf(r[k], __shfl_xor_sync(0xffffffffu, r[k], sh));
-            const float nm0 = fmaxf(m0, r[0]), nm1 = fmaxf(m1, r[1]), nw0 = fmaxf(w0, r[2]), nw1 = fmaxf(w1, r[3]);
-            l0 *= exp2_approx(m0 - nm0);
-            l1 *= exp2_approx(m1 - nm1);
-            const float al0 = exp2_approx(w0 - nw0), al1 = exp2_approx(w1 - nw1);
-            m0 = nm0; m1 = nm1; w0 = nw0; w1 = nw1;
-            #pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                o[i][0] *= al0; o[i][1] *= al1; o[i][2] *= al0; o[i][3] *= al1;
-            }
-        }
-        l0 += exp2_approx(s0 - m0) + exp2_approx(s2 - m0);
-        l1 += exp2_approx(s1 - m1) + exp2_approx(s3 - m1);
-        const float b0 = kBias - w0, b1 = kBias - w1;
-        const float p0 = exp2_approx(s0 + ea + b0) * ma, p1 = exp2_approx(s1 + ea + b1) * ma;
-        const float p2 = exp2_approx(s2 + eb + b0) * mb, p3 = exp2_approx(s3 + eb + b1) * mb;
-        // an invisible token's scales may hold anything: its weight is 0
-        const uint32_t pa = va ? pack_f16x2(p0, p1) : 0u, pb = vb ? pack_f16x2(p2, p3) : 0u;
-        const uint32_t q0 = movmatrix_trans(pa), q1 = movmatrix_trans(pb);
-        uint32_t r0 = 0, r1 = 0;
-        if constexpr (kSplit) {
-            const float2 xa = __half22float2(*reinterpret_cast<const __half2*>(&pa));
-            const float2 xb = __half22float2(*reinterpret_cast<const __half2*>(&pb));
-            r0 = movmatrix_trans(va ? pack_f16x2(p0 - xa.x, p1 - xa.y) : 0u);
-            r1 = movmatrix_trans(vb ? pack_f16x2(p2 - xb.x, p3 - xb.y) : 0u);
-        }
+        float vsa = lds_f32(scales + 256 + ta * 4), vsb = lds_f32(scales + 256 + tb * 4);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] += c2[i];
+        const float k0 = f0 * ksa, k1 = f1 * ksa, k2 = f0 * ksb, k3 = f1 * ksb;
+        float x0 = fmaf(c[0], k0, -m0), x1 = fmaf(c[1], k1, -m1), x2 = fmaf(c[2], k2, -m0), x3 = fmaf(c[3], k3, -m1);
         if (partial) {
-            // codes of invisible tokens may be anything (an e4m3 NaN among them)
+            // an invisible token's scales and codes may be anything (an e4m3 NaN among them)
+            x0 = va ? x0 : -INFINITY;
+            x1 = va ? x1 : -INFINITY;
+            x2 = vb ? x2 : -INFINITY;
+            x3 = vb ? x3 : -INFINITY;
+            vsa = va ? vsa : 0.f;
+            vsb = vb ? vsb : 0.f;
             #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const bool vis = v_tok[k] >= t_lo && v_tok[k] < t_hi;
                 #pragma unroll
                 for (int j = 0; j < kVWords; ++j) vw[k][j] = vis ? vw[k][j] : 0u;
             }
+        }
+        if (__any_sync(0xffffffffu, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) > kLazyCoded ||
+                                        fmaxf(vsa, vsb) * r >= (float)(2 << kBias))) {
+            float y[3];
+            y[0] = fmaxf(va ? c[0] * k0 : -INFINITY, vb ? c[2] * k2 : -INFINITY);
+            y[1] = fmaxf(va ? c[1] * k1 : -INFINITY, vb ? c[3] * k3 : -INFINITY);
+            y[2] = fmaxf(vsa, vsb);
+            #pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1)
+                #pragma unroll
+                for (int k = 0; k < 3; ++k) y[k] = fmaxf(y[k], __shfl_xor_sync(0xffffffffu, y[k], sh));
+            const float n0 = fmaxf(m0, y[0]), n1 = fmaxf(m1, y[1]);
+            // 2^(kBias - exponent of the largest scale), at most 2^127
+            const int e = min(max((int)(__float_as_uint(y[2]) >> 23), kBias), 253);
+            const float rn = fminf(r, __uint_as_float((uint32_t)(254 + kBias - e) << 23));
+            const float al0 = exp2_approx(m0 - n0), al1 = exp2_approx(m1 - n1), ar = rn / r;
+            l0 *= al0;
+            l1 *= al1;
+            #pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                o[i][0] *= al0 * ar; o[i][1] *= al1 * ar; o[i][2] *= al0 * ar; o[i][3] *= al1 * ar;
+            }
+            m0 = n0;
+            m1 = n1;
+            r = rn;
+            x0 = va ? fmaf(c[0], k0, -m0) : -INFINITY;
+            x1 = va ? fmaf(c[1], k1, -m1) : -INFINITY;
+            x2 = vb ? fmaf(c[2], k2, -m0) : -INFINITY;
+            x3 = vb ? fmaf(c[3], k3, -m1) : -INFINITY;
+        }
+        const float e0 = exp2_approx(x0), e1 = exp2_approx(x1), e2 = exp2_approx(x2), e3 = exp2_approx(x3);
+        l0 += e0 + e2;
+        l1 += e1 + e3;
+        const float ga = vsa * r, gb = vsb * r;
+        const float p0 = e0 * ga, p1 = e1 * ga, p2 = e2 * gb, p3 = e3 * gb;
+        const uint32_t pa = pack_f16x2(p0, p1), pb = pack_f16x2(p2, p3);
+        const uint32_t q0 = movmatrix_trans(pa), q1 = movmatrix_trans(pb);
+        uint32_t r0 = 0, r1 = 0;
+        if constexpr (kSplit) {
+            const float2 xa = __half22float2(*reinterpret_cast<const __half2*>(&pa));
+            const float2 xb = __half22float2(*reinterpret_cast<const __half2*>(&pb));
+            r0 = movmatrix_trans(pack_f16x2(p0 - xa.x, p1 - xa.y));
+            r1 = movmatrix_trans(pack_f16x2(p2 - xb.x, p3 - xb.y));
         }
         // O^T += V^T P^T: m-tile 2 j + u holds dimensions (D / 8) gr + 4 j +
         // 2 u (row gr) and + 1 (row gr + 8)
@@ -505,15 +514,14 @@ struct Consumer {
             ml[h0] = make_float2(m0, s0);
             ml[h0 + 1] = make_float2(m1, s1);
         }
-        // from units of 2^(w - kBias) to the softmax's 2^m
-        const float u0 = exp2_approx(w0 - kBias - m0), u1 = exp2_approx(w1 - kBias - m1);
+        const float u = 1.f / r;
         #pragma unroll
         for (int mt = 0; mt < KS; mt += 2) {
             const int d = (D / 8) * gr + 2 * mt;
             *reinterpret_cast<float4*>(ow + h0 * (D + 4) + d) =
-                make_float4(o[mt][0] * u0, o[mt][2] * u0, o[mt + 1][0] * u0, o[mt + 1][2] * u0);
+                make_float4(o[mt][0] * u, o[mt][2] * u, o[mt + 1][0] * u, o[mt + 1][2] * u);
             *reinterpret_cast<float4*>(ow + (h0 + 1) * (D + 4) + d) =
-                make_float4(o[mt][1] * u1, o[mt][3] * u1, o[mt + 1][1] * u1, o[mt + 1][3] * u1);
+                make_float4(o[mt][1] * u, o[mt][3] * u, o[mt + 1][1] * u, o[mt + 1][3] * u);
         }
     }
 };
@@ -1315,23 +1323,31 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         {
             constexpr int P = C::kPagesPerStage;
             const int np = (mt.flags >> kPagesShift) & 15;
-            #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                if (kCoded && (p & 1) != warp >> 2) continue;   // coded: four warps per page, every other page
-                if (p < np && (mt.flags & (1 << (kValidShift + p)))) {
+            if constexpr (kCoded) {
+                // four warps per page, every other page; rolled, so that one
+                // copy of the page's code stays in the instruction cache
+                #pragma unroll 1
+                for (int p = warp >> 2; p < np; p += kCW / 4) {
+                    if (!(mt.flags & (1 << (kValidShift + p)))) continue;
                     const int lo_p = mt.t_lo - p * kPageSize, hi_p = mt.t_hi - p * kPageSize;
-                    const bool partial = lo_p > 0 || hi_p < kPageSize;
-                    if constexpr (kCoded)
-                        cs.page(kbase + p * C::kTileBytes, kbase + (P + p) * C::kTileBytes,
-                                sbase + C::kOffScale + (stage * P + p) * C::kScaleBytes, 16 * (warp & 3), lane, lo_p,
-                                hi_p, partial);
-                    else if constexpr (sizeof(T) == 2)
-                        cs.page(kbase + p * C::kTileBytes, kbase + (P + p) * C::kTileBytes, warp, lane, lo_p, hi_p,
-                                partial, a.scale_log2);
-                    else
-                        cs.page(smem + stage * C::kStageBytes + p * C::kTileBytes,
-                                smem + stage * C::kStageBytes + (P + p) * C::kTileBytes, warp, lane, lo_p, hi_p, partial,
-                                a.scale_log2);
+                    cs.page(kbase + p * C::kTileBytes, kbase + (P + p) * C::kTileBytes,
+                            sbase + C::kOffScale + (stage * P + p) * C::kScaleBytes, 16 * (warp & 3), lane, lo_p, hi_p,
+                            lo_p > 0 || hi_p < kPageSize);
+                }
+            } else {
+                #pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    if (p < np && (mt.flags & (1 << (kValidShift + p)))) {
+                        const int lo_p = mt.t_lo - p * kPageSize, hi_p = mt.t_hi - p * kPageSize;
+                        const bool partial = lo_p > 0 || hi_p < kPageSize;
+                        if constexpr (sizeof(T) == 2)
+                            cs.page(kbase + p * C::kTileBytes, kbase + (P + p) * C::kTileBytes, warp, lane, lo_p, hi_p,
+                                    partial, a.scale_log2);
+                        else
+                            cs.page(smem + stage * C::kStageBytes + p * C::kTileBytes,
+                                    smem + stage * C::kStageBytes + (P + p) * C::kTileBytes, warp, lane, lo_p, hi_p,
+                                    partial, a.scale_log2);
+                    }
                 }
             }
         }
