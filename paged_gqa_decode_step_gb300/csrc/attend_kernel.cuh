@@ -774,7 +774,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_full + 8 * s, kCoded ? 33 : 1);   // coded: each producer lane's scales, too
             mbar_init(bar_empty + 8 * s, kCW);
         }
         *s_issued = 0;
@@ -981,8 +981,8 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         // writes the stage's meta, arms the full barrier and issues the TMA
         // copies.  No warp-wide collectives sit in the loop.
         // Coded cache: the whole warp runs it in step and an elected lane
-        // issues (a stage takes 12 copies, or 24 at head dim 64, which cost a
-        // diverged lane 100 clocks each: more than the stage's time in HBM).
+        // issues (a diverged lane took 100 clocks per copy, a stage's time in
+        // HBM for its 12 to 24); the scales come as one 16-byte copy per lane.
         const bool lead = !kCoded || lane == 0;
         auto copy_tile = [](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
             if constexpr (kCoded) elect_tma_2d(dst, map, x, y, bar);
@@ -1086,7 +1086,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                         pidv[p] = p < np ? pids[j + p] : -1;
                         if (p < np && pidv[p] >= 0 && pidv[p] < a.num_pages) {
                             flags |= 1 << (kValidShift + p);
-                            bytes += 2 * C::kTileBytes + C::kScaleBytes;
+                            bytes += 2 * C::kTileBytes;
                         } else if (p < np) {
                             if (lead) set_error(ctrl, kErrBadPage);
                         }
@@ -1109,12 +1109,13 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                                           fb);
                             }
                             if constexpr (kCoded) {
-                                const uint32_t sdst = sbase + C::kOffScale + (stage * P + p) * C::kScaleBytes;
-                                copy_bulk(sdst, a.k_scale + y, kPageSize * 4, fb);
-                                copy_bulk(sdst + kPageSize * 4, a.v_scale + y, kPageSize * 4, fb);
+                                // 64 K scales and 64 V scales, 16 bytes a lane
+                                const float* src = (lane < 16 ? a.k_scale : a.v_scale) + y + (lane & 15) * 4;
+                                cp_async16(sbase + C::kOffScale + (stage * P + p) * C::kScaleBytes + lane * 16, src);
                             }
                         }
                     }
+                    if constexpr (kCoded) cp_async_arrive(fb);
                     if (j == 0) {
                         const uint32_t qdst = sbase + C::kOffQ + stage * C::kQBytes;
                         if (dep) {
@@ -1143,10 +1144,10 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             if (ok && !aborted) {
                 // Terminator: the next stage carries no data, only the end flag.
                 if (wait_for(bar_empty + 8 * stage, phase ^ 1)) {
-                    if (lead) {
-                        meta[stage].flags = kTerm;
-                        mbar_arrive(bar_full + 8 * stage);
-                    }
+                    if (lead) meta[stage].flags = kTerm;
+                    __syncwarp(kCoded ? 0xffffffffu : 1u);
+                    mbar_arrive(bar_full + 8 * stage);
+                    if (kCoded && lead) mbar_arrive(bar_full + 8 * stage);
                 } else {
                     ok = false;
                 }
