@@ -837,13 +837,20 @@ static pdattn_status make_code_map(CUtensorMap* map, const void* codes, const pd
     return PDATTN_OK;
 }
 
-// Decode: the split plan's regions, then the coded query rows (f16, with the
-// remainder row for f32 inputs, and 16 bytes for the factor).
+// Decode: merge counters, two partial slots per CTA (attend_kernel.cuh) and the
+// coded query rows (f16, with the remainder row for f32 inputs, and 16 bytes
+// for the factor).
 static int coded_q_row(const pdattn_params* p) { return (p->dtype == PDATTN_F32 ? 4 : 2) * p->head_dim + 16; }
 
 static WsLayout coded_layout(const pdattn_params* p, int grid) {
-    WsLayout L = ws_layout(p->rows, p->heads, p->kv_heads, p->head_dim, p->pages_per_row, 0, p->chunk_pages, grid);
-    L.total = align256(L.q_rot + (size_t)p->rows * p->heads * coded_q_row(p));
+    const size_t rows = p->rows, g = p->heads / p->kv_heads, slots = 2 * (size_t)grid;
+    WsLayout L = {};
+    size_t off = 256;
+    L.merge_cnt = off; off = align256(off + sizeof(int) * rows * p->kv_heads);
+    L.part_ml = off; off = align256(off + sizeof(float2) * slots * g);
+    L.part_o = off; off = align256(off + sizeof(float) * slots * g * p->head_dim);
+    L.q_rot = off; off = align256(off + rows * p->heads * coded_q_row(p));
+    L.total = off;
     return L;
 }
 
@@ -903,18 +910,13 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
     CUtensorMap km, vm;
     if ((s = make_code_map(&km, cache->k, p)) != PDATTN_OK) return s;
     if ((s = make_code_map(&vm, cache->v, p)) != PDATTN_OK) return s;
-    PrepArgs pa = prep_args(p, positions, table, ws, L, grid);
-    pa.do_plan = 1;
-    int n = 0;
-    cudaError_t e = launch_prep(pa, p->dtype, (cudaStream_t)stream, &n);
-    if (e != cudaSuccess) return cuda_fail(e, "plan launch");
     CodeArgs ca = code_args(p, cache, p->rows, k_new, v_new, positions, ws);
     ca.q = q;
     ca.table = table;
-    ca.after_plan = 1;
+    ca.merge_cnt = reinterpret_cast<int*>(ws + L.merge_cnt);
     ca.q_row_bytes = coded_q_row(p);
     ca.q_out = reinterpret_cast<uint8_t*>(ws + L.q_rot);
-    e = launch_code(ca, p->dtype, cache->code, (cudaStream_t)stream);
+    cudaError_t e = launch_code(ca, p->dtype, cache->code, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded rope/write launch");
     AttendArgs aa = {};
     aa.rows = p->rows;
@@ -925,7 +927,6 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
     aa.pages_per_row = p->pages_per_row;
     aa.num_pages = p->num_pages;
     aa.window = p->window;
-    aa.chunk_pages = p->chunk_pages;
     aa.q = ws + L.q_rot;
     aa.positions = positions;
     aa.table = table;
@@ -937,7 +938,7 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
     aa.v_scale = cache->v_scale;
     e = launch_attend_coded(aa, km, vm, p->dtype, cache->code, grid, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded attention launch");
-    g_launches = n + 2;
+    g_launches = 2;
     return PDATTN_OK;
 }
 

@@ -58,6 +58,9 @@ enum : int { kFirst = 1, kLast = 2, kTerm = 8 };
 struct Meta {
     int row, kvh, nch, slot, t_lo, t_hi, flags, chunk;
 };
+// An item's nch field (coded decode): pieces of one item that do not fit a
+// queue slot carry on the one before and are carried on by the next.
+constexpr int kCarriesOn = 1 << 30, kCarriedOn = 1 << 29, kNchMask = (1 << 29) - 1;
 constexpr int kPagesShift = 8;
 constexpr int kValidShift = 16;
 
@@ -96,6 +99,9 @@ struct Cfg {
     static constexpr int kQHeads = kElem == 2 || kCoded ? kMaxGroup : G;
     static constexpr int kQBytes = kQHeads * kQRow;
     static constexpr int kORow = D + 4;                          // padded head row of a stashed output
+    // Coded decode's shares: what an item's start, merge and part-filled last
+    // stage cost, in pages.
+    static constexpr int kItemUnits = 3;
     static constexpr int kOffQ = kStages * kStageBytes;
     static constexpr int kWarpQBytes = (kElem == 4 && G > 1 && !kCoded) ? kCW * kQBytes : 0;  // f32: private copies
     static constexpr int kWarpPBytes = (kElem == 4 && !kCoded) ? kCW * G * (64 / kCW) * 4 : 0;   // f32: p buffers
@@ -824,10 +830,13 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     const int g = a.group, Hk = a.kv_heads;
     const int nf = first_wave(a.rows, Hk, gridDim.x);
 
+    // Coded decode has no planner: every CTA finds its own share of the work
+    // (below) and the coding launch clears the merge counters.
     // The plan header in one round trip: four independent 16-byte loads
     // (fields status .. test_hold; see Ctrl), checked in registers.  Only
     // after the wait for the preceding launch (the planner's).
     auto read_plan = [&](int* n_items, int* chunk_pages) -> bool {
+        if constexpr (kCoded) return true;
         const int4 h0 = __ldcg(reinterpret_cast<const int4*>(ctrl));
         const int4 h1 = __ldcg(reinterpret_cast<const int4*>(ctrl) + 1);
         const int4 h2 = __ldcg(reinterpret_cast<const int4*>(ctrl) + 2);
@@ -871,6 +880,82 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             *pid0 = lane < npg ? __ldg(trow + lane) : -1;
             *pid1 = lane + 32 < npg ? __ldg(trow + lane + 32) : -1;
         };
+        if constexpr (kCoded) {
+            // Static shares: the (row, kv head) pairs in order, each as many
+            // units as it has pages plus U for its start and merge, cut into
+            // one equal run of units per CTA.  Unit x belongs to CTA
+            // ((x + 1) G - 1) / W, so every CTA knows how many others share a
+            // pair.  A CTA's partial results are at most two: of a pair it
+            // starts (slot 2 b + 1) and of one it carries on (slot 2 b).  All
+            // from the call's inputs: no wait, no plan launch (5 us) and no
+            // work cursor; the shares differ by one page.
+            const int R = a.rows, max_pos = a.pages_per_row * kPageSize;
+            const long long b = blockIdx.x;
+            constexpr int U = C::kItemUnits;
+            auto row_at = [&](int v, int* pos, int* lo) -> int {
+                *pos = v < R ? __ldg(a.positions + v) : -1;
+                if (*pos < 0 || *pos >= max_pos) return 0;
+                *lo = row_lo(*pos, a.window);
+                return *pos / kPageSize - *lo / kPageSize + 1;
+            };
+            int pos = -1, lo = 0;
+            long long W = 0;
+            #pragma unroll 4
+            for (int v = lane; v < R; v += 32) {
+                const int n = row_at(v, &pos, &lo);
+                W += n ? n + U : 0;
+            }
+            #pragma unroll
+            for (int sh = 16; sh > 0; sh >>= 1) W += __shfl_xor_sync(0xffffffffu, W, sh);
+            W *= Hk;
+            const long long G = min((long long)gridDim.x, W / (U + 1));   // fewer CTAs than pages: each has a page
+            const long long x0 = b < G ? b * W / G : W, x1 = b < G ? (b + 1) * W / G : 0;
+            if (lane == 0) *s_early = 1;   // published by the item barrier's arrival
+            // Shared pairs go first, so that their merges run under the pairs
+            // the CTA has to itself.
+            for (int whole = 0; whole < 2; ++whole) {
+                long long before = 0;          // units of the rows before, per kv head
+                for (int r0 = 0; r0 < R && before * Hk < x1 && ok; r0 += 32) {
+                    const int n = row_at(r0 + lane, &pos, &lo);
+                    int upto = n ? n + U : 0;
+                    #pragma unroll
+                    for (int sh = 1; sh < 32; sh <<= 1) {
+                        const int up = __shfl_up_sync(0xffffffffu, upto, sh);
+                        if (lane >= sh) upto += up;
+                    }
+                    const long long start = (before + upto - (n ? n + U : 0)) * Hk;
+                    uint32_t mine = __ballot_sync(0xffffffffu, n > 0 && start < x1 && start + (long long)(n + U) * Hk > x0);
+                    before += __shfl_sync(0xffffffffu, upto, 31);
+                    while (mine && ok) {
+                        const int l = __ffs(mine) - 1;
+                        mine &= mine - 1;
+                        const int row = r0 + l, nr = __shfl_sync(0xffffffffu, n, l), rpos = __shfl_sync(0xffffffffu, pos, l);
+                        const int rlo = __shfl_sync(0xffffffffu, lo, l);
+                        const long long rs = __shfl_sync(0xffffffffu, start, l);
+                        for (int h = x0 > rs ? (int)((x0 - rs) / (nr + U)) : 0; h < Hk && ok; ++h) {
+                            const long long u0 = rs + (long long)h * (nr + U) + U;   // unit of the pair's first page
+                            if (u0 >= x1) break;
+                            const int p0 = (int)(max(x0, u0) - u0), p1 = (int)(min(x1, u0 + nr) - u0);
+                            if (p0 >= p1 || (p1 - p0 == nr) != (whole == 1)) continue;
+                            const int b0 = (int)(((u0 + 1) * G - 1) / W), b1 = (int)(((u0 + nr) * G - 1) / W);
+                            for (int q = p0; q < p1 && ok; q += kChunkMax) {
+                                const int npg = min(kChunkMax, p1 - q), first = rlo / kPageSize + q;
+                                int pid0, pid1;
+                                load_pids(row, first, npg, &pid0, &pid1);
+                                ok = queue_item(make_int4(row, h << 16 | ((int)b - b0),
+                                                          (b1 - b0 + 1) | (q > p0 ? kCarriesOn : 0) |
+                                                              (q + npg < p1 ? kCarriedOn : 0),
+                                                          2 * (int)b + (p0 == 0 ? 1 : 0)),
+                                                make_int4(first, npg, rpos, rlo), pid0, pid1);
+                            }
+                        }
+                    }
+                }
+            }
+            if (ok) ok = queue_item(make_int4(0, 0, 0, 0), make_int4(0, -1, 0, 0), -1, -1);
+            if (!ok && lane == 0) fail_timeout(ctrl);
+            return;
+        }
         // The first-wave item comes from the call's inputs (positions, the
         // table), which no launch of this call writes: it is queued before
         // the wait, so that its pages load while the planner and the rope
@@ -1045,7 +1130,9 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 const int* pids = reinterpret_cast<const int*>(slotp + sizeof(ItemDesc));
                 const int npg = d1.y;
                 if (npg < 0) break;             // end of the work
-                const int row = d0.x, kvh = d0.y >> 16, chunk = d0.y & 0xffff, nch = d0.z, slot = d0.w;
+                const int row = d0.x, kvh = d0.y >> 16, chunk = d0.y & 0xffff, slot = d0.w;
+                const int nch = kCoded ? d0.z & kNchMask : d0.z;
+                const bool starts = !kCoded || !(d0.z & kCarriesOn), ends = !kCoded || !(d0.z & kCarriedOn);
                 const int first_page = d1.x, pos = d1.z, lo = d1.w;
                 const int y_kv = kvh * kPageSize;
                 const uint8_t* qsrc = static_cast<const uint8_t*>(a.q) + ((size_t)row * a.heads + kvh * g) * C::kQSrcRow;
@@ -1076,8 +1163,8 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                     const int t0 = (first_page + j) * kPageSize;
                     const int t_lo = max(lo, t0) - t0;
                     const int t_hi = min(pos, t0 + np * kPageSize - 1) - t0 + 1;
-                    int flags = (j == 0 ? kFirst : 0) | (j + np == npg ? kLast : 0) | (np << kPagesShift);
-                    uint32_t bytes = (j == 0 ? g * C::kQSrcRow : 0);
+                    int flags = (starts && j == 0 ? kFirst : 0) | (ends && j + np == npg ? kLast : 0) | (np << kPagesShift);
+                    uint32_t bytes = (starts && j == 0 ? g * C::kQSrcRow : 0);
                     const uint32_t fb = bar_full + 8 * stage;
                     const uint32_t dst = sbase + stage * C::kStageBytes;
                     int pidv[P];
@@ -1116,7 +1203,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                         }
                     }
                     if constexpr (kCoded) cp_async_arrive(fb);
-                    if (j == 0) {
+                    if (starts && j == 0) {
                         const uint32_t qdst = sbase + C::kOffQ + stage * C::kQBytes;
                         if (dep) {
                             issue_q(qdst, qsrc, fb);
@@ -1259,6 +1346,9 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 if (last) {
                     // out = sum_c e^(m_c - M) o_c / sum_c e^(m_c - M) l_c over the chunks
                     const int slot0 = slot - mt.chunk;
+                    auto slot_of = [&](int c) {
+                        return kCoded ? 2 * ((int)blockIdx.x - mt.chunk + c) + (c == 0 ? 1 : 0) : slot0 + c;
+                    };
                     for (int u = lane; u < g * D / 8; u += 32) {
                         const int j = u / (D / 8), d0 = (u % (D / 8)) * 8;
                         // one pass with a running maximum, so the loads of
@@ -1268,8 +1358,8 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                         for (int e = 0; e < 8; ++e) O[e] = 0.f;
                         #pragma unroll 4
                         for (int c = 0; c < nch; ++c) {
-                            const float2 ml = __ldcg(part_ml + (size_t)(slot0 + c) * g + j);
-                            const float4* src = reinterpret_cast<const float4*>(part_o + ((size_t)(slot0 + c) * g + j) * D + d0);
+                            const float2 ml = __ldcg(part_ml + (size_t)slot_of(c) * g + j);
+                            const float4* src = reinterpret_cast<const float4*>(part_o + ((size_t)slot_of(c) * g + j) * D + d0);
                             const float4 p0 = __ldcg(src), p1 = __ldcg(src + 1);
                             const float Mn = fmaxf(M, ml.x);
                             const float fa = exp2_approx(M - Mn), f = exp2_approx(ml.x - Mn);

@@ -124,6 +124,7 @@ struct CodeArgs {
     float* v_scale;
     uint8_t* q_out;
     float* q_factor;
+    int* merge_cnt;         // decode: [rows, kv_heads] counters to clear
     char* ws;
 };
 
