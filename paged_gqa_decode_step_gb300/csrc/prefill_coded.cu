@@ -458,13 +458,27 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             // (unrolled passes: 1.5 times the kernel's time).  Reading S twice
             // costs 30 clocks per chunk.
             float top = -INFINITY;
-            #pragma unroll 1
-            for (int q4 = 0; q4 < 4; ++q4) {
-                uint32_t x[32];
-                tmem_ld32(s_addr + 32 * q4, x);
-                tmem_wait_ld();
-                if (state != 0) mask(x, q4);
-                top = fmaxf(top, max32(x));
+            if (state == 0) {
+                // the load brings the maximum along
+                #pragma unroll 1
+                for (int q2 = 0; q2 < 2; ++q2) {
+                    uint32_t x[32], y[32];
+                    float mx, my;
+                    tmem_ld32_max(s_addr + 64 * q2, x, mx);
+                    tmem_ld32_max(s_addr + 64 * q2 + 32, y, my);
+                    tmem_wait_ld();
+                    asm volatile("" : "+f"(mx), "+f"(my));   // no use of them ahead of the wait
+                    top = fmax3(top, mx, my);
+                }
+            } else {
+                #pragma unroll 1
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    uint32_t x[32];
+                    tmem_ld32(s_addr + 32 * q4, x);
+                    tmem_wait_ld();
+                    mask(x, q4);
+                    top = fmaxf(top, max32(x));
+                }
             }
             const float mx = top * f;
             const bool need = mx > m_run + kRescale;
