@@ -935,9 +935,9 @@ __global__ void __launch_bounds__(kCpThreads, 1)
 // ---------------------------------------------------------------------------
 // Merge of split tiles: out = sum_c 2^(mu_c - M) o_c / sum_c 2^(mu_c - M) l_c
 // over a tile's pieces, with the sink's share of the denominator.  Block
-// (tile, kv head, 32 rows); a warp takes four rows, a lane D / 32 dimensions.
+// (tile, kv head, 8 rows); a warp takes a row, a lane D / 32 dimensions.
 // ---------------------------------------------------------------------------
-constexpr int kMergeRows = 32;
+constexpr int kMergeRows = 8;
 
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ CodedPrefillArgs ca) {
