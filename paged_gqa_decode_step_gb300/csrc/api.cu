@@ -1039,10 +1039,7 @@ pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_ca
     aa.slot_rows = L.slot_rows;
     aa.part_o = reinterpret_cast<float*>(ws + L.part_o);
     aa.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
-    // a split tile has at least two of the 4 grid / kv_heads pieces
-    const int most = (2 * grid + p->kv_heads - 1) / p->kv_heads;
-    const int merge_tiles = split ? (n_tokens < most ? n_tokens : most) : 0;
-    e = launch_prefill_coded(aa, qm, cache->code, grid, merge_tiles, (cudaStream_t)stream);
+    e = launch_prefill_coded(aa, qm, cache->code, grid, split, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded prefill attention launch");
     g_launches = split ? 4 : 3;
     return PDATTN_OK;

@@ -884,7 +884,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // Static shares: the (row, kv head) pairs in order, each as many
             // units as it has pages plus U for its start and merge, cut into
             // one equal run of units per CTA.  Unit x belongs to CTA
-            // ((x + 1) G - 1) / W, so every CTA knows how many others share a
+            // ((x + 1) ctas - 1) / W, so every CTA knows how many others share a
             // pair.  A CTA's partial results are at most two: of a pair it
             // starts (slot 2 b + 1) and of one it carries on (slot 2 b).  All
             // from the call's inputs: no wait, no plan launch (5 us) and no
@@ -908,8 +908,8 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             #pragma unroll
             for (int sh = 16; sh > 0; sh >>= 1) W += __shfl_xor_sync(0xffffffffu, W, sh);
             W *= Hk;
-            const long long G = min((long long)gridDim.x, W / (U + 1));   // fewer CTAs than pages: each has a page
-            const long long x0 = b < G ? b * W / G : W, x1 = b < G ? (b + 1) * W / G : 0;
+            const long long ctas = min((long long)gridDim.x, W / (U + 1));   // fewer CTAs than pages: each has a page
+            const long long x0 = b < ctas ? b * W / ctas : W, x1 = b < ctas ? (b + 1) * W / ctas : 0;
             if (lane == 0) *s_early = 1;   // published by the item barrier's arrival
             // Shared pairs go first, so that their merges run under the pairs
             // the CTA has to itself.
@@ -937,7 +937,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                             if (u0 >= x1) break;
                             const int p0 = (int)(max(x0, u0) - u0), p1 = (int)(min(x1, u0 + nr) - u0);
                             if (p0 >= p1 || (p1 - p0 == nr) != (whole == 1)) continue;
-                            const int b0 = (int)(((u0 + 1) * G - 1) / W), b1 = (int)(((u0 + nr) * G - 1) / W);
+                            const int b0 = (int)(((u0 + 1) * ctas - 1) / W), b1 = (int)(((u0 + nr) * ctas - 1) / W);
                             for (int q = p0; q < p1 && ok; q += kChunkMax) {
                                 const int npg = min(kChunkMax, p1 - q), first = rlo / kPageSize + q;
                                 int pid0, pid1;

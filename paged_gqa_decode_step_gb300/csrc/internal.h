@@ -190,10 +190,9 @@ cudaError_t launch_packed(const PrefillArgs& a, const CUtensorMap& q_map, const 
 
 // The tile list alone, with sub-tiles if a.split_grid > 0 (one block).
 cudaError_t launch_prefill_plan(const PrefillPrepArgs& a, cudaStream_t stream);
-// Attention of the units, then (merge_tiles > 0: an upper bound on split
-// tiles) the merge of split tiles.
-cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int code, int grid,
-                                 int merge_tiles, cudaStream_t stream);
+// Attention of the units, then, where tiles may be split, their merge.
+cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int code, int grid, bool merge,
+                                 cudaStream_t stream);
 cudaError_t launch_code(const CodeArgs& a, int dtype, int code, cudaStream_t stream);
 cudaError_t launch_read(const ReadArgs& a, int dtype, int code, cudaStream_t stream);
 

@@ -706,6 +706,9 @@ __global__ void __launch_bounds__(kCpThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
+    // Everything below reads what the planner and the coding launch wrote.
+    griddep_launch_dependents();
+    griddep_wait();
     const int Hk = a.kv_heads, g = a.group, Tq = a.tile_tokens / 2;
     const int n_units = (ctrl->magic == kPlanMagic ? ctrl->n_items : 0) * Hk;
     const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + ca.units);
@@ -934,25 +937,27 @@ __global__ void __launch_bounds__(kCpThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Merge of split tiles: out = sum_c 2^(mu_c - M) o_c / sum_c 2^(mu_c - M) l_c
-// over a tile's pieces, with the sink's share of the denominator.  Block
-// (tile, kv head, 8 rows); a warp takes a row, a lane D / 32 dimensions.
+// over a tile's pieces, with the sink's share of the denominator.  A warp
+// takes a row of a (tile, kv head), a lane D / 32 dimensions.
 // ---------------------------------------------------------------------------
-constexpr int kMergeRows = 8;
+constexpr int kMergeBlocksPerSm = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ CodedPrefillArgs ca) {
     constexpr int N = D / 32;
     const PrefillArgs& a = ca.a;
     const Ctrl* ctrl = reinterpret_cast<const Ctrl*>(a.ws + a.L.ctrl);
-    if (ctrl->n_items == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kvh = blockIdx.y, g = a.group;
+    griddep_wait();
+    const int lane = threadIdx.x & 31, g = a.group, Hk = a.kv_heads;
     const __nv_bfloat16* sinks = static_cast<const __nv_bfloat16*>(a.sinks);
-    for (int j = blockIdx.x; j < ctrl->max_items; j += gridDim.x) {   // tiles up to the last split one
+    // max_items: tiles up to the last split one (of 0 units none)
+    const int rows = ctrl->n_items == 0 ? 0 : ctrl->max_items * Hk * ca.slot_rows;
+    for (int w = blockIdx.x * 8 + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8) {
+        const int r = w % ca.slot_rows, kvh = w / ca.slot_rows % Hk, j = w / ca.slot_rows / Hk;
         const PfTile t = reinterpret_cast<const PfTile*>(a.ws + a.L.tiles)[j];
         const int nch = t.pad & 4095, slot0 = t.pad >> 12;
-        if (nch == 0) continue;
-        const int r1 = min((int)(blockIdx.z + 1) * kMergeRows, t.ntok * g);
-        for (int r = blockIdx.z * kMergeRows + warp; r < r1; r += 8) {
+        if (nch == 0 || r >= t.ntok * g) continue;
+        {
             const size_t at0 = ((size_t)slot0 * a.kv_heads + kvh) * ca.slot_rows + r;
             const size_t step = (size_t)a.kv_heads * ca.slot_rows;
             float M = -1.0e30f, L = 0.f, O[N] = {};
@@ -990,8 +995,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Code
 }
 
 template <int D, typename Code>
-cudaError_t launch_d(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int grid, int merge_tiles,
-                     cudaStream_t stream) {
+cudaError_t launch_d(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int grid, bool merge, cudaStream_t stream) {
     using C = CpCfg<D>;
     auto kern = prefill_coded_kernel<D, Code>;
     static int configured_mask = 0;   // bit per device id < 31
@@ -1003,23 +1007,35 @@ cudaError_t launch_d(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int g
         if (e != cudaSuccess) return e;
         if (dev < 31) __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
-    kern<<<grid, kCpThreads, C::kSmem, stream>>>(q_map, ca);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || merge_tiles == 0) return e;
-    const dim3 mg((unsigned)merge_tiles, (unsigned)ca.a.kv_heads, (unsigned)((ca.slot_rows + kMergeRows - 1) / kMergeRows));
-    merge_kernel<D><<<mg, 256, 0, stream>>>(ca);
-    return cudaGetLastError();
+    // Both are programmatic dependents: their start-up runs under the launch
+    // before, and they wait before they read what it wrote.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kCpThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, q_map, ca);
+    if (e != cudaSuccess || !merge) return e;
+    cfg.gridDim = dim3((unsigned)(grid * kMergeBlocksPerSm));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, merge_kernel<D>, ca);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int code, int grid,
-                                 int merge_tiles, cudaStream_t stream) {
+                                 bool merge, cudaStream_t stream) {
     if (ca.a.head_dim == 128)
-        return code == 0 ? launch_d<128, E4m3>(ca, q_map, grid, merge_tiles, stream)
-                         : launch_d<128, Int8>(ca, q_map, grid, merge_tiles, stream);
-    return code == 0 ? launch_d<64, E4m3>(ca, q_map, grid, merge_tiles, stream)
-                     : launch_d<64, Int8>(ca, q_map, grid, merge_tiles, stream);
+        return code == 0 ? launch_d<128, E4m3>(ca, q_map, grid, merge, stream)
+                         : launch_d<128, Int8>(ca, q_map, grid, merge, stream);
+    return code == 0 ? launch_d<64, E4m3>(ca, q_map, grid, merge, stream)
+                     : launch_d<64, Int8>(ca, q_map, grid, merge, stream);
 }
 
 }  // namespace pdattn

@@ -794,6 +794,163 @@ __device__ void split_tiles(const PrefillPrepArgs& a) {
     }
 }
 
+// Both steps at once for calls of up to kUnitTokens tokens: every intermediate
+// stays in registers and shared memory, so that the plan costs one round trip
+// to the inputs and its stores (in two steps over global memory the plan took
+// 10 us of a small call's 25).  Returns false, having written nothing, when
+// there are more than kUnitTiles tiles.
+constexpr int kUnitTokens = kChunk, kUnitTiles = 2 * kPrepThreads;
+
+__device__ bool build_units_small(const PrefillPrepArgs& a) {
+    __shared__ int s_warp[32];
+    __shared__ int s_last[kPrepThreads];
+    __shared__ int s_t0[kUnitTiles + 1], s_row[kUnitTiles], s_lo[kUnitTiles], s_hi[kUnitTiles];
+    __shared__ int s_off[kPfBuckets], s_order[kUnitTiles], s_sub[kUnitTiles + 1], s_slot[kUnitTiles];
+    __shared__ int s_bad, s_last_split;
+    const int tid = threadIdx.x, n = a.n_tokens, Tq = a.tile_tokens, max_pos = a.pages_per_row * kPageSize;
+    if (n > kUnitTokens) return false;
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
+    const int per = (n + kPrepThreads - 1) / kPrepThreads, i0 = tid * per;   // consecutive tokens per thread
+    int r[kPerThread], ps[kPerThread];
+    bool bad = false;
+    #pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const bool mine = k < per && i0 + k < n;
+        r[k] = mine ? __ldg(a.row_of + i0 + k) : -1;
+        ps[k] = mine ? __ldg(a.positions + i0 + k) : 0;
+        if (mine && (r[k] < 0 || r[k] >= a.rows || ps[k] < 0 || ps[k] >= max_pos || (a.rope_cos && ps[k] >= a.rope_len)))
+            bad = true;
+    }
+    int last = -1;
+    #pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        if (k < per && i0 + k < n) last = r[k];
+    s_last[tid] = last;
+    for (int b = tid; b < kPfBuckets; b += kPrepThreads) s_off[b] = 0;
+    if (tid == 0) { s_bad = 0; s_last_split = 0; }
+    __syncthreads();
+    if (bad) s_bad = 1;
+    // run starts, then tile starts
+    unsigned starts = 0;
+    int last_start = -1;
+    #pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        if (k >= per || i0 + k >= n) continue;
+        if (i0 + k == 0 || r[k] != (k ? r[k - 1] : s_last[tid - 1])) {
+            starts |= 1u << k;
+            last_start = i0 + k;
+        }
+    }
+    int total;
+    int rs = block_scan_excl<true>(last_start, -1, s_warp, &total);
+    unsigned tile_starts = 0;
+    #pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        if (k >= per || i0 + k >= n) continue;
+        if (starts >> k & 1) rs = i0 + k;
+        if ((i0 + k - rs) % Tq == 0) tile_starts |= 1u << k;
+    }
+    int n_tiles;
+    const int id0 = block_scan_excl<false>(__popc(tile_starts), 0, s_warp, &n_tiles);
+    if (n_tiles > kUnitTiles) return false;
+    int id = id0;
+    #pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        if (tile_starts >> k & 1) {
+            s_t0[id] = i0 + k;
+            s_row[id] = r[k];
+            s_lo[id] = INT_MAX;
+            s_hi[id] = -1;
+            ++id;
+        }
+    if (tid == 0) s_t0[n_tiles] = n;
+    __syncthreads();
+    int cur = id0 - 1;
+    #pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        if (k >= per || i0 + k >= n) continue;
+        if (tile_starts >> k & 1) ++cur;
+        const int pos = min(max(ps[k], 0), max_pos - 1);
+        atomicMin(&s_lo[cur], row_lo(pos, a.window));
+        atomicMax(&s_hi[cur], pos);
+    }
+    __syncthreads();
+    // counting sort by pages, longest first; two tiles (and buckets) per thread
+    auto pages = [&](int b) { return s_hi[b] / kPageSize - s_lo[b] / kPageSize + 1; };
+    int work = 0;
+    for (int b = tid; b < n_tiles; b += kPrepThreads) {
+        const int npg = pages(b);
+        work += (npg + 1) / 2;
+        atomicAdd(&s_off[kPfBuckets - 1 - min(npg, kPfBuckets - 1)], 1);
+    }
+    int blocks_all;
+    block_scan_excl<false>(work, 0, s_warp, &blocks_all);     // (also the barrier before s_off is read)
+    static_assert(kPfBuckets == 2 * kPrepThreads, "two buckets per thread");
+    const int h0 = s_off[2 * tid], h1 = s_off[2 * tid + 1];
+    const int off = block_scan_excl<false>(h0 + h1, 0, s_warp, &total);
+    s_off[2 * tid] = off;
+    s_off[2 * tid + 1] = off + h0;
+    __syncthreads();
+    for (int b = tid; b < n_tiles; b += kPrepThreads)
+        s_order[atomicAdd(&s_off[kPfBuckets - 1 - min(pages(b), kPfBuckets - 1)], 1)] = b;
+    __syncthreads();
+    // pieces, as split_tiles cuts them
+    const long long per_unit = 2ll * a.split_grid;
+    const long long Cb = max((blocks_all * (long long)a.kv_heads + per_unit - 1) / per_unit, (long long)kMinSplitBlocks);
+    auto pieces = [&](int at) {
+        return at < n_tiles ? (int)(((pages(s_order[at]) + 1) / 2 + Cb - 1) / Cb) : 0;
+    };
+    const int c0 = pieces(2 * tid), c1 = pieces(2 * tid + 1);
+    int n_sub, n_slot;
+    const int sub = block_scan_excl<false>(c0 + c1, 0, s_warp, &n_sub);
+    const int slot = block_scan_excl<false>((c0 > 1 ? c0 : 0) + (c1 > 1 ? c1 : 0), 0, s_warp, &n_slot);
+    PfTile* tiles = reinterpret_cast<PfTile*>(a.ws + a.L.tiles);
+    auto place = [&](int at, int c, int first_sub, int first_slot) {
+        s_sub[at] = first_sub;
+        s_slot[at] = first_slot;
+        if (c > 1) {
+            // what the merge needs of a split tile
+            const int b = s_order[at];
+            int4* dst = reinterpret_cast<int4*>(tiles + at);
+            dst[0] = make_int4(s_t0[b], s_t0[b + 1] - s_t0[b], s_row[b], 0);
+            dst[1] = make_int4(0, 0, 0, first_slot << 12 | c);
+            atomicMax(&s_last_split, at + 1);
+        } else if (at < n_tiles) {
+            reinterpret_cast<int4*>(tiles + at)[1] = make_int4(0, 0, 0, 0);
+        }
+    };
+    place(2 * tid, c0, sub, slot);
+    place(2 * tid + 1, c1, sub + c0, slot + (c0 > 1 ? c0 : 0));
+    __syncthreads();
+    PfTile* out = reinterpret_cast<PfTile*>(a.ws + a.units);
+    for (int i = tid; i < n_sub; i += kPrepThreads) {
+        int lo = 0, hi = kUnitTiles - 1;                    // the last tile that starts at or before i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (s_sub[mid] <= i) lo = mid;
+            else hi = mid - 1;
+        }
+        const int b = s_order[lo], npg = pages(b), blocks = (npg + 1) / 2;
+        const int nc = (int)((blocks + Cb - 1) / Cb), c = i - s_sub[lo];
+        const int b0 = (int)((long long)c * blocks / nc), b1 = (int)((long long)(c + 1) * blocks / nc);
+        int4* dst = reinterpret_cast<int4*>(out + i);
+        dst[0] = make_int4(s_t0[b], s_t0[b + 1] - s_t0[b], s_row[b], s_lo[b] / kPageSize + 2 * b0);
+        dst[1] = make_int4(min(2 * (b1 - b0), npg - 2 * b0), s_lo[b], s_hi[b], nc > 1 ? s_slot[lo] + c + 1 : 0);
+    }
+    if (tid == 0) {
+        if (s_bad) set_error(ctrl, kErrBadPos);
+        ctrl->n_items = s_bad ? 0 : n_sub;
+        ctrl->max_items = s_bad ? 0 : s_last_split;
+        ctrl->next_item = 0;
+        ctrl->done_ctas = 0;
+        ctrl->kv_heads = a.kv_heads;
+        ctrl->group = a.heads / a.kv_heads;
+        ctrl->head_dim = a.head_dim;
+        ctrl->magic = kPlanMagic;
+    }
+    return true;
+}
+
 template <typename T>
 __device__ void rope_write_token(const PrefillPrepArgs& a, int i) {
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
@@ -1026,6 +1183,7 @@ __global__ void __launch_bounds__(kPrepThreads) prefill_plan_kernel(const __grid
 // The tile list and its sub-tiles (coded prefill).
 __global__ void __launch_bounds__(kPrepThreads) prefill_split_kernel(const __grid_constant__ PrefillPrepArgs a) {
     griddep_launch_dependents();
+    if (build_units_small(a)) return;
     build_prefill_plan(a);
     __syncthreads();
     split_tiles(a);
