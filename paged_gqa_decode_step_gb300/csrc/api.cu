@@ -869,7 +869,7 @@ static CodedPfLayout coded_pf_layout(const pdattn_params* p, int n_tokens, int g
     const int g = p->heads / p->kv_heads, tile_tokens = 2 * (kPfRows / g);
     L.base = pf_layout(n_tokens, p->heads, p->head_dim, 2);
     L.slot_rows = (n_tokens < tile_tokens ? n_tokens : tile_tokens) * g;
-    const size_t slots = 4 * (size_t)grid;
+    const size_t slots = 2 * (size_t)grid;
     size_t off = L.base.total;
     L.factor = off; off = align256(off + sizeof(float) * (size_t)n_tokens * p->heads);
     L.units = off; off = align256(off + sizeof(PfTile) * ((size_t)n_tokens + slots));

@@ -85,7 +85,7 @@ struct PrefillPrepArgs {
     void* v_pool;
     char* ws;
     PfLayout L;
-    int split_grid;         // > 0: also list sub-tiles at `units`, for about two units per CTA of this many
+    int split_grid;         // > 0: also list sub-tiles at `units`, of about a share of this many CTAs each
     size_t units;
 };
 

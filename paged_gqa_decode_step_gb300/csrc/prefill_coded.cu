@@ -950,47 +950,46 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Code
     griddep_wait();
     const int lane = threadIdx.x & 31, g = a.group, Hk = a.kv_heads;
     const __nv_bfloat16* sinks = static_cast<const __nv_bfloat16*>(a.sinks);
-    // max_items: tiles up to the last split one (of 0 units none)
-    const int rows = ctrl->n_items == 0 ? 0 : ctrl->max_items * Hk * ca.slot_rows;
+    // tiles up to the last split one (of 0 units none), rows of the fullest of them
+    const int most = ctrl->chunk_pages * g;
+    const int rows = ctrl->n_items == 0 ? 0 : ctrl->max_items * Hk * most;
     for (int w = blockIdx.x * 8 + (threadIdx.x >> 5); w < rows; w += gridDim.x * 8) {
-        const int r = w % ca.slot_rows, kvh = w / ca.slot_rows % Hk, j = w / ca.slot_rows / Hk;
+        const int r = w % most, kvh = w / most % Hk, j = w / most / Hk;
         const PfTile t = reinterpret_cast<const PfTile*>(a.ws + a.L.tiles)[j];
         const int nch = t.pad & 4095, slot0 = t.pad >> 12;
         if (nch == 0 || r >= t.ntok * g) continue;
-        {
-            const size_t at0 = ((size_t)slot0 * a.kv_heads + kvh) * ca.slot_rows + r;
-            const size_t step = (size_t)a.kv_heads * ca.slot_rows;
-            float M = -1.0e30f, L = 0.f, O[N] = {};
-            #pragma unroll 4
-            for (int c = 0; c < nch; ++c) {
-                const float2 ml = __ldcg(ca.part_ml + at0 + c * step);
-                const float* src = ca.part_o + (at0 + c * step) * D + lane * N;
-                float x[N];
-                if constexpr (N == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-                    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-                    x[0] = v.x; x[1] = v.y;
-                }
-                const float Mn = fmaxf(M, ml.x);
-                const float fa = exp2_approx(M - Mn), fc = exp2_approx(ml.x - Mn);
-                M = Mn;
-                L = L * fa + fc * ml.y;
-                #pragma unroll
-                for (int e = 0; e < N; ++e) O[e] = O[e] * fa + fc * x[e];
+        const size_t at0 = ((size_t)slot0 * a.kv_heads + kvh) * ca.slot_rows + r;
+        const size_t step = (size_t)a.kv_heads * ca.slot_rows;
+        float M = -1.0e30f, L = 0.f, O[N] = {};
+        #pragma unroll 4
+        for (int c = 0; c < nch; ++c) {
+            const float2 ml = __ldcg(ca.part_ml + at0 + c * step);
+            const float* src = ca.part_o + (at0 + c * step) * D + lane * N;
+            float x[N];
+            if constexpr (N == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                x[0] = v.x; x[1] = v.y;
             }
-            const int h = kvh * g + r % g;
-            const float sk = sinks != nullptr ? __bfloat162float(sinks[h]) * 1.4426950408889634f : 0.f;
-            const float inv = sink_scale(M, L, sinks != nullptr, sk);
-            __nv_bfloat16* dst =
-                static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + r / g) * a.heads + h) * D + lane * N;
-            if constexpr (N == 4)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv),
-                                                            pack_bf16x2(O[2] * inv, O[3] * inv));
-            else
-                *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(O[0] * inv, O[1] * inv);
+            const float Mn = fmaxf(M, ml.x);
+            const float fa = exp2_approx(M - Mn), fc = exp2_approx(ml.x - Mn);
+            M = Mn;
+            L = L * fa + fc * ml.y;
+            #pragma unroll
+            for (int e = 0; e < N; ++e) O[e] = O[e] * fa + fc * x[e];
         }
+        const int h = kvh * g + r % g;
+        const float sk = sinks != nullptr ? __bfloat162float(sinks[h]) * 1.4426950408889634f : 0.f;
+        const float inv = sink_scale(M, L, sinks != nullptr, sk);
+        __nv_bfloat16* dst =
+            static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + r / g) * a.heads + h) * D + lane * N;
+        if constexpr (N == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv),
+                                                        pack_bf16x2(O[2] * inv, O[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(O[0] * inv, O[1] * inv);
     }
 }
 

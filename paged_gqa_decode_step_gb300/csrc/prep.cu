@@ -723,31 +723,33 @@ __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
 
 // Sub-tiles for a call with few tiles: tiles longer than Cb blocks of two
 // pages are cut along their keys into equal pieces, Cb = total blocks x kv
-// heads / (2 x grid) (about two units per CTA), at least kMinSplitBlocks (a
-// piece pays for its partial and the merge).  A sub-tile's pad is its partial
-// slot + 1 (0: the whole tile); a split tile's pad becomes first slot << 12 |
-// pieces.  Bounds: Cb >= blocks x Hk / (2 grid) makes the pieces of split
-// tiles at most 4 grid / Hk, so slots x Hk stay within 4 grid, and a tile's
-// pieces within 2 grid / Hk + 1.
+// heads / grid (a CTA's share; twice as many pieces took 143 us instead of
+// 119 on 32 rows of drafted tokens), at least kMinSplitBlocks (a piece pays
+// for its partial and the merge).  A sub-tile's pad is its partial slot + 1
+// (0: the whole tile); a split tile's pad becomes first slot << 12 | pieces.
+// Bounds: Cb >= blocks x Hk / grid makes the pieces of split tiles at most
+// 2 grid / Hk, so slots x Hk stay within 2 grid, and a tile's pieces within
+// grid / Hk + 1.  For the merge, max_items gets the tiles up to the last split
+// one and chunk_pages the most tokens of a split tile.
 constexpr int kMinSplitBlocks = 4;
 
 __device__ void split_tiles(const PrefillPrepArgs& a) {
     __shared__ int s_warp[32];
     __shared__ int s_sub[kPrepThreads], s_slot[kPrepThreads];
     __shared__ unsigned long long s_work;
-    __shared__ int s_last;
+    __shared__ int s_last, s_tokens;
     const int tid = threadIdx.x;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
     PfTile* tiles = reinterpret_cast<PfTile*>(a.ws + a.L.tiles);
     PfTile* sub = reinterpret_cast<PfTile*>(a.ws + a.units);
-    if (tid == 0) { s_work = 0; s_last = 0; }
+    if (tid == 0) { s_work = 0; s_last = 0; s_tokens = 0; }
     __syncthreads();
     const int n_tiles = ctrl->n_items;
     unsigned long long w = 0;
     for (int j = tid; j < n_tiles; j += blockDim.x) w += (tiles[j].npg + 1) / 2;
     if (w) atomicAdd(&s_work, w);
     __syncthreads();
-    const unsigned long long per = 2ull * a.split_grid;
+    const unsigned long long per = a.split_grid;
     const long long Cb = max((long long)((s_work * a.kv_heads + per - 1) / per), (long long)kMinSplitBlocks);
     int n_sub = 0, n_slot = 0;
     for (int base = 0; base < n_tiles; base += kPrepThreads) {
@@ -762,6 +764,7 @@ __device__ void split_tiles(const PrefillPrepArgs& a) {
         if (nch > 1) {
             tiles[j].pad = slot << 12 | nch;
             atomicMax(&s_last, j + 1);
+            atomicMax(&s_tokens, tiles[j].ntok);
         }
         __syncthreads();
         for (int i = tid; i < subs; i += blockDim.x) {
@@ -790,7 +793,8 @@ __device__ void split_tiles(const PrefillPrepArgs& a) {
     }
     if (tid == 0) {
         ctrl->n_items = n_sub;
-        ctrl->max_items = s_last;    // tiles up to the last split one
+        ctrl->max_items = s_last;
+        ctrl->chunk_pages = s_tokens;
     }
 }
 
@@ -806,7 +810,7 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
     __shared__ int s_last[kPrepThreads];
     __shared__ int s_t0[kUnitTiles + 1], s_row[kUnitTiles], s_lo[kUnitTiles], s_hi[kUnitTiles];
     __shared__ int s_off[kPfBuckets], s_order[kUnitTiles], s_sub[kUnitTiles + 1], s_slot[kUnitTiles];
-    __shared__ int s_bad, s_last_split;
+    __shared__ int s_bad, s_last_split, s_tokens;
     const int tid = threadIdx.x, n = a.n_tokens, Tq = a.tile_tokens, max_pos = a.pages_per_row * kPageSize;
     if (n > kUnitTokens) return false;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
@@ -827,7 +831,7 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
         if (k < per && i0 + k < n) last = r[k];
     s_last[tid] = last;
     for (int b = tid; b < kPfBuckets; b += kPrepThreads) s_off[b] = 0;
-    if (tid == 0) { s_bad = 0; s_last_split = 0; }
+    if (tid == 0) { s_bad = 0; s_last_split = 0; s_tokens = 0; }
     __syncthreads();
     if (bad) s_bad = 1;
     // run starts, then tile starts
@@ -895,7 +899,7 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
         s_order[atomicAdd(&s_off[kPfBuckets - 1 - min(pages(b), kPfBuckets - 1)], 1)] = b;
     __syncthreads();
     // pieces, as split_tiles cuts them
-    const long long per_unit = 2ll * a.split_grid;
+    const long long per_unit = a.split_grid;
     const long long Cb = max((blocks_all * (long long)a.kv_heads + per_unit - 1) / per_unit, (long long)kMinSplitBlocks);
     auto pieces = [&](int at) {
         return at < n_tiles ? (int)(((pages(s_order[at]) + 1) / 2 + Cb - 1) / Cb) : 0;
@@ -915,6 +919,7 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
             dst[0] = make_int4(s_t0[b], s_t0[b + 1] - s_t0[b], s_row[b], 0);
             dst[1] = make_int4(0, 0, 0, first_slot << 12 | c);
             atomicMax(&s_last_split, at + 1);
+            atomicMax(&s_tokens, s_t0[b + 1] - s_t0[b]);
         } else if (at < n_tiles) {
             reinterpret_cast<int4*>(tiles + at)[1] = make_int4(0, 0, 0, 0);
         }
@@ -941,6 +946,7 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
         if (s_bad) set_error(ctrl, kErrBadPos);
         ctrl->n_items = s_bad ? 0 : n_sub;
         ctrl->max_items = s_bad ? 0 : s_last_split;
+        ctrl->chunk_pages = s_tokens;
         ctrl->next_item = 0;
         ctrl->done_ctas = 0;
         ctrl->kv_heads = a.kv_heads;
