@@ -444,7 +444,7 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
                 }
             }
             auto mask = [&](uint32_t (&y)[32], int q4) {
-                if (state >> (2 * q4) & 3) {
+                if (state >> (2 * q4) & 1) {
                     const int from = min(max(c_lo - 32 * q4, 0), 32), to = min(max(c_hi + 1 - 32 * q4, 0), 32);
                     const uint32_t vis = (uint32_t)((1ull << to) - 1) & ~(uint32_t)((1ull << from) - 1);
                     #pragma unroll
@@ -473,6 +473,7 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             } else {
                 #pragma unroll 1
                 for (int q4 = 0; q4 < 4; ++q4) {
+                    if (state >> (2 * q4) & 2) continue;
                     uint32_t x[32];
                     tmem_ld32(s_addr + 32 * q4, x);
                     tmem_wait_ld();
@@ -507,12 +508,6 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             // over columns that chunks 0 .. q / 2 held, which have been read
             auto weights = [&](const uint32_t (&y)[32], int q4) {
                 uint32_t pk[16];
-                if ((state >> (2 * q4) & 3) == 2) {
-                    #pragma unroll
-                    for (int c = 0; c < 16; ++c) pk[c] = 0;
-                    tmem_st16(s_addr + 16 * q4, pk);
-                    return;
-                }
                 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                     float p0, p1;
@@ -527,6 +522,12 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             #pragma unroll 1
             for (int q4 = 0; q4 < 4; ++q4) {
                 uint32_t x[32];
+                if (state >> (2 * q4) & 2) {
+                    #pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] = 0;
+                    tmem_st16(s_addr + 16 * q4, *reinterpret_cast<const uint32_t(*)[16]>(&x[0]));
+                    continue;
+                }
                 tmem_ld32(s_addr + 32 * q4, x);
                 tmem_wait_ld();
                 if (state != 0) mask(x, q4);
