@@ -813,6 +813,7 @@ pdattn_status pdattn_coded_read(const pdattn_params* p, const pdattn_coded_cache
     a.slots = slots;
     a.k_out = k_out;
     a.v_out = v_out;
+    a.wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
     a.ws = static_cast<char*>(workspace);
     cudaError_t e = launch_read(a, p->dtype, cache->code, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded read launch");

@@ -222,16 +222,26 @@ __global__ void __launch_bounds__(kCodeThreads) read_kernel(const __grid_constan
             const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
             f[4 * k] = x.x * s; f[4 * k + 1] = x.y * s; f[4 * k + 2] = y.x * s; f[4 * k + 3] = y.y * s;
         }
-        if constexpr (sizeof(T) == 2) {
-            #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                reinterpret_cast<uint4*>(dst)[k] =
-                    make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
-                               pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
-        } else {
-            #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                reinterpret_cast<float4*>(dst)[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+        constexpr int kWords = 4 * sizeof(T);
+        uint32_t u[kWords];
+        #pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            if constexpr (sizeof(T) == 2) u[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+            else u[k] = __float_as_uint(f[k]);
+        }
+        // whole 32-byte sectors where the outputs' alignment allows them
+        #pragma unroll
+        for (int k = 0; k < kWords; k += 8) {
+            uint32_t* to = reinterpret_cast<uint32_t*>(dst) + k;
+            if (a.wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                             ::"l"(to), "r"(u[k]), "r"(u[k + 1]), "r"(u[k + 2]), "r"(u[k + 3]), "r"(u[k + 4]),
+                               "r"(u[k + 5]), "r"(u[k + 6]), "r"(u[k + 7])
+                             : "memory");
+            } else {
+                reinterpret_cast<uint4*>(to)[0] = make_uint4(u[k], u[k + 1], u[k + 2], u[k + 3]);
+                reinterpret_cast<uint4*>(to)[1] = make_uint4(u[k + 4], u[k + 5], u[k + 6], u[k + 7]);
+            }
         }
     };
     put(kc, ks, a.k_out);

@@ -130,6 +130,7 @@ struct CodeArgs {
 
 struct ReadArgs {
     int n_tokens, kv_heads, head_dim, num_pages;
+    int wide;               // 1: both outputs are 32-byte aligned
     const uint8_t* k;
     const uint8_t* v;
     const float* k_scale;
