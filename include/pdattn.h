@@ -346,9 +346,14 @@ pdattn_status pdattn_packed_attend(const pdattn_params* p, int32_t n_tokens, con
  * such a token are NaN in every dimension, and no other output changes.
  * Pages are shared and slots addressed as in the cache of T above.  The four
  * calls below take T = bf16 or f32 (pdattn_coded_prefill: bf16) and the same
- * head dims, groups, windows, scales, rope tables and sinks.  Codes and
- * scales are 16-byte aligned.  Scales that no call has written may hold
- * anything where no output sees them.
+ * head dims, groups, windows, scales, rope tables and sinks; chunk_pages is
+ * not used.  Codes and scales are 16-byte aligned.  Codes and scales that no
+ * call has written may hold anything where no output sees them.
+ *
+ * The attention calls hold codes times the ratio of their scale to a power of
+ * two at or above the scales around them (K: of 128 keys; V: of the row so
+ * far).  A value whose V scale is more than 2^14 below the largest V scale
+ * its row sees loses bits (2^-24 of that largest scale is the finest step).
  */
 typedef enum { PDATTN_E4M3 = 0, PDATTN_INT8 = 1 } pdattn_code;
 
@@ -400,7 +405,9 @@ pdattn_status pdattn_coded_read(const pdattn_params* p, const pdattn_coded_cache
  * and v_new into the slot of position positions[r] through table[r], then
  * attends over what the codes stand for.  Queries are not rounded to T
  * (the kernels hold them, and the weights, in f16 with a scale of their own;
- * for f32 in two f16 parts each); every sum is f32.
+ * for f32 in two f16 parts each); every sum is f32.  Two launches, no plan:
+ * equal shares of the visible pages are found on the device.  The same call
+ * on the same inputs gives the same bits.
  */
 pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cache* cache, const void* q,
                                   const void* k_new, const void* v_new, const int32_t* positions,
@@ -414,7 +421,8 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
  * for.  Layouts, errors and rules are those of pdattn_prefill_paged; bf16
  * only.  The products run on f16 tensor-core tiles (codes times the ratio of
  * their scale to a power of two, 11 bits); few tokens over long rows are
- * split along the keys and merged.
+ * split along the keys and merged.  Three launches, or four with the merge.
+ * n_tokens may be any number up to the one the workspace was sized for.
  */
 pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,
                                    const void* q, const void* k_new, const void* v_new, const int32_t* positions,
