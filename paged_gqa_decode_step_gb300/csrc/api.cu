@@ -897,6 +897,10 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
     pdattn_status s = check_coded(p, cache);
     if (s != PDATTN_OK) return s;
     if ((s = check_tokens(p, p->rows)) != PDATTN_OK) return s;
+    // the device counts shares of the work in 32 bits (a pair has at most a
+    // few units more than pages)
+    if ((long long)p->rows * p->kv_heads * ((long long)p->pages_per_row + 8) >= (1ll << 30))
+        return fail(PDATTN_EUNSUPPORTED, "rows x kv_heads x pages_per_row too large for one decode call");
     if (p->rows == 0) return PDATTN_OK;
     if (!q || !k_new || !v_new || !positions || !table || !out) return fail(PDATTN_EINVAL, "NULL data pointer");
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))

@@ -883,14 +883,13 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         if constexpr (kCoded) {
             // Static shares: the (row, kv head) pairs in order, each as many
             // units as it has pages plus U for its start and merge, cut into
-            // one equal run of units per CTA.  Unit x belongs to CTA
-            // ((x + 1) ctas - 1) / W, so every CTA knows how many others share a
-            // pair.  A CTA's partial results are at most two: of a pair it
-            // starts (slot 2 b + 1) and of one it carries on (slot 2 b).  All
-            // from the call's inputs: no wait, no plan launch (5 us) and no
-            // work cursor; the shares differ by one page.
-            const int R = a.rows, max_pos = a.pages_per_row * kPageSize;
-            const long long b = blockIdx.x;
+            // equal runs of `share` units, one per CTA.  Unit x belongs to CTA
+            // x / share, so every CTA knows how many others share a pair.  A
+            // CTA's partial results are at most two: of a pair it starts (slot
+            // 2 b + 1) and of one it carries on (slot 2 b).  All from the
+            // call's inputs: no wait, no plan launch (5 us) and no work cursor.
+            // (The host keeps the units under 2^30.)
+            const int R = a.rows, max_pos = a.pages_per_row * kPageSize, b = blockIdx.x;
             constexpr int U = C::kItemUnits;
             auto row_at = [&](int v, int* pos, int* lo) -> int {
                 *pos = v < R ? __ldg(a.positions + v) : -1;
@@ -898,23 +897,20 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 *lo = row_lo(*pos, a.window);
                 return *pos / kPageSize - *lo / kPageSize + 1;
             };
-            int pos = -1, lo = 0;
-            long long W = 0;
+            int pos = -1, lo = 0, W = 0;
             #pragma unroll 4
             for (int v = lane; v < R; v += 32) {
                 const int n = row_at(v, &pos, &lo);
                 W += n ? n + U : 0;
             }
-            #pragma unroll
-            for (int sh = 16; sh > 0; sh >>= 1) W += __shfl_xor_sync(0xffffffffu, W, sh);
-            W *= Hk;
-            const long long ctas = min((long long)gridDim.x, W / (U + 1));   // fewer CTAs than pages: each has a page
-            const long long x0 = b < ctas ? b * W / ctas : W, x1 = b < ctas ? (b + 1) * W / ctas : 0;
+            W = (int)__reduce_add_sync(0xffffffffu, (unsigned)W) * Hk;
+            const int share = max((W + (int)gridDim.x - 1) / (int)gridDim.x, U + 1);
+            const int x0 = b * share, x1 = min(W, x0 + share);
             if (lane == 0) *s_early = 1;   // published by the item barrier's arrival
             // Shared pairs go first, so that their merges run under the pairs
             // the CTA has to itself.
             for (int whole = 0; whole < 2; ++whole) {
-                long long before = 0;          // units of the rows before, per kv head
+                int before = 0;            // units of the rows before, of one kv head
                 for (int r0 = 0; r0 < R && before * Hk < x1 && ok; r0 += 32) {
                     const int n = row_at(r0 + lane, &pos, &lo);
                     int upto = n ? n + U : 0;
@@ -923,29 +919,29 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                         const int up = __shfl_up_sync(0xffffffffu, upto, sh);
                         if (lane >= sh) upto += up;
                     }
-                    const long long start = (before + upto - (n ? n + U : 0)) * Hk;
-                    uint32_t mine = __ballot_sync(0xffffffffu, n > 0 && start < x1 && start + (long long)(n + U) * Hk > x0);
+                    const int start = (before + upto - (n ? n + U : 0)) * Hk;
+                    uint32_t mine = __ballot_sync(0xffffffffu, n > 0 && start < x1 && start + (n + U) * Hk > x0);
                     before += __shfl_sync(0xffffffffu, upto, 31);
                     while (mine && ok) {
                         const int l = __ffs(mine) - 1;
                         mine &= mine - 1;
-                        const int row = r0 + l, nr = __shfl_sync(0xffffffffu, n, l), rpos = __shfl_sync(0xffffffffu, pos, l);
-                        const int rlo = __shfl_sync(0xffffffffu, lo, l);
-                        const long long rs = __shfl_sync(0xffffffffu, start, l);
-                        for (int h = x0 > rs ? (int)((x0 - rs) / (nr + U)) : 0; h < Hk && ok; ++h) {
-                            const long long u0 = rs + (long long)h * (nr + U) + U;   // unit of the pair's first page
+                        const int row = r0 + l, nr = __shfl_sync(0xffffffffu, n, l);
+                        const int rpos = __shfl_sync(0xffffffffu, pos, l), rlo = __shfl_sync(0xffffffffu, lo, l);
+                        const int rs = __shfl_sync(0xffffffffu, start, l);
+                        for (int h = x0 > rs ? (x0 - rs) / (nr + U) : 0; h < Hk && ok; ++h) {
+                            const int u0 = rs + h * (nr + U) + U;       // unit of the pair's first page
                             if (u0 >= x1) break;
-                            const int p0 = (int)(max(x0, u0) - u0), p1 = (int)(min(x1, u0 + nr) - u0);
+                            const int p0 = max(x0, u0) - u0, p1 = min(x1, u0 + nr) - u0;
                             if (p0 >= p1 || (p1 - p0 == nr) != (whole == 1)) continue;
-                            const int b0 = (int)(((u0 + 1) * ctas - 1) / W), b1 = (int)(((u0 + nr) * ctas - 1) / W);
+                            const int b0 = u0 / share, b1 = (u0 + nr - 1) / share;
                             for (int q = p0; q < p1 && ok; q += kChunkMax) {
                                 const int npg = min(kChunkMax, p1 - q), first = rlo / kPageSize + q;
                                 int pid0, pid1;
                                 load_pids(row, first, npg, &pid0, &pid1);
-                                ok = queue_item(make_int4(row, h << 16 | ((int)b - b0),
+                                ok = queue_item(make_int4(row, h << 16 | (b - b0),
                                                           (b1 - b0 + 1) | (q > p0 ? kCarriesOn : 0) |
                                                               (q + npg < p1 ? kCarriedOn : 0),
-                                                          2 * (int)b + (p0 == 0 ? 1 : 0)),
+                                                          2 * b + (p0 == 0 ? 1 : 0)),
                                                 make_int4(first, npg, rpos, rlo), pid0, pid1);
                             }
                         }

@@ -86,8 +86,11 @@ __global__ void __launch_bounds__(kCodeThreads, 5) code_kernel(const __grid_cons
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws);
     const int Hk = a.kv_heads, Hq = a.q ? a.heads : 0, per = Hq + 2 * Hk, i = blockIdx.x;
     const int lane = threadIdx.x % kLanes, e0 = 8 * lane;
-    if (a.merge_cnt)
+    if (a.merge_cnt) {
         for (int h = threadIdx.x; h < Hk; h += blockDim.x) a.merge_cnt[(size_t)i * Hk + h] = 0;
+        // a plan left here by another call is overwritten by this one
+        if (i == 0 && threadIdx.x == 0) ctrl->magic = 0;
+    }
     const int pos = __ldg(a.positions + i);
     // a token's position must lie in the rope table, and for the attention
     // calls in the page table

@@ -87,6 +87,7 @@ def test_counts(b):
         assert _calls(b, p, c, n=2 ** 28)[call]() == b.EUNSUPPORTED
     assert _calls(b, _p(b, rows=0), c, at=NULL, ws=NULL)["decode"]() == b.OK
     assert _calls(b, _p(b, rows=0), c)["prefill"]() == b.EINVAL
+    assert _calls(b, _p(b, rows=2 ** 20, pages_per_row=2 ** 10), c)["decode"]() == b.EUNSUPPORTED
     assert _calls(b, _p(b, dtype=torch.float32), c)["prefill"]() == b.EUNSUPPORTED   # f16 tensor-core tiles: bf16 only
     assert b.last_launch_count() == 0
     assert b.lib.pdattn_coded_workspace_size(p, -1) == 0
@@ -144,10 +145,10 @@ def test_the_shares_of_a_decode_call_cover_every_page_once():
         Hk, grid = rnd.choice([1, 2, 8, 12]), rnd.choice([1, 7, 152])
         pages = [rnd.choice([0, 1, 1, 2, 5, 17, 129]) for _ in range(rnd.randint(1, 40))]
         W = sum(n + U for n in pages if n) * Hk
-        G = min(grid, W // (U + 1))
+        share = max(-(-W // grid), U + 1)
         seen, partial = {}, {}
         for c in range(grid):
-            x0, x1 = (c * W // G, (c + 1) * W // G) if c < G else (W, 0)
+            x0, x1 = c * share, min(W, (c + 1) * share)
             start, slots = 0, []
             for r, n in enumerate(pages):
                 if not n:
@@ -157,7 +158,7 @@ def test_the_shares_of_a_decode_call_cover_every_page_once():
                     p0, p1 = max(x0, u0) - u0, min(x1, u0 + n) - u0
                     if p0 >= p1:
                         continue
-                    b0, b1 = ((u0 + 1) * G - 1) // W, ((u0 + n) * G - 1) // W
+                    b0, b1 = u0 // share, (u0 + n - 1) // share
                     for p in range(p0, p1):
                         assert (r, h, p) not in seen
                         seen[r, h, p] = c

@@ -208,6 +208,39 @@ def test_prefill_with_more_tiles_than_are_split():
     assert r.b.last_launch_count() == 3
 
 
+@pytest.mark.parametrize("rows,chunk", [(1100, 1), (1, 4200)])
+def test_prefill_plans_of_many_tiles_and_many_tokens(rows, chunk):
+    # more tiles, and more tokens, than the one-pass planner holds, in calls small enough to be split
+    r = Run(cu.Case(1, 1, 64, [(5 * i) % 140 for i in range(rows)], [chunk] * rows, kind=INT8, theta=0.0))
+    r.check("prefill")
+    assert r.b.last_launch_count() == 4
+
+
+def test_scale_and_chunk_pages():
+    c = cu.Case(8, 2, 64, [300, 9], [1, 1])
+    r = Run(c, scale=0.05, chunk_pages=3)        # decode takes any chunk_pages and does not use it
+    r.decode()
+    r.b.check_status(r.ws)
+    c.write()
+    want, bound = cu.attend(c.cache, cu.rope(c.q.float(), c.cos, c.sin, c.positions), c.positions, c.rows, c.table,
+                            scale=0.05)
+    cu.hold(r.out, want, bound)
+
+
+def test_an_uncoded_plan_does_not_outlive_a_coded_step():
+    r = Run(cu.Case(8, 2, 128, [130, 20], [1, 1]))
+    b = r.b
+    ws = torch.zeros(max(b.workspace_size(r.p), b.coded_workspace_size(r.p)), dtype=torch.uint8, device="cuda")
+    b.plan(r.p, r.pos, ws)
+    r.ws = ws
+    r.decode()
+    pools = [torch.zeros(r.c.pages, 2, 64, 128, dtype=BF16, device="cuda") for _ in range(2)]
+    b.attend(r.p, r.q, r.pos, r.table, *pools, torch.empty_like(r.q), ws)
+    with pytest.raises(b.PdattnError) as e:
+        b.check_status(ws)
+    assert e.value.status == b.EINVAL
+
+
 def test_prefill_writes_outputs_aligned_to_16_bytes_only():
     c = cu.Case(8, 2, 128, [0, 90], [70, 5])
     r = Run(c)
