@@ -906,7 +906,6 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             W = (int)__reduce_add_sync(0xffffffffu, (unsigned)W) * Hk;
             const int share = max((W + (int)gridDim.x - 1) / (int)gridDim.x, U + 1);
             const int x0 = b * share, x1 = min(W, x0 + share);
-            if (lane == 0) *s_early = 1;   // published by the item barrier's arrival
             // Shared pairs go first, so that their merges run under the pairs
             // the CTA has to itself.
             for (int whole = 0; whole < 2; ++whole) {
@@ -1118,6 +1117,10 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 if (q_pending) issue_q(q_dst, q_src, q_bar);
                 q_pending = false;
             };
+            // Coded: the coding launch, with no planner before it, is over when
+            // the first item comes; an early start would only hold the query
+            // copy back behind a ring of pages.
+            if constexpr (kCoded) resolve();
             while (ok && !aborted) {
                 if (!wait_for(bar_ifull + 8 * islot, iphase)) { ok = false; break; }
                 const uint8_t* slotp = item_q + islot * C::kItemBytes;
