@@ -23,57 +23,93 @@
 namespace pdattn {
 
 constexpr int kCodeThreads = 256;
+constexpr float kEdge = 8.67361738e-19f;       // 2^-60
 
-// Eight consecutive elements as f32.
+// Pairs of f32 as one instruction's operand.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
+        " mul.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
+        " sub.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mov.b64 rc, {%6, %7};\n"
+        " fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// The larger magnitude of three; a NaN wins.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Eight consecutive elements as loaded, and as pairs of f32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        f[2 * k] = __uint_as_float(w[k] << 16);
-        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+        #pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) v[k] = __ldg(reinterpret_cast<const uint4*>(p) + k);
     }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
-    #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p) + k);
-        f[4 * k] = v.x; f[4 * k + 1] = v.y; f[4 * k + 2] = v.z; f[4 * k + 3] = v.w;
-    }
-}
-
-// x / s rounded to nearest, for many x of one s: with r = RN(1 / s) and
-// q0 = RN(x r), the remainder x - s q0 is exact in one FMA and q0 + r * rem
-// rounds to the quotient (Markstein, IBM J. Res. Dev. 34, 1990).  Needs
-// quotient, remainder and s clear of the ends of the exponent range; a vector
-// whose largest magnitude lies outside [2^-60, 2^60] divides directly.  (The
-// remainder of a quotient below 2^-11 may then still be inexact; such a
-// quotient is under half of any code's smallest step.)
-struct Divider {
-    float s, r;
-    bool direct;
-    __device__ __forceinline__ Divider(float scale, uint32_t top) {
-        s = scale;
-        r = __fdiv_rn(1.f, scale);
-        direct = top < (uint32_t)(127 - 60) << 23 || top > (uint32_t)(127 + 60) << 23;
-    }
-    __device__ void apply(float (&x)[8]) const {
-        if (direct) {
-            #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __fdiv_rn(x[k], s);
+    __device__ __forceinline__ float2 pair(int k) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t w = k == 0 ? v[0].x : k == 1 ? v[0].y : k == 2 ? v[0].z : v[0].w;
+            return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
         } else {
-            #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float q0 = __fmul_rn(x[k], r);
-                x[k] = __fmaf_rn(__fmaf_rn(-s, q0, x[k]), r, q0);
-            }
+            const uint4& q = v[k / 2];
+            return k & 1 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
+                         : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
         }
     }
 };
+
+// x becomes -x / s, rounded to nearest, with s = max(top / qmax, 2^-126) of
+// the finite vector's largest magnitude `top`; returns s.
+//
+// For many x of one s: with r = RN(1 / s) and q0 = RN(x r), the remainder
+// x - s q0 is exact in one FMA and q0 + r * rem rounds to the quotient
+// (Markstein, IBM J. Res. Dev. 34, 1990); top / qmax the same way.  That needs
+// quotient, remainder and s clear of the ends of the exponent range, so a
+// vector whose top lies outside [2^-60, 2^60] is scaled by a power of two
+// first.  (A remainder of a quotient below 2^-11 may still be inexact, and its
+// x rounded by the scaling; such a quotient is under half of any code's
+// smallest step.)  The quotients are negated so that a zero keeps its sign: a
+// remainder of nothing is +0, and -r times it leaves a zero of either sign.
+template <typename Code>
+__device__ __forceinline__ float divide_by_scale(float2 (&x)[8], float top) {
+    constexpr float kBig = 18446744073709551616.f, kSmall = 1.f / kBig;    // 2^64, 2^-64
+    constexpr float kRq = 1.f / Code::kQMax;
+    float up = 1.f, down = 1.f;
+    if (top < kEdge || top > 1.f / kEdge) {
+        up = top < 1.f ? kBig : kSmall;
+        down = top < 1.f ? kSmall : kBig;
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = mul2(x[k], make_float2(up, up));
+    }
+    const float t = top * up;
+    const float t0 = __fmul_rn(t, kRq);
+    const float s = fmaxf(__fmaf_rn(__fmaf_rn(-Code::kQMax, t0, t), kRq, t0), kScaleMin * up);
+    const float r = __frcp_rn(s);
+    const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 n0 = mul2(x[k], nr);
+        x[k] = fma2(fma2(s2, n0, x[k]), nr, n0);
+    }
+    return s * down;
+}
 
 // Block = one token; its vectors (`heads` queries in attention calls, then
 // keys, then values) are dealt to groups of D / 16 lanes, so that every lane
@@ -110,36 +146,51 @@ __global__ void __launch_bounds__(kCodeThreads, 5) code_kernel(const __grid_cons
         else if (!slot_ok) set_error(ctrl, kErrBadPage);
     }
     const int end = !pos_ok ? 0 : slot_ok ? per : Hq;
+    const uint32_t group = ((1u << kLanes) - 1) << ((threadIdx.x & 31) / kLanes * kLanes);
+    #pragma unroll 1
     for (int j = threadIdx.x / kLanes; j < end; j += blockDim.x / kLanes) {
         const bool is_q = j < Hq, is_v = j >= Hq + Hk;
         const int h = is_q ? j : (is_v ? j - Hq - Hk : j - Hq);
         const T* src = static_cast<const T*>(is_q ? a.q : (is_v ? a.v_new : a.k_new)) +
                        ((size_t)i * (is_q ? Hq : Hk) + h) * D;
-        float lo[8], hi[8];
-        load8<T>(src + e0, lo);
-        load8<T>(src + kHalf + e0, hi);
+        Raw8<T> raw_lo, raw_hi;
+        raw_lo.load(src + e0);
+        raw_hi.load(src + kHalf + e0);
+        float2 x[8];                        // four pairs of the lower half, four of the upper
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[k] = raw_lo.pair(k);
+            x[4 + k] = raw_hi.pair(k);
+        }
         if (a.rope_cos && !is_v) {
-            const T* cr = static_cast<const T*>(a.rope_cos) + (size_t)pos * D;
-            const T* sr = static_cast<const T*>(a.rope_sin) + (size_t)pos * D;
-            float cl[8], ch[8], sl[8], sh[8];
-            load8<T>(cr + e0, cl);
-            load8<T>(cr + kHalf + e0, ch);
-            load8<T>(sr + e0, sl);
-            load8<T>(sr + kHalf + e0, sh);
+            const T* cr = static_cast<const T*>(a.rope_cos) + (size_t)pos * D + e0;
+            const T* sr = static_cast<const T*>(a.rope_sin) + (size_t)pos * D + e0;
+            Raw8<T> cos_lo, cos_hi, sin_lo, sin_hi;
+            cos_lo.load(cr);
+            cos_hi.load(cr + kHalf);
+            sin_lo.load(sr);
+            sin_hi.load(sr + kHalf);
+            // (not packed: packed products came out fused with the sums)
+            auto rotate = [](float u, float c, float v, float t, bool minus) {
+                return minus ? __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, t)) : __fadd_rn(__fmul_rn(u, c), __fmul_rn(v, t));
+            };
             #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float x = lo[k], y = hi[k];
-                lo[k] = __fsub_rn(__fmul_rn(x, cl[k]), __fmul_rn(y, sl[k]));
-                hi[k] = __fadd_rn(__fmul_rn(y, ch[k]), __fmul_rn(x, sh[k]));
+            for (int k = 0; k < 4; ++k) {
+                const float2 u = x[k], v = x[4 + k], cl = cos_lo.pair(k), ch = cos_hi.pair(k), sl = sin_lo.pair(k),
+                             sh = sin_hi.pair(k);
+                x[k] = make_float2(rotate(u.x, cl.x, v.x, sl.x, true), rotate(u.y, cl.y, v.y, sl.y, true));
+                x[4 + k] = make_float2(rotate(v.x, ch.x, u.x, sh.x, false), rotate(v.y, ch.y, u.y, sh.y, false));
             }
         }
         // the largest magnitude as its bits (they order like the value), so
         // that an infinity or a NaN anywhere shows in the result
-        uint32_t top = 0;
+        float top_a = 0.f, top_b = 0.f;
         #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            top = max(top, max(__float_as_uint(lo[k]) & 0x7fffffffu, __float_as_uint(hi[k]) & 0x7fffffffu));
-        const uint32_t group = ((1u << kLanes) - 1) << ((threadIdx.x & 31) / kLanes * kLanes);
+        for (int k = 0; k < 4; ++k) {
+            top_a = top3(top_a, x[k].x, x[k].y);
+            top_b = top3(top_b, x[4 + k].x, x[4 + k].y);
+        }
+        uint32_t top = __float_as_uint(top3(top_a, top_b, 0.f));
         #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(group, top, d));
         const bool finite = top < 0x7f800000u;
@@ -152,10 +203,10 @@ __global__ void __launch_bounds__(kCodeThreads, 5) code_kernel(const __grid_cons
             uint32_t w[8], r[8];
             #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float x0 = (k < 4 ? lo : hi)[2 * (k & 3)] * down, x1 = (k < 4 ? lo : hi)[2 * (k & 3) + 1] * down;
-                w[k] = pack_f16x2(x0, x1);
-                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                r[k] = pack_f16x2(x0 - back.x, x1 - back.y);
+                const float2 y = mul2(x[k], make_float2(down, down));
+                w[k] = pack_f16x2(y.x, y.y);
+                const float2 rest = sub2(y, __half22float2(*reinterpret_cast<const __half2*>(&w[k])));
+                r[k] = pack_f16x2(rest.x, rest.y);
             }
             *reinterpret_cast<uint4*>(row + e0 * 2) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(row + (kHalf + e0) * 2) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -169,22 +220,17 @@ __global__ void __launch_bounds__(kCodeThreads, 5) code_kernel(const __grid_cons
             }
         } else {
             // a vector that holds an infinity or a NaN stands for NaN throughout
-            float scale = fmaxf(__fdiv_rn(__uint_as_float(top), Code::kQMax), kScaleMin);
+            float scale = __uint_as_float(0x7fc00000u);
             if (finite) {
-                const Divider by(scale, top);
-                by.apply(lo);
-                by.apply(hi);
+                scale = divide_by_scale<Code>(x, __uint_as_float(top));
             } else {
-                scale = __uint_as_float(0x7fc00000u);
                 #pragma unroll
-                for (int k = 0; k < 8; ++k) lo[k] = hi[k] = 0.f;
+                for (int k = 0; k < 8; ++k) x[k] = make_float2(-0.f, -0.f);
             }
             const size_t at = ((size_t)(slot / kPageSize) * Hk + h) * kPageSize + slot % kPageSize;
             uint8_t* dst = (is_v ? a.v : a.k) + at * D;
-            *reinterpret_cast<uint2*>(dst + e0) = make_uint2(encode4<Code>(lo[0], lo[1], lo[2], lo[3]),
-                                                             encode4<Code>(lo[4], lo[5], lo[6], lo[7]));
-            *reinterpret_cast<uint2*>(dst + kHalf + e0) = make_uint2(encode4<Code>(hi[0], hi[1], hi[2], hi[3]),
-                                                                     encode4<Code>(hi[4], hi[5], hi[6], hi[7]));
+            *reinterpret_cast<uint2*>(dst + e0) = make_uint2(encode4<Code>(x[0], x[1]), encode4<Code>(x[2], x[3]));
+            *reinterpret_cast<uint2*>(dst + kHalf + e0) = make_uint2(encode4<Code>(x[4], x[5]), encode4<Code>(x[6], x[7]));
             if (lane == 0) (is_v ? a.v_scale : a.k_scale)[at] = scale;
         }
     }

@@ -42,22 +42,27 @@ __device__ __forceinline__ void widen4<Int8>(uint32_t w, uint32_t& lo, uint32_t&
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
-// Four values already divided by their scale -> four codes (round to nearest
-// even; a quotient past qmax by a rounding saturates).
+// Four values already divided by their scale, with their signs turned -> four
+// codes, rounded to nearest even.  (A quotient is past qmax by a rounding at
+// most.)
 template <typename Code>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d);
+__device__ __forceinline__ uint32_t encode4(float2 a, float2 b);
 template <>
-__device__ __forceinline__ uint32_t encode4<E4m3>(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t encode4<E4m3>(float2 a, float2 b) {
     uint32_t w;
     asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
         " mov.b32 %0, {lo, hi};\n}"
-        : "=r"(w) : "f"(a), "f"(b), "f"(c), "f"(d));
-    return w;
+        : "=r"(w) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return w ^ 0x80808080u;
 }
+// int8: beside 1.5 * 2^23 the last bit is worth 1, so the sum is rounded to an
+// integer and its low byte is that integer's.
 template <>
-__device__ __forceinline__ uint32_t encode4<Int8>(float a, float b, float c, float d) {
-    auto one = [](float x) { return (uint32_t)(min(127, max(-127, __float2int_rn(x))) & 0xff); };
-    return one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+__device__ __forceinline__ uint32_t encode4<Int8>(float2 a, float2 b) {
+    constexpr float kOnes = 12582912.f;
+    const uint32_t lo = __byte_perm(__float_as_uint(__fsub_rn(kOnes, a.x)), __float_as_uint(__fsub_rn(kOnes, a.y)), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(__fsub_rn(kOnes, b.x)), __float_as_uint(__fsub_rn(kOnes, b.y)), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {

@@ -94,6 +94,27 @@ def test_write_at_the_ends_of_the_range(kind, dtype):
 
 
 @pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_write_divides_as_the_formula_does_at_every_exponent(kind):
+    g = torch.Generator().manual_seed(11)
+    n, D = 2048, 64
+    c = cu.Case(8, 8, D, [0], [n], F32, kind, theta=0.0, seed=6)
+    # every mantissa bit random; a vector's exponents lie within 2^6, the vectors' anywhere an f32 has one
+    low = torch.randint(1, 248, (n, 8, 1), generator=g, dtype=torch.int32)
+    low[:, 0] = torch.randint(60, 74, (n, 1), generator=g, dtype=torch.int32)       # about 2^-60
+    low[:, 1] = torch.randint(180, 194, (n, 1), generator=g, dtype=torch.int32)     # about 2^60
+    exps = low + torch.randint(0, 7, (n, 8, D), generator=g, dtype=torch.int32)
+    bits = (exps << 23) | torch.randint(0, 2 ** 23, (n, 8, D), generator=g, dtype=torch.int32)
+    sign = torch.randint(0, 2, (n, 8, D), generator=g, dtype=torch.int32) << 31
+    x = (bits | sign).view(torch.float32)
+    c.k_new, c.v_new = x, x.flip(0).contiguous()
+    r = Run(c)
+    r.b.coded_write(r.p, r.cache, r.k, r.v, r.pos, r.slots, r.ws)
+    r.b.check_status(r.ws)
+    c.write()
+    c.cache.same(r.tensors)
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
 @pytest.mark.parametrize("dtype,D,kv_heads,n", [(BF16, 128, 8, 1), (BF16, 64, 5, 333), (F32, 128, 2, 66), (F32, 64, 1, 31)])
 def test_read_gives_what_the_codes_stand_for(kind, dtype, D, kv_heads, n):
     g = torch.Generator().manual_seed(n)
