@@ -132,6 +132,76 @@ __device__ __forceinline__ int take_unit(CpBars& bars, const UnitSlot* s_unit, u
 }
 
 // ---------------------------------------------------------------------------
+// MMA sequences.  The issuing warp bounds short and long rows alike, and with
+// four code streams per scheduler an instruction of it costs some ten clocks:
+// a block's MMAs and their commits are one run of code under one elected lane,
+// with conditions as predicates and descriptors whose upper words (constant,
+// see smem_desc) need no carry.
+// ---------------------------------------------------------------------------
+#define PDATTN_MMA_SS(off, pred, acc)                                                                       \
+    "add.u32 x, %1, " off ";\n add.u32 y, %2, " off ";\n mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"       \
+    "@" pred " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " acc ";\n"
+#define PDATTN_MMA_TS(aoff, boff, pred, acc)                                                                \
+    "add.u32 x, %1, " aoff ";\n add.u32 y, %2, " boff ";\n mov.b64 b, {y, %5};\n"                          \
+    "@" pred " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, " acc ";\n"
+#define PDATTN_COMMIT(pred, bar)                                                                            \
+    "@" pred " tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [" bar "];\n"
+
+// Upper word of the descriptors: stride 1024 bytes, version 1, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+// S = Q K^T over D dimensions; then the commits of S, and if so flagged of the
+// Q tile (bit 0) and of K's stage (bit 1).
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t q_lo, uint32_t k_lo, uint32_t idesc, uint32_t s_full,
+                                         uint32_t q_empty, uint32_t k_empty, uint32_t flags) {
+    if constexpr (D == 128)
+        asm volatile(
+            "{\n .reg .pred e, f, t, c0, c1;\n .reg .b32 x, y;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n"
+            " setp.ne.u32 t, 0, 0;\n not.pred f, t;\n and.b32 x, %4, 1;\n setp.ne.and.u32 c0, x, 0, e;\n"
+            " and.b32 y, %4, 2;\n setp.ne.and.u32 c1, y, 0, e;\n"
+            PDATTN_MMA_SS("0", "e", "t") PDATTN_MMA_SS("2", "e", "f") PDATTN_MMA_SS("4", "e", "f")
+            PDATTN_MMA_SS("6", "e", "f") PDATTN_MMA_SS("1024", "e", "f") PDATTN_MMA_SS("1026", "e", "f")
+            PDATTN_MMA_SS("1028", "e", "f") PDATTN_MMA_SS("1030", "e", "f")
+            PDATTN_COMMIT("e", "%6") PDATTN_COMMIT("c0", "%7") PDATTN_COMMIT("c1", "%8") "}"
+            ::"r"(s_tmem), "r"(q_lo), "r"(k_lo), "r"(idesc), "r"(flags), "n"(kDescHi), "r"(s_full), "r"(q_empty),
+              "r"(k_empty)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred e, f, t, c0, c1;\n .reg .b32 x, y;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n"
+            " setp.ne.u32 t, 0, 0;\n not.pred f, t;\n and.b32 x, %4, 1;\n setp.ne.and.u32 c0, x, 0, e;\n"
+            " and.b32 y, %4, 2;\n setp.ne.and.u32 c1, y, 0, e;\n"
+            PDATTN_MMA_SS("0", "e", "t") PDATTN_MMA_SS("2", "e", "f") PDATTN_MMA_SS("4", "e", "f")
+            PDATTN_MMA_SS("6", "e", "f")
+            PDATTN_COMMIT("e", "%6") PDATTN_COMMIT("c0", "%7") PDATTN_COMMIT("c1", "%8") "}"
+            ::"r"(s_tmem), "r"(q_lo), "r"(k_lo), "r"(idesc), "r"(flags), "n"(kDescHi), "r"(s_full), "r"(q_empty),
+              "r"(k_empty)
+            : "memory");
+}
+
+// O (+)= P V over a block's keys, one page of them with kOne; then the commits
+// that the flags ask for.
+constexpr uint32_t kPend = 1, kFirst = 2, kLast = 4, kOne = 8, kFrees = 16;
+__device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t idesc,
+                                         uint32_t v_empty, uint32_t o_done, uint32_t flags) {
+    asm volatile(
+        "{\n .reg .pred e, f, t, two, c0, c1;\n .reg .b32 x, y;\n .reg .b64 b;\n elect.sync _|e, 0xffffffff;\n"
+        " and.b32 x, %4, 2;\n setp.eq.u32 t, x, 0;\n setp.eq.u32 f, 0, 0;\n"
+        " and.b32 y, %4, 8;\n setp.eq.and.u32 two, y, 0, e;\n and.b32 x, %4, 16;\n setp.ne.and.u32 c0, x, 0, e;\n"
+        " and.b32 y, %4, 4;\n setp.ne.and.u32 c1, y, 0, e;\n"
+        PDATTN_MMA_TS("0", "0", "e", "t") PDATTN_MMA_TS("8", "128", "e", "f") PDATTN_MMA_TS("16", "256", "e", "f")
+        PDATTN_MMA_TS("24", "384", "e", "f") PDATTN_MMA_TS("32", "512", "two", "f") PDATTN_MMA_TS("40", "640", "two", "f")
+        PDATTN_MMA_TS("48", "768", "two", "f") PDATTN_MMA_TS("56", "896", "two", "f")
+        PDATTN_COMMIT("c0", "%6") PDATTN_COMMIT("c1", "%7") "}"
+        ::"r"(o_tmem), "r"(p_tmem), "r"(v_lo), "r"(idesc), "r"(flags), "n"(kDescHi), "r"(v_empty), "r"(o_done)
+        : "memory");
+}
+#undef PDATTN_MMA_SS
+#undef PDATTN_MMA_TS
+#undef PDATTN_COMMIT
+
+// ---------------------------------------------------------------------------
 // The block warp: descriptors of the unit stream's blocks.
 // ---------------------------------------------------------------------------
 // A scale's power of two at or above it, as a biased exponent in [1, 252].
@@ -798,37 +868,14 @@ __global__ void __launch_bounds__(kCpThreads, 1)
         constexpr uint32_t idesc_o = instr_desc(128, D, 0, 1, 0);
         bool issued = false;
         bool ok = true;
-        const uint64_t dq = smem_desc(q_s, 16, 1024), dk = smem_desc(st_s, 16, 1024);
-        const uint64_t dv = smem_desc(st_s + C::kKBytes, 16384, 1024);
-        auto qk = [&](int h, int s, bool one_page) {
-            const uint32_t idesc = one_page ? idesc_s64 : idesc_s;
-            const uint64_t a0 = dq + (uint64_t)(h * (C::kQBytes >> 4));
-            const uint64_t b0 = dk + (uint64_t)(s * (C::kStageBytes >> 4));
-            #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                umma_f16kind(tmem + 128u * h, a0 + (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2),
-                             b0 + (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 2), idesc, ks > 0 ? 1u : 0u);
-            umma_commit(smem_u32(&bars.s_full[h]));
-        };
-        auto pv = [&](int h, uint32_t j, int s, bool first, bool one_page) -> bool {
-            if (!cwait(smem_u32(&bars.p_full[h]), j & 1, abort, ctrl)) return false;
-            tc_fence_after();
-            issued = true;
-            const uint64_t b0 = dv + (uint64_t)(s * (C::kStageBytes >> 4));
-            #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                if (ks < 4 || !one_page)
-                    umma_f16kind_ts(tmem + C::kColO + h * D, tmem + 128u * h + ks * 8, b0 + (uint64_t)(ks * 128),
-                                    idesc_o, (first && ks == 0) ? 0u : 1u);
-            return true;
-        };
+        const uint32_t q_lo = (uint32_t)smem_desc(q_s, 16, 1024), k_lo = (uint32_t)smem_desc(st_s, 16, 1024);
+        const uint32_t v_lo = (uint32_t)smem_desc(st_s + C::kKBytes, 16384, 1024);
         // Blocks of successive units form one stream.  A step takes one block:
         // for each half that works on it, the half's pending PV (of its
         // previous block), then S of this block.  A pending PV of the unit
         // before goes out at the next unit's first step in any case.  The
         // half loop stays rolled so that each MMA sequence is issued from one
         // place; per-half state is selected by value.
-        constexpr uint32_t kPend = 1, kFirst = 2, kLast = 4, kOne = 8, kFrees = 16;
         uint32_t it = 0, uq0 = 0, uq1 = 0;               // blocks; units per half
         uint32_t cs0 = 0, cs1 = 0, f0 = 0, f1 = 0;       // S issued per half; flags of the pending PV
         uint32_t pit0 = 0, pit1 = 0;                     // its block
@@ -868,10 +915,13 @@ __global__ void __launch_bounds__(kCpThreads, 1)
                     const uint32_t pit = h ? pit1 : pit0;
                     ok = cwait(smem_u32(&bars.v_ready[pit % C::kStages]), (pit / C::kStages) & 1, abort, ctrl);
                     if (!ok) break;
-                    ok = pv(h, (h ? cs1 : cs0) - 1, pit % C::kStages, f & kFirst, f & kOne);
+                    ok = cwait(smem_u32(&bars.p_full[h]), ((h ? cs1 : cs0) - 1) & 1, abort, ctrl);
                     if (!ok) break;
-                    if (f & kFrees) umma_commit(smem_u32(&bars.v_empty[pit % C::kStages]));
-                    if (f & kLast) umma_commit(smem_u32(&bars.o_done[h]));
+                    tc_fence_after();
+                    issued = true;
+                    issue_pv(tmem + C::kColO + h * D, tmem + 128u * h,
+                             v_lo + (pit % C::kStages) * (C::kStageBytes >> 4), idesc_o,
+                             smem_u32(&bars.v_empty[pit % C::kStages]), smem_u32(&bars.o_done[h]), f);
                     if (h) f1 = 0;
                     else f0 = 0;
                 }
@@ -888,10 +938,11 @@ __global__ void __launch_bounds__(kCpThreads, 1)
                     }
                     tc_fence_after();
                     issued = true;
-                    qk(h, s, one);
-                    // the half's last block of the unit
+                    // the half's last block of the unit; the block's last half frees K
                     const bool last = 2 * (bk + (alt ? 2 : 1)) >= npg;
-                    if (last) umma_commit(smem_u32(&bars.q_empty[h]));
+                    issue_qk<D>(tmem + 128u * h, q_lo + h * (C::kQBytes >> 4), k_lo + s * (C::kStageBytes >> 4),
+                                one ? idesc_s64 : idesc_s, smem_u32(&bars.s_full[h]), smem_u32(&bars.q_empty[h]),
+                                smem_u32(&bars.k_empty[s]), (last ? 1u : 0u) | (alt || h == nh - 1 ? 2u : 0u));
                     const uint32_t nf = kPend | (first ? kFirst : 0) | (last ? kLast : 0) | (one ? kOne : 0) |
                                         (alt || h == nh - 1 ? kFrees : 0);
                     if (h) {
@@ -906,7 +957,6 @@ __global__ void __launch_bounds__(kCpThreads, 1)
                 }
             }
             if (!ok || end) break;
-            umma_commit(smem_u32(&bars.k_empty[s]));     // this block's S issued
             ++it;
             ++bk;
         }
