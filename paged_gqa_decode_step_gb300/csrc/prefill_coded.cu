@@ -325,87 +325,93 @@ __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw,
     const size_t src_off = (size_t)(cw * 8 + kx) * D + (lane & 3) * 16;
     const int dst0 = cw * 1024 + kx * 128 + (((2 * (lane & 3)) ^ kx) << 4);
     const int dst1 = cw * 1024 + kx * 128 + (((2 * (lane & 3) + 1) ^ kx) << 4);
+    // Operands go in the order K0, K1, V0, K2, V1, ...: a block's S is issued a
+    // step before its PV, and its V's stage is freed a step after its K's.  (In
+    // the order of blocks each K waited for the V before it.)
     uint4 r[kPer];                              // codes of the next operand to convert: key i / boxes, box i % boxes
-    int y0 = -1, y1 = -1;                       // pages of the next codes to load
-    auto take_desc = [&](uint32_t n, int* all_in) -> bool {
-        if (!cwait(smem_u32(&bars.desc_full[n % kDescs]), (n / kDescs) & 1, abort, ctrl)) return false;
-        const uint4 d = lds128(smem_u32(&s_desc[n % kDescs]));
-        y0 = (int)d.x;
-        y1 = (int)d.y;
-        *all_in = (int)d.z;
-        return y0 >= 0;
-    };
-    int all_in = 1, next_in = 1;
-    if (!take_desc(0, &all_in)) return;
-    const uint8_t* p0 = ca.k + (size_t)y0 * D + src_off;
-    const uint8_t* p1 = ca.k + (size_t)max(y1, 0) * D + src_off;
-    #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    auto pages_of = [&](uint32_t n) { return lds128(smem_u32(&s_desc[n % kDescs])); };   // y0, y1, all_in
+    auto fetch = [&](int i, const uint8_t* p0, const uint8_t* p1, bool two) {
         const int j = i / C::kBoxes;
-        if (j < kKeys / 2 || y1 >= 0)
+        if (j < kKeys / 2 || two)
             r[i] = __ldg(reinterpret_cast<const uint4*>((j < kKeys / 2 ? p0 : p1) + (j & 1) * 32 * D + (i % C::kBoxes) * 64));
-    }
+    };
+    if (!cwait(smem_u32(&bars.desc_full[0]), 0, abort, ctrl)) return;
+    uint4 d = pages_of(0);
+    if ((int)d.x < 0) return;
+    #pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        fetch(i, ca.k + (size_t)d.x * D + src_off, ca.k + (size_t)max((int)d.y, 0) * D + src_off, (int)d.y >= 0);
+    uint32_t b = 0, end = UINT_MAX;             // the operand's block; one past the last block, once known
+    bool is_k = true;
     #pragma unroll 1
-    for (uint32_t it = 0;; ++it) {
-        const int st = it % C::kStages;
-        const uint32_t par = (it / C::kStages) & 1;
-        const bool two = y1 >= 0;
-        bool more = true;
-        // K, then V, through one copy of the code.  Each register is refilled
-        // as soon as it is converted, a whole operand ahead of its use.
-        #pragma unroll 1
-        for (int op = 0; op < 2; ++op) {
-            if (op == 1) {
-                more = take_desc(it + 1, &next_in);
-                if (!more && *abort) return;
+    for (;;) {
+        // the operand after this one
+        bool next_k = !is_k || b == 0, more = true;
+        uint32_t nb = is_k ? (b == 0 ? 1 : b - 1) : b + 2;
+        if (next_k) {
+            if (end == UINT_MAX) {
+                if (!cwait(smem_u32(&bars.desc_full[nb % kDescs]), (nb / kDescs) & 1, abort, ctrl)) return;
+                if ((int)pages_of(nb).x < 0) end = nb;
             }
-            const uint8_t* pool = op == 0 ? ca.v : ca.k;
-            p0 = pool + (size_t)max(y0, 0) * D + src_off;
-            p1 = pool + (size_t)max(y1, 0) * D + src_off;
-            uint32_t r2[kKeys];
-            #pragma unroll
-            for (int j = 0; j < kKeys; ++j) {
-                const uint32_t rr = s_desc[it % kDescs].ratio[32 * j + cw * 8 + kx];
-                r2[j] = __byte_perm(rr, rr, op == 0 ? 0x1010 : 0x3232);
+            if (nb >= end) {
+                next_k = false;
+                nb = is_k ? b : b + 1;
+                more = nb < end;
             }
-            if (!all_in) {
-                // a row outside the tile's keys (ratio 0) may hold any codes, e4m3's NaN among them
-                #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (r2[i / C::kBoxes] == 0) r[i] = make_uint4(0, 0, 0, 0);
-            }
-            if (!cwait(smem_u32(op == 0 ? &bars.k_empty[st] : &bars.v_empty[st]), par ^ 1, abort, ctrl)) return;
-            uint8_t* base = stages + st * C::kStageBytes + op * C::kKBytes;
-            #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int j = i / C::kBoxes;
-                if (j < kKeys / 2 || two) {
-                    const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-                    uint32_t h[8];
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        widen4<Code>(w[e], h[2 * e], h[2 * e + 1]);
-                        h[2 * e] = mul_f16x2(h[2 * e], r2[j]);
-                        h[2 * e + 1] = mul_f16x2(h[2 * e + 1], r2[j]);
-                    }
-                    uint8_t* to = base + (i % C::kBoxes) * 16384 + j * 4096;
-                    *reinterpret_cast<uint4*>(to + dst0) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(to + dst1) = make_uint4(h[4], h[5], h[6], h[7]);
-                }
-                if (more && (j < kKeys / 2 || y1 >= 0))
-                    r[i] = __ldg(reinterpret_cast<const uint4*>((j < kKeys / 2 ? p0 : p1) + (j & 1) * 32 * D +
-                                                                (i % C::kBoxes) * 64));
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(op == 0 ? &bars.k_ready[st] : &bars.v_ready[st]));
         }
+        const bool two = (int)d.y >= 0, all_in = d.z != 0;
+        if (more) d = pages_of(nb);
+        const bool next_two = (int)d.y >= 0;
+        const uint8_t* pool = (next_k ? ca.k : ca.v) + src_off;
+        const uint8_t* p0 = pool + (size_t)d.x * D;
+        const uint8_t* p1 = pool + (size_t)max((int)d.y, 0) * D;
+        const int st = b % C::kStages;
+        const uint32_t par = (b / C::kStages) & 1;
+        uint32_t r2[kKeys];
+        #pragma unroll
+        for (int j = 0; j < kKeys; ++j) {
+            const uint32_t rr = s_desc[b % kDescs].ratio[32 * j + cw * 8 + kx];
+            r2[j] = __byte_perm(rr, rr, is_k ? 0x1010 : 0x3232);
+        }
+        if (!all_in) {
+            // a row outside the tile's keys (ratio 0) may hold any codes, e4m3's NaN among them
+            #pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (r2[i / C::kBoxes] == 0) r[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (!cwait(smem_u32(is_k ? &bars.k_empty[st] : &bars.v_empty[st]), par ^ 1, abort, ctrl)) return;
+        uint8_t* base = stages + st * C::kStageBytes + (is_k ? 0 : C::kKBytes);
+        // each register is refilled as soon as it is converted, a whole operand ahead of its use
+        #pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int j = i / C::kBoxes;
+            if (j < kKeys / 2 || two) {
+                const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+                uint32_t h[8];
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    widen4<Code>(w[e], h[2 * e], h[2 * e + 1]);
+                    h[2 * e] = mul_f16x2(h[2 * e], r2[j]);
+                    h[2 * e + 1] = mul_f16x2(h[2 * e + 1], r2[j]);
+                }
+                uint8_t* to = base + (i % C::kBoxes) * 16384 + j * 4096;
+                *reinterpret_cast<uint4*>(to + dst0) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(to + dst1) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            if (more) fetch(i, p0, p1, next_two);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
         if (lane == 0) {
-            mbar_arrive(smem_u32(&bars.desc_empty[it % kDescs]));
-            if (cw == 0) *s_blocks = (int)it + 1;   // progress, for the scheduler
+            mbar_arrive(smem_u32(is_k ? &bars.k_ready[st] : &bars.v_ready[st]));
+            if (!is_k) {
+                mbar_arrive(smem_u32(&bars.desc_empty[b % kDescs]));
+                if (cw == 0) *s_blocks = (int)b + 1;   // progress, for the scheduler
+            }
         }
         if (!more) return;
-        all_in = next_in;
+        is_k = next_k;
+        b = nb;
     }
 }
 
