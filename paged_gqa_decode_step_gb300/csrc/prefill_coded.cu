@@ -309,109 +309,100 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
 }
 
 // ---------------------------------------------------------------------------
-// Converters (four warps): codes of the unit stream's blocks to f16.
+// Converters: codes of the unit stream's blocks to f16, K by two warps and V
+// by two.  (Four warps that take K and V in turn meet twice the barriers:
+// drafted tokens 116 us against 111.)
 // ---------------------------------------------------------------------------
 template <int D, typename Code>
 __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw, int lane, uint8_t* stages, CpBars& bars,
                                              const BlockDesc* s_desc, volatile int* s_blocks, volatile int* abort,
                                              Ctrl* ctrl) {
     using C = CpCfg<D>;
-    // A thread takes 16 codes of four keys (32 j + 8 cw + lane / 4, j = 0..3)
-    // from each 64-column box: eight lanes then store the even 16-byte chunks
-    // of one key and the odd ones of the next, which fill the eight bank
-    // groups, and every address is a constant away from two bases.
+    // A thread takes 16 codes of four keys (32 j + 16 w + 8 part + lane / 4,
+    // j = 0..3) from each 64-column box, in two parts: eight lanes then store
+    // the even 16-byte chunks of one key and the odd ones of the next, which
+    // fill the eight bank groups, and every address is a constant away from two
+    // bases.
     constexpr int kKeys = 4, kPer = kKeys * C::kBoxes;
-    const int kx = lane >> 2;
-    const size_t src_off = (size_t)(cw * 8 + kx) * D + (lane & 3) * 16;
-    const int dst0 = cw * 1024 + kx * 128 + (((2 * (lane & 3)) ^ kx) << 4);
-    const int dst1 = cw * 1024 + kx * 128 + (((2 * (lane & 3) + 1) ^ kx) << 4);
-    // Operands go in the order K0, K1, V0, K2, V1, ...: a block's S is issued a
-    // step before its PV, and its V's stage is freed a step after its K's.  (In
-    // the order of blocks each K waited for the V before it.)
-    uint4 r[kPer];                              // codes of the next operand to convert: key i / boxes, box i % boxes
-    auto pages_of = [&](uint32_t n) { return lds128(smem_u32(&s_desc[n % kDescs])); };   // y0, y1, all_in
+    const bool is_k = cw < 2;
+    const int kx = lane >> 2, w16 = (cw & 1) * 16;
+    const uint8_t* pool = (is_k ? ca.k : ca.v) + (size_t)(w16 + kx) * D + (lane & 3) * 16;
+    const uint32_t pick = is_k ? 0x1010 : 0x3232;
+    uint64_t* ready = is_k ? bars.k_ready : bars.v_ready;
+    uint64_t* empty = is_k ? bars.k_empty : bars.v_empty;
+    stages += (is_k ? 0 : C::kKBytes) + w16 * 128 + kx * 128;
+    const int dst0 = ((2 * (lane & 3)) ^ kx) << 4, dst1 = ((2 * (lane & 3) + 1) ^ kx) << 4;
+    uint4 r[kPer];                              // the next part's codes: key i / boxes, box i % boxes
     auto fetch = [&](int i, const uint8_t* p0, const uint8_t* p1, bool two) {
         const int j = i / C::kBoxes;
         if (j < kKeys / 2 || two)
             r[i] = __ldg(reinterpret_cast<const uint4*>((j < kKeys / 2 ? p0 : p1) + (j & 1) * 32 * D + (i % C::kBoxes) * 64));
     };
     if (!cwait(smem_u32(&bars.desc_full[0]), 0, abort, ctrl)) return;
-    uint4 d = pages_of(0);
+    uint4 d = lds128(smem_u32(&s_desc[0]));     // y0, y1, all_in
     if ((int)d.x < 0) return;
     #pragma unroll
     for (int i = 0; i < kPer; ++i)
-        fetch(i, ca.k + (size_t)d.x * D + src_off, ca.k + (size_t)max((int)d.y, 0) * D + src_off, (int)d.y >= 0);
-    uint32_t b = 0, end = UINT_MAX;             // the operand's block; one past the last block, once known
-    bool is_k = true;
+        fetch(i, pool + (size_t)d.x * D, pool + (size_t)max((int)d.y, 0) * D, (int)d.y >= 0);
     #pragma unroll 1
-    for (;;) {
-        // the operand after this one
-        bool next_k = !is_k || b == 0, more = true;
-        uint32_t nb = is_k ? (b == 0 ? 1 : b - 1) : b + 2;
-        if (next_k) {
-            if (end == UINT_MAX) {
-                if (!cwait(smem_u32(&bars.desc_full[nb % kDescs]), (nb / kDescs) & 1, abort, ctrl)) return;
-                if ((int)pages_of(nb).x < 0) end = nb;
-            }
-            if (nb >= end) {
-                next_k = false;
-                nb = is_k ? b : b + 1;
-                more = nb < end;
-            }
-        }
+    for (uint32_t it = 0;; ++it) {
+        const int st = it % C::kStages;
         const bool two = (int)d.y >= 0, all_in = d.z != 0;
-        if (more) d = pages_of(nb);
-        const bool next_two = (int)d.y >= 0;
-        const uint8_t* pool = (next_k ? ca.k : ca.v) + src_off;
-        const uint8_t* p0 = pool + (size_t)d.x * D;
-        const uint8_t* p1 = pool + (size_t)max((int)d.y, 0) * D;
-        const int st = b % C::kStages;
-        const uint32_t par = (b / C::kStages) & 1;
-        uint32_t r2[kKeys];
-        #pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-            const uint32_t rr = s_desc[b % kDescs].ratio[32 * j + cw * 8 + kx];
-            r2[j] = __byte_perm(rr, rr, is_k ? 0x1010 : 0x3232);
-        }
-        if (!all_in) {
-            // a row outside the tile's keys (ratio 0) may hold any codes, e4m3's NaN among them
+        bool more = true;
+        #pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            uint32_t r2[kKeys];
             #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (r2[i / C::kBoxes] == 0) r[i] = make_uint4(0, 0, 0, 0);
-        }
-        if (!cwait(smem_u32(is_k ? &bars.k_empty[st] : &bars.v_empty[st]), par ^ 1, abort, ctrl)) return;
-        uint8_t* base = stages + st * C::kStageBytes + (is_k ? 0 : C::kKBytes);
-        // each register is refilled as soon as it is converted, a whole operand ahead of its use
-        #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int j = i / C::kBoxes;
-            if (j < kKeys / 2 || two) {
-                const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-                uint32_t h[8];
-                #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    widen4<Code>(w[e], h[2 * e], h[2 * e + 1]);
-                    h[2 * e] = mul_f16x2(h[2 * e], r2[j]);
-                    h[2 * e + 1] = mul_f16x2(h[2 * e + 1], r2[j]);
-                }
-                uint8_t* to = base + (i % C::kBoxes) * 16384 + j * 4096;
-                *reinterpret_cast<uint4*>(to + dst0) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(to + dst1) = make_uint4(h[4], h[5], h[6], h[7]);
+            for (int j = 0; j < kKeys; ++j) {
+                const uint32_t rr = s_desc[it % kDescs].ratio[32 * j + w16 + 8 * part + kx];
+                r2[j] = __byte_perm(rr, rr, pick);
             }
-            if (more) fetch(i, p0, p1, next_two);
+            if (part == 0) {
+                if (!cwait(smem_u32(&empty[st]), (it / C::kStages + 1) & 1, abort, ctrl)) return;
+            } else {
+                // the next part is the next block's first
+                if (!cwait(smem_u32(&bars.desc_full[(it + 1) % kDescs]), ((it + 1) / kDescs) & 1, abort, ctrl)) return;
+                d = lds128(smem_u32(&s_desc[(it + 1) % kDescs]));
+                more = (int)d.x >= 0;
+            }
+            if (!all_in) {
+                // a row outside the tile's keys (ratio 0) may hold any codes, e4m3's NaN among them
+                #pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (r2[i / C::kBoxes] == 0) r[i] = make_uint4(0, 0, 0, 0);
+            }
+            const uint8_t* p0 = pool + (size_t)d.x * D + (part == 0 ? 8 * D : 0);
+            const uint8_t* p1 = pool + (size_t)max((int)d.y, 0) * D + (part == 0 ? 8 * D : 0);
+            const bool next_two = (int)d.y >= 0;
+            uint8_t* base = stages + st * C::kStageBytes + part * 1024;
+            // each register is refilled as soon as it is converted
+            #pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int j = i / C::kBoxes;
+                if (j < kKeys / 2 || two) {
+                    const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+                    uint32_t h[8];
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        widen4<Code>(w[e], h[2 * e], h[2 * e + 1]);
+                        h[2 * e] = mul_f16x2(h[2 * e], r2[j]);
+                        h[2 * e + 1] = mul_f16x2(h[2 * e + 1], r2[j]);
+                    }
+                    uint8_t* to = base + (i % C::kBoxes) * 16384 + j * 4096;
+                    *reinterpret_cast<uint4*>(to + dst0) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(to + dst1) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                if (more) fetch(i, p0, p1, next_two);
+            }
         }
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(smem_u32(is_k ? &bars.k_ready[st] : &bars.v_ready[st]));
-            if (!is_k) {
-                mbar_arrive(smem_u32(&bars.desc_empty[b % kDescs]));
-                if (cw == 0) *s_blocks = (int)b + 1;   // progress, for the scheduler
-            }
+            mbar_arrive(smem_u32(&ready[st]));
+            mbar_arrive(smem_u32(&bars.desc_empty[it % kDescs]));
+            if (cw == 2) *s_blocks = (int)it + 1;   // progress, for the scheduler
         }
         if (!more) return;
-        is_k = next_k;
-        b = nb;
     }
 }
 
@@ -744,9 +735,9 @@ __global__ void __launch_bounds__(kCpThreads, 1)
     for (int i = tid; i < 2 * C::kQBytes / 16; i += kCpThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) {
         for (int s = 0; s < 4; ++s) {
-            mbar_init(smem_u32(&bars.k_ready[s]), 4);
+            mbar_init(smem_u32(&bars.k_ready[s]), 2);
             mbar_init(smem_u32(&bars.k_empty[s]), 1);
-            mbar_init(smem_u32(&bars.v_ready[s]), 4);
+            mbar_init(smem_u32(&bars.v_ready[s]), 2);
             mbar_init(smem_u32(&bars.v_empty[s]), 1);
         }
         for (int r = 0; r < kDescs; ++r) {
@@ -913,8 +904,10 @@ __global__ void __launch_bounds__(kCpThreads, 1)
             const int s = it % C::kStages;
             const bool one = npg - 2 * bk == 1;
             bool k_waited = false;
+            const bool one_half = alt && bk > 0;         // the other half has nothing to issue
+            const int h_from = one_half ? bk & 1 : 0, h_to = one_half ? h_from + 1 : 2;
             #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+            for (int h = h_from; h < h_to; ++h) {
                 const bool here = alt ? h == (bk & 1) : h < nh;
                 const uint32_t f = h ? f1 : f0;
                 if ((f & kPend) && (here || bk == 0)) {
