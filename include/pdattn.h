@@ -370,7 +370,10 @@ typedef struct {
  * Bytes of workspace for the coded calls (0 if the parameters are invalid):
  * pdattn_coded_decode of p->rows rows, pdattn_coded_prefill of up to n_tokens
  * tokens, pdattn_coded_write and pdattn_coded_read of any number.  Zero-fill
- * it once before first use.  Calls that share it must be ordered.
+ * it once before first use.  Calls that share it must be ordered; the two
+ * attention calls overwrite plans and tile lists that other calls left there
+ * (pdattn_attend then records PDATTN_EINVAL, pdattn_prefill_attend does
+ * nothing).
  */
 size_t pdattn_coded_workspace_size(const pdattn_params* p, int32_t n_tokens);
 

@@ -16,6 +16,7 @@ constexpr int kMaxGroup = 8;          // query heads per kv head (the MMA's N)
 constexpr int kChunkMax = 64;         // largest pages-per-split the planner picks
 constexpr int kItemsPerCta = 4;       // planner's target work items per persistent CTA
 constexpr uint32_t kPlanMagic = 0x70646174u;
+constexpr uint32_t kCodedPlanMagic = 0x70646163u;   // of a coded prefill: no other call runs it
 
 // Status bits in the workspace's status word.
 constexpr int kErrBadPage = 1;

@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kCpThreads, 1)
     griddep_launch_dependents();
     griddep_wait();
     const int Hk = a.kv_heads, g = a.group, Tq = a.tile_tokens / 2;
-    const int n_units = (ctrl->magic == kPlanMagic ? ctrl->n_items : 0) * Hk;
+    const int n_units = (ctrl->magic == kCodedPlanMagic ? ctrl->n_items : 0) * Hk;
     const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + ca.units);
 
     if (warp >= 8) {

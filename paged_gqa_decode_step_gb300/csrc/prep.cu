@@ -717,7 +717,7 @@ __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
         ctrl->kv_heads = a.kv_heads;
         ctrl->group = a.heads / a.kv_heads;
         ctrl->head_dim = a.head_dim;
-        ctrl->magic = kPlanMagic;
+        ctrl->magic = a.units ? kCodedPlanMagic : kPlanMagic;
     }
 }
 
@@ -952,7 +952,7 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
         ctrl->kv_heads = a.kv_heads;
         ctrl->group = a.heads / a.kv_heads;
         ctrl->head_dim = a.head_dim;
-        ctrl->magic = kPlanMagic;
+        ctrl->magic = kCodedPlanMagic;
     }
     return true;
 }

@@ -262,6 +262,20 @@ def test_an_uncoded_plan_does_not_outlive_a_coded_step():
     assert e.value.status == b.EINVAL
 
 
+@pytest.mark.parametrize("prefix,chunk", [([900, 30], [5, 3]), ([0] * 40, [300] * 40)])   # split tiles, and none
+def test_a_coded_prefills_tiles_serve_no_other_call(prefix, chunk):
+    c = cu.Case(8, 2, 64, prefix, chunk, BF16, E4M3, seed=8)
+    r = Run(c)
+    k_pool, v_pool = (torch.zeros(c.pages, 2, 64, 64, dtype=BF16, device="cuda") for _ in range(2))
+    r.check("prefill")
+    before = r.out.clone()
+    r.b.prefill_attend(r.p, r.pos, r.table, k_pool, v_pool, r.out, r.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(r.out, before)
+    r.b.check_status(r.ws)
+    r.check("prefill")
+
+
 def test_prefill_writes_outputs_aligned_to_16_bytes_only():
     c = cu.Case(8, 2, 128, [0, 90], [70, 5])
     r = Run(c)
