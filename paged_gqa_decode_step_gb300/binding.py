@@ -391,7 +391,7 @@ def _same_device(*tensors):
 
 def _check_coded(p, cache, ws, n, heads, ints, table, **named):
     """Arguments of a coded call: `named` of [n, heads, D] (heads by name), ints of [n] int32."""
-    if not isinstance(cache, CodedCache):
+    if not isinstance(cache, CodedCache) or not hasattr(cache, "_pool"):
         raise TypeError("cache must come from make_coded_cache or new_coded_cache")
     if cache._pool != (p.num_pages, p.kv_heads, 64, p.head_dim):
         raise ValueError(f"cache has pools {cache._pool}, the parameters another shape")

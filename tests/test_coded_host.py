@@ -123,6 +123,13 @@ int main(void) {
     assert got == [ctypes.sizeof(C), C.v_scale.offset, C.code.offset, C.reserved.offset, b.E4M3, b.INT8]
 
 
+def test_the_binding_wants_a_cache_that_it_made(b):
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    for cache in (_cache(b), None):                      # a bare block names no tensors and no pool shape
+        with pytest.raises(TypeError):
+            b.coded_write(_p(b), cache, x, x, x, x, x)
+
+
 @pytest.mark.parametrize("kind", [torch.float8_e4m3fn, torch.int8])
 def test_the_reference_codes(kind):
     x = torch.randn(50, 64, generator=torch.Generator().manual_seed(1))
