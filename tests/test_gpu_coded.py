@@ -174,6 +174,14 @@ def test_decode_windows_and_sinks(dtype, window):
     Run(cu.Case(16, 2, 64, [c - 1 for c in ctx], [1] * len(ctx), dtype, INT8, 1.5e5, window, sinks=True)).check("decode")
 
 
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("heads,kv_heads,D", [(4, 4, 64), (6, 3, 128), (6, 2, 64), (8, 2, 64), (10, 2, 128)])
+def test_f32_decode_of_small_groups(kind, heads, kv_heads, D):
+    # groups of up to four heads hold both f16 parts of a head in one tile, larger ones take two passes
+    ctx = [1, 17, 64, 129, 2500]
+    Run(cu.Case(heads, kv_heads, D, [c - 1 for c in ctx], [1] * len(ctx), F32, kind, 1e4, 700, sinks=True)).check("decode")
+
+
 @pytest.mark.parametrize("dtype,D,rows,ctx", [(BF16, 128, 1, 9000), (F32, 64, 1, 5001), (BF16, 64, 3, 4133)])
 def test_decode_of_long_rows_shared_by_many_ctas(dtype, D, rows, ctx):
     Run(cu.Case(2, 1, D, [ctx - 1 - 7 * i for i in range(rows)], [1] * rows, dtype, E4M3, 0.0)).check("decode")
