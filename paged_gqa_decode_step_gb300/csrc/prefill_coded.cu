@@ -8,15 +8,19 @@
 //   * Codes.  Four converter warps read a block's codes straight from the
 //     cache (contiguous pages, one block ahead, in registers) and store
 //     K' = code * r as f16 where the MMA reads it; r = scale / ref in (0, 1]
-//     with ref a power of two.  For K ref is the block's largest scale
-//     rounded up, and the block's scores are multiplied by it; for V it is
-//     the largest so far in the unit, and O is rescaled when it grows (it
-//     then travels with the running maximum's rescale).  r and code * r
-//     round to f16's 11 bits (2^-12 of the value, against 2^-9 for bf16);
-//     values under 2^-14 ref round to a step of 2^-24 ref.  Converting once
-//     per unit and block costs each SM 12 codes per clock at full MMA rate.
+//     with ref a power of two at or above the block's scales.  The block's
+//     scores are multiplied by K's ref; a row's O is in units of V's, which
+//     seldom changes along a unit.  r and code * r round to f16's 11 bits
+//     (2^-12 of the value, against 2^-9 for bf16).  Converting once per unit
+//     and block costs each SM 12 codes per clock at full MMA rate.
 //     Multiplying the scales into S and P instead would put two more
 //     instructions per score into the softmax, which bounds the kernel.
+//   * Blocks with a scale further than 2^kSpread below its ref do just that
+//     (wide_block): ratios to one ref would run out of f16's exponents, and a
+//     key that a query does not see must not take bits off those it sees.
+//     There K' and V' are the codes themselves, and a row takes its V ref from
+//     the keys it sees.  Rows that come to a block of another V ref than their
+//     own go the same way.
 //   * Types.  Q comes as f16 rows with a factor each (code_kernel), P is f16
 //     kept 2^7 above the usual scale: f16's 11 bits hold all weights above
 //     2^-21 of the largest.
@@ -34,6 +38,7 @@
 // MMAs, 2 loads Q (TMA), 3 describes the blocks (pages, refs, ratios) a few
 // ahead of their use; 4 to 7 convert; 8 to 11 and 12 to 15 are the softmax and
 // epilogue of the halves.  Waits are bounded as in prefill.cu.
+#include <cfloat>
 #include <climits>
 
 #include "coded.cuh"
@@ -47,6 +52,8 @@ constexpr int kCpThreads = 512;
 constexpr float kRescale = 8.0f;    // lazy rescale threshold (log2 units)
 constexpr float kPBias = 7.0f;      // weights are kept 2^7 up: at most 2^(kRescale + kPBias) = 2^15
 constexpr int kDescs = 8;           // ring of block descriptors, longer than any stage ring
+constexpr int kSpread = 13;         // a scale's exponent below its block's ref, at most: f16 ratios have 14 below 1
+constexpr int kRoom = 3;            // a unit's first V ref above its block's scales, in exponents
 
 template <int D>
 struct CpCfg {
@@ -96,11 +103,13 @@ struct __align__(32) UnitSlot {
 };
 
 // A block of 128 keys: the first rows of its two pages in the pools (y1 -1: one
-// page; y0 -1: the end of the work), whether the tile sees every key, the refs
-// and per key the K ratio (low half) and the V ratio.
+// page; y0 -1: the end of the work), whether the tile sees every key, the refs,
+// whether the softmax applies each key's scales (wide) in their place, and per
+// key the K ratio (low half) and the V ratio.
 struct __align__(16) BlockDesc {
     int y0, y1, all_in, pad;
-    float k_ref, v_ref, pad2[2];
+    float k_ref, v_ref;
+    int wide, pad2;
     uint32_t ratio[128];
 };
 
@@ -204,10 +213,14 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint3
 // ---------------------------------------------------------------------------
 // The block warp: descriptors of the unit stream's blocks.
 // ---------------------------------------------------------------------------
-// A scale's power of two at or above it, as a biased exponent in [1, 252].
+constexpr uint32_t kAboveZeros = 0x00800001u;   // the scale after 2^-126
+constexpr uint32_t kScaleEnd = 0x7e000000u;     // 2^125: no scale of a finite key or value reaches it
+
+// A scale's power of two at or above it, as a biased exponent in [1, 250] (finite
+// keys and values have scales of at most 2^122).
 __device__ __forceinline__ int exp_above(uint32_t bits) {
     const int e = (int)(bits >> 23) + ((bits & 0x7fffffu) != 0);
-    return min(max(e, 1), 252);
+    return min(max(e, 1), 250);
 }
 
 template <int D>
@@ -241,7 +254,7 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
             }
             return (page * Hk + kvh) * kPageSize;
         };
-        int v_exp = 1;                          // biased exponent of the unit's V ref so far
+        int v_run = 1;                          // biased exponent of the V ref before
         #pragma unroll 1
         for (int bk = 0; 2 * bk < npg; ++bk, ++n) {
             int y0 = -1, y1 = -1;
@@ -261,33 +274,65 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
                 const uint32_t m = n - kAhead;
                 if (!cwait(smem_u32(&bars.desc_empty[m % kDescs]), (m / kDescs) & 1, abort, ctrl)) return;
             }
-            const int key0 = (t.first_page + 2 * bk) * kPageSize + 4 * lane;
-            uint32_t kb[4], vb[4], kmax = 0, vmax = 0;
-            bool bad[4], in_range = true;
+            const int key0 = (t.first_page + 2 * bk) * kPageSize, key_end = key0 + (y1 >= 0 ? 128 : 64);
+            const bool all_in = key0 >= t.lo_min && key_end - 1 <= t.pos_max && y1 >= 0;
+            uint32_t kb[4], vb[4];
             #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const bool in = key0 + e >= t.lo_min && key0 + e <= t.pos_max;
-                in_range = in_range && in;
-                kb[e] = in ? __float_as_uint(ks[e]) & 0x7fffffffu : 0u;
-                vb[e] = in ? __float_as_uint(vs[e]) & 0x7fffffffu : 0u;
-                bad[e] = kb[e] >= 0x7e000000u || vb[e] >= 0x7e000000u;   // no scale of a finite key or value
-                if (bad[e]) kb[e] = vb[e] = 0u;
-                kmax = max(kmax, kb[e]);
-                vmax = max(vmax, vb[e]);
+                kb[e] = __float_as_uint(ks[e]);
+                vb[e] = __float_as_uint(vs[e]);
             }
-            kmax = __reduce_max_sync(0xffffffffu, kmax);
-            vmax = __reduce_max_sync(0xffffffffu, vmax);
+            uint32_t outside = 0, bad = 0;          // bits: this lane's keys out of range, and of no finite scale
+            if (!all_in) {
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = key0 + 4 * lane + e;
+                    if (key < t.lo_min || key > t.pos_max) {
+                        outside |= 1u << e;
+                        kb[e] = vb[e] = 0u;
+                    }
+                }
+            }
+            // largest scales, and smallest ones above 2^-126, which zeros have (they
+            // lose nothing): the difference wraps for that and for 0
+            uint32_t kmax, vmax;
+            #pragma unroll 1
+            while (true) {
+                kmax = __reduce_max_sync(0xffffffffu, max(max(kb[0], kb[1]), max(kb[2], kb[3])));
+                vmax = __reduce_max_sync(0xffffffffu, max(max(vb[0], vb[1]), max(vb[2], vb[3])));
+                if (__builtin_expect(max(kmax, vmax) < kScaleEnd, 1)) break;
+                #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (max(kb[e], vb[e]) >= kScaleEnd) {
+                        bad |= 1u << e;
+                        kb[e] = vb[e] = 0u;
+                    }
+            }
+            const uint32_t kmin = min(min(kb[0] - kAboveZeros, kb[1] - kAboveZeros), min(kb[2] - kAboveZeros, kb[3] - kAboveZeros));
+            const uint32_t vmin = min(min(vb[0] - kAboveZeros, vb[1] - kAboveZeros), min(vb[2] - kAboveZeros, vb[3] - kAboveZeros));
             const int k_exp = exp_above(kmax);
-            v_exp = max(v_exp, exp_above(vmax));
+            // V keeps the ref of the block before unless its own scales are larger or
+            // much smaller, and a new ref leaves them room to grow
+            int v_exp = exp_above(vmax);
+            v_exp = v_run >= v_exp && v_run <= v_exp + 2 * kRoom ? v_run : v_exp + kRoom;
+            v_run = v_exp;
+            const bool wide = __any_sync(0xffffffffu, kmin < (uint32_t)max(k_exp - kSpread - 1, 0) << 23 ||
+                                                          vmin < (uint32_t)max(v_exp - kSpread - 1, 0) << 23);
             const float k_down = __uint_as_float((uint32_t)(254 - k_exp) << 23);
             const float v_down = __uint_as_float((uint32_t)(254 - v_exp) << 23);
             uint32_t own[4];
             #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 own[e] = pack_f16x2(__uint_as_float(kb[e]) * k_down, __uint_as_float(vb[e]) * v_down);
-                if (bad[e]) own[e] = 0x7e00u;                             // K ratio NaN, V ratio 0
+            if (__builtin_expect(wide, 0)) {
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) own[e] = outside >> e & 1 ? 0u : 0x3c003c00u;   // the codes themselves
             }
-            const bool all_in = __all_sync(0xffffffffu, in_range);
+            if (__builtin_expect(bad != 0, 0)) {
+                #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (bad >> e & 1) own[e] = 0x7e00u;               // K ratio NaN, V ratio 0
+            }
             // The converters load one operand ahead, 16 KB: enough for L2's
             // latency but not for HBM's, so the pages go to L2 from here.
             if (lane < 4) {
@@ -298,8 +343,7 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
             *reinterpret_cast<uint4*>(d.ratio + 4 * lane) = make_uint4(own[0], own[1], own[2], own[3]);
             if (lane == 0) {
                 *reinterpret_cast<int4*>(&d) = make_int4(y0, y1, all_in ? 1 : 0, 0);
-                *reinterpret_cast<float2*>(&d.k_ref) =
-                    make_float2(__uint_as_float((uint32_t)k_exp << 23), __uint_as_float((uint32_t)v_exp << 23));
+                *reinterpret_cast<int4*>(&d.k_ref) = make_int4(k_exp << 23, v_exp << 23, wide ? 1 : 0, 0);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars.desc_full[n % kDescs]));
@@ -430,6 +474,97 @@ __device__ __forceinline__ float sink_scale(float mu, float l, bool has_sink, fl
     return f / (l * f + exp2_approx(sk - Mp));
 }
 
+// A row's softmax state: maximum and sum (as softmax_half keeps them) and the
+// V ref that its O is in units of.
+struct RowState {
+    float m, l, v_ref;
+};
+
+// The softmax of a block with the scales applied here (whole warp).  Wide: S
+// holds the products of queries and K codes, and every key's scales are read
+// from the cache, by one lane for its column; otherwise all keys have the
+// block's refs for scales.  Scores take K's in f32; a weight takes V's relative
+// to the row's V ref, a power of two at or above every V scale the row has
+// seen, on its way to f16.  Out of line and of 8 columns at a time: it must not
+// crowd the loops that other blocks run in, and a call's first such block finds
+// none of it in the caches.
+template <int D>
+__device__ __noinline__ RowState wide_block(uint32_t s_addr, uint32_t o_addr, const float* k_scale,
+                                            const float* v_scale, const BlockDesc* desc, float qf, int c_lo, int c_hi,
+                                            bool has_o, int lane, RowState st) {
+    const uint4 dy = lds128(smem_u32(desc)), dq = lds128(smem_u32(&desc->k_ref));   // y0, y1; k_ref, v_ref, wide
+    // the scales of columns 32 q4 + lane
+    auto scale_of = [&](const float* scales, uint32_t ref, int q4) {
+        const int y = (int)(q4 < 2 ? dy.x : dy.y);
+        return dq.z == 0 ? __uint_as_float(ref) : y >= 0 ? __ldcg(scales + y + (q4 & 1) * 32 + lane) : 0.f;
+    };
+    float ks = 0.f, vs = 0.f, top = -INFINITY, big = 0.f;
+    #pragma unroll 1
+    for (int c0 = 0; c0 < 128; c0 += 8) {
+        if (c0 % 32 == 0) {
+            ks = scale_of(k_scale, dq.x, c0 / 32);
+            vs = scale_of(v_scale, dq.y, c0 / 32);
+        }
+        uint32_t x[8];
+        tmem_ld8_wait(s_addr + c0, x);
+        #pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float f = fminf(qf * __shfl_sync(0xffffffffu, ks, c0 + c), FLT_MAX);
+            const float v = __shfl_sync(0xffffffffu, vs, c0 + c);
+            if (c0 + c >= c_lo && c0 + c <= c_hi) {
+                top = fmaxf(top, __fmul_rn(__uint_as_float(x[c]), f));
+                big = fmaxf(big, v);
+            }
+        }
+    }
+    float alpha = 1.f;
+    if (top > st.m + kRescale) {
+        alpha = exp2_approx(st.m - top);
+        st.m = top;
+        st.l *= alpha;
+    }
+    const float ref = fmaxf(st.v_ref, __uint_as_float((uint32_t)exp_above(__float_as_uint(big)) << 23));
+    alpha *= st.v_ref / ref;
+    st.v_ref = ref;
+    if (has_o && __any_sync(0xffffffffu, alpha != 1.f)) {
+        #pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 8) {
+            uint32_t o[8];
+            tmem_ld8_wait(o_addr + c0, o);
+            #pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st8(o_addr + c0, o);
+        }
+    }
+    const float down = 1.f / ref;
+    #pragma unroll 1
+    for (int c0 = 0; c0 < 128; c0 += 8) {
+        if (c0 % 32 == 0) {
+            ks = scale_of(k_scale, dq.x, c0 / 32);
+            vs = scale_of(v_scale, dq.y, c0 / 32);
+        }
+        uint32_t x[8];
+        float w[8];
+        tmem_ld8_wait(s_addr + c0, x);
+        #pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float f = fminf(qf * __shfl_sync(0xffffffffu, ks, c0 + c), FLT_MAX);
+            const float v = __shfl_sync(0xffffffffu, vs, c0 + c);
+            w[c] = 0.f;
+            if (c0 + c >= c_lo && c0 + c <= c_hi) {
+                // (rounded like the maximum, which then differs from itself by nothing)
+                const float p = exp2_approx(__fadd_rn(__fmul_rn(__uint_as_float(x[c]), f), -st.m) + kPBias);
+                st.l += p;
+                w[c] = p * (v * down);
+            }
+        }
+        // over columns of S that have been read
+        tmem_st4(s_addr + c0 / 2, pack_f16x2(w[0], w[1]), pack_f16x2(w[2], w[3]), pack_f16x2(w[4], w[5]),
+                 pack_f16x2(w[6], w[7]));
+    }
+    return st;
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int half, int quarter, int lane, uint32_t tmem,
                                              CpBars& bars, const BlockDesc* s_desc, volatile AltSums& s_alt,
@@ -476,7 +611,7 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
         const int pos = active ? max(pos_next, 0) : INT_MAX;
         const int lo = active && W > 0 && pos - W + 1 > 0 ? pos - W + 1 : 0;
         const float qf = f_next;
-        float m_run = -INFINITY, l = 0.f, v_ref = 1.f;
+        float m_run = -INFINITY, l = 0.f, v_ref = kScaleMin;
         const int first = alt ? half : 0, stride = alt ? 2 : 1;
         for (int b = first; b < nb; b += stride) {
             ok = cwait(s_full, ch & 1, abort, ctrl);
@@ -491,9 +626,9 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             const int di = (it + b) % kDescs;
             ok = cwait(smem_u32(&bars.desc_full[di]), ((it + b) / kDescs) & 1, abort, ctrl);
             if (!ok) break;
-            const float v_new = *reinterpret_cast<const volatile float*>(&s_desc[di].v_ref);
+            const uint4 dq = lds128(smem_u32(&s_desc[di].k_ref));      // k_ref, v_ref, wide
             // a factor that underflows keeps -inf times it at -inf
-            const float f = fmaxf(qf * *reinterpret_cast<const volatile float*>(&s_desc[di].k_ref), kScaleMin);
+            const float f = fmaxf(qf * __uint_as_float(dq.x), kScaleMin), v_blk = __uint_as_float(dq.y);
             const int pg0 = t.first_page + 2 * b, key0 = pg0 * kPageSize, npb = min(2, t.npg - 2 * b);
             // keys c of this block visible to the row: c_lo <= c <= c_hi;
             // 32-column chunks visible to every row of the warp skip the test, and
@@ -501,7 +636,22 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             const int c_lo = lo - key0, c_hi = min(pos - key0, npb * kPageSize - 1);
             // (per chunk: 0 wholly visible to the warp, 1 not, 2 wholly hidden)
             int state = 0;
-            if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 2 * kPageSize - 1)) {
+            if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 2 * kPageSize - 1 && dq.z == 0 && v_ref == v_blk)) {
+                const bool sees = active && c_hi >= max(c_lo, 0);
+                // a row takes the V ref of its first keys (its O is zero)
+                if (dq.z == 0 && (!active || (sees && m_run == -INFINITY))) v_ref = v_blk;
+                if (__any_sync(0xffffffffu, dq.z != 0 || (sees && v_ref != v_blk))) {
+                    const RowState st = wide_block<D>(s_addr, o_addr, ca.k_scale, ca.v_scale, &s_desc[di], qf, c_lo, c_hi,
+                                                      b > first, lane, RowState{m_run, l, v_ref});
+                    m_run = st.m;
+                    l = st.l;
+                    v_ref = st.v_ref;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full);
+                    continue;
+                }
                 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {
                     const int b0 = 32 * q4;
@@ -556,8 +706,6 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
                 m_run = mx;
                 l *= alpha;
             }
-            if (b > first) alpha *= v_ref / v_new;         // powers of two: exact
-            v_ref = v_new;
             if (b > first && __any_sync(0xffffffffu, alpha != 1.f)) {
                 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {

@@ -558,3 +558,48 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     assert e.value.status == ETIMEOUT
     hold.fill_(0)
     r.check("decode")
+
+
+# ---------------------------------------------------------------------------
+# keys that a token does not see
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("power", [10, 20, 24, 30, 60])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("heads,kv_heads,D,prefix,chunk,at,window,kind", [
+    (4, 1, 128, 300, 40, 335, 0, E4M3),      # a later token of the chunk; tiles of 64, cut along the keys
+    (8, 2, 64, 150, 20, 165, 0, INT8),       # tiles of one half: blocks alternate
+    (2, 2, 64, 30, 230, 100, 50, E4M3),      # the window leaves it behind inside a tile of 256
+    (16, 2, 128, 300, 30, 290, 20, INT8),    # a cached token that the last tokens' window excludes
+])
+def test_a_huge_key_or_value_leaves_the_tokens_that_do_not_see_it_alone(heads, kv_heads, D, prefix, chunk, at, window,
+                                                                        kind, which, power):
+    c = cu.Case(heads, kv_heads, D, [prefix], [chunk], BF16, kind, window=window, seed=power)
+    if at >= prefix:
+        getattr(c, which + "_new")[at - prefix] *= 2.0 ** power
+    else:
+        slot = int(c.table[0, at // 64]) * 64 + at % 64
+        getattr(c.cache, which + "s")[slot // 64, :, slot % 64] *= 2.0 ** power
+    r = Run(c)
+    r.prefill()
+    r.b.check_status(r.ws)
+    c.write()
+    c.cache.same(r.tensors)
+    want, bound = c.want("prefill")
+    # a token that sees a value 2^24 times the others' may lose the others
+    sees = (c.positions >= at) & ((c.positions < at + window) if window else torch.tensor(True))
+    held = torch.ones_like(sees) if which == "k" or power < 14 else ~sees
+    assert held.any() and not held.all() or which == "k" or power < 14
+    cu.hold(r.out[held.cuda()], want[held], bound[held])
+
+
+def test_sizes_of_keys_and_values_all_over_the_range():
+    # every token of another size; rows split, alternating and whole
+    g = torch.Generator().manual_seed(12)
+    for prefix, chunk, window in (([700], [9], 0), ([90, 0], [130, 70], 0), ([200], [150], 60)):
+        c = cu.Case(8, 2, 128, prefix, chunk, BF16, E4M3, 0.0, window)
+        c.cache.ks *= 2.0 ** torch.randint(-30, 2, c.cache.ks.shape, generator=g)
+        c.cache.vs *= 2.0 ** torch.randint(-30, 30, c.cache.vs.shape, generator=g)
+        c.k_new *= 2.0 ** torch.randint(-30, 2, c.k_new.shape[:2], generator=g)[..., None]
+        c.v_new *= 2.0 ** torch.randint(-30, 30, c.v_new.shape[:2], generator=g)[..., None]
+        c.k_new[3], c.v_new[5] = 0.0, 0.0
+        Run(c).check("prefill")
