@@ -424,7 +424,9 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
  * for.  Layouts, errors and rules are those of pdattn_prefill_paged; bf16
  * only.  The products run on f16 tensor-core tiles (codes times the ratio of
  * their scale to a power of two, 11 bits); few tokens over long rows are
- * split along the keys and merged.  Three launches, or four with the merge.
+ * split along the keys and merged.  With a window, tokens of a row that follow
+ * one another in the call and whose windows do not meet are computed apart.
+ * Three launches, or four with the merge.
  * n_tokens may be any number up to the one the workspace was sized for.
  */
 pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_cache* cache, int32_t n_tokens,

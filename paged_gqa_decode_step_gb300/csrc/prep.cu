@@ -603,6 +603,13 @@ __device__ void sort_tiles(const PfTile* raw, PfTile* tiles, int n_tiles, int* s
     __syncthreads();
 }
 
+// Coded prefill: whether the window leaves positions between two tokens of a row
+// that neither sees.  A tile starts there, so that every key in its range is one
+// that some token of it sees: other slots may hold codes that are no numbers.
+__device__ __forceinline__ bool apart(const PrefillPrepArgs& a, int p0, int p1) {
+    return a.units != 0 && a.window > 0 && (row_lo(p1, a.window) - 1 > p0 || row_lo(p0, a.window) - 1 > p1);
+}
+
 __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
     __shared__ int s_warp[32];
     __shared__ int s_off[kPfBuckets];
@@ -617,9 +624,10 @@ __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
     if (tid == 0) s_bad = 0;
 
     // 1. tile starts: a token starts a tile when it starts a run of its row
-    //    or lies a multiple of Tq tokens after its run's start; each tile's
-    //    visible positions [lo_min, pos_max] by atomics on its descriptor.
-    int carry_run = 0, n_tiles = 0, id_before = -1;
+    //    (or of its windows, see apart) or lies a multiple of Tq tokens after
+    //    its run's start; each tile's visible positions [lo_min, pos_max] by
+    //    atomics on its descriptor.
+    int carry_run = 0, n_tiles = 0, id_before = -1, pos_before = 0;
     bool bad = false;
     for (int base = 0; base < n; base += kChunk) {
         stage_chunk(a.row_of, a.positions, base, n, -1, 0, s_id, s_pos);
@@ -632,6 +640,7 @@ __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
             ps[k] = s_pos[pad_idx(tid * kPerThread + k)];
         }
         const int r_before = tid > 0 ? s_id[pad_idx(tid * kPerThread - 1)] : id_before;
+        const int p_before = tid > 0 ? s_pos[pad_idx(tid * kPerThread - 1)] : pos_before;
         unsigned run_starts = 0;
         int last_start = -1;
         #pragma unroll
@@ -640,7 +649,7 @@ __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
             if (i >= n) continue;
             if (r[k] < 0 || r[k] >= a.rows || ps[k] < 0 || ps[k] >= max_pos || (a.rope_cos && ps[k] >= a.rope_len))
                 bad = true;
-            if (i == 0 || r[k] != (k ? r[k - 1] : r_before)) {
+            if (i == 0 || r[k] != (k ? r[k - 1] : r_before) || apart(a, k ? ps[k - 1] : p_before, ps[k])) {
                 run_starts |= 1u << k;
                 last_start = i;
             }
@@ -669,6 +678,7 @@ __device__ void build_prefill_plan(const PrefillPrepArgs& a) {
             }
         }
         id_before = s_id[pad_idx(kChunk - 1)];
+        pos_before = s_pos[pad_idx(kChunk - 1)];
         __syncthreads();   // descriptors initialised before the atomics below; staging free
         int cur = first_id - 1, lmin = INT_MAX, pmax = -1;
         #pragma unroll
@@ -807,7 +817,7 @@ constexpr int kUnitTokens = kChunk, kUnitTiles = 2 * kPrepThreads;
 
 __device__ bool build_units_small(const PrefillPrepArgs& a) {
     __shared__ int s_warp[32];
-    __shared__ int s_last[kPrepThreads];
+    __shared__ int s_last[kPrepThreads], s_last_pos[kPrepThreads];
     __shared__ int s_t0[kUnitTiles + 1], s_row[kUnitTiles], s_lo[kUnitTiles], s_hi[kUnitTiles];
     __shared__ int s_off[kPfBuckets], s_order[kUnitTiles], s_sub[kUnitTiles + 1], s_slot[kUnitTiles];
     __shared__ int s_bad, s_last_split, s_tokens;
@@ -825,11 +835,15 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
         if (mine && (r[k] < 0 || r[k] >= a.rows || ps[k] < 0 || ps[k] >= max_pos || (a.rope_cos && ps[k] >= a.rope_len)))
             bad = true;
     }
-    int last = -1;
+    int last = -1, last_pos = 0;
     #pragma unroll
     for (int k = 0; k < kPerThread; ++k)
-        if (k < per && i0 + k < n) last = r[k];
+        if (k < per && i0 + k < n) {
+            last = r[k];
+            last_pos = ps[k];
+        }
     s_last[tid] = last;
+    s_last_pos[tid] = last_pos;
     for (int b = tid; b < kPfBuckets; b += kPrepThreads) s_off[b] = 0;
     if (tid == 0) { s_bad = 0; s_last_split = 0; s_tokens = 0; }
     __syncthreads();
@@ -840,7 +854,8 @@ __device__ bool build_units_small(const PrefillPrepArgs& a) {
     #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
         if (k >= per || i0 + k >= n) continue;
-        if (i0 + k == 0 || r[k] != (k ? r[k - 1] : s_last[tid - 1])) {
+        if (i0 + k == 0 || r[k] != (k ? r[k - 1] : s_last[tid - 1]) ||
+            apart(a, k ? ps[k - 1] : s_last_pos[tid - 1], ps[k])) {
             starts |= 1u << k;
             last_start = i0 + k;
         }

@@ -603,3 +603,61 @@ def test_sizes_of_keys_and_values_all_over_the_range():
         c.v_new *= 2.0 ** torch.randint(-30, 30, c.v_new.shape[:2], generator=g)[..., None]
         c.k_new[3], c.v_new[5] = 0.0, 0.0
         Run(c).check("prefill")
+
+
+def _garbage_where_nobody_looks(r):
+    """Finite garbage in every slot that no single token sees: scales of 1e30, codes that are NaN in e4m3."""
+    c = r.c
+    seen = torch.zeros(c.pages * 64, dtype=torch.bool)
+    for row, pos in zip(c.rows.tolist(), c.positions.tolist()):
+        t = torch.arange(max(0, pos - c.window + 1) if c.window > 0 else 0, pos + 1)
+        seen[c.table[row].long()[t // 64] * 64 + t % 64] = True
+    page, off = (~seen.view(c.pages, 64)).nonzero(as_tuple=True)
+    for codes, scales in ((r.tensors[0], r.tensors[2]), (r.tensors[1], r.tensors[3])):
+        codes.view(torch.uint8)[page, :, off] = 0x7f
+        scales[page, :, off] = 1e30
+
+
+def _moved(c, positions):
+    """The case with its tokens at other positions of their rows."""
+    c.positions = positions.to(torch.int32)
+    c.slots = (c.table[c.rows.long(), c.positions.long() // 64] * 64 + c.positions % 64).to(torch.int32)
+    return c
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("heads,kv_heads,order", [(8, 2, "two runs"), (8, 2, "in turn"), (2, 2, "two runs"), (2, 2, "backwards"),
+                                                  (16, 2, "three runs")])
+def test_keys_between_the_windows_of_a_rows_tokens_reach_no_output(heads, kv_heads, order, kind):
+    at = {"two runs": [*range(5, 15), *range(890, 900)], "in turn": [x for i in range(10) for x in (5 + i, 890 + i)],
+          "backwards": [*range(899, 889, -1), *range(14, 4, -1)],
+          "three runs": [*range(300, 308), *range(10, 14), *range(892, 900)]}[order]
+    outs = []
+    for dirty in (False, True):
+        r = Run(_moved(cu.Case(heads, kv_heads, 128, [880], [20], kind=kind, window=50), torch.tensor(at)))
+        if dirty:
+            _garbage_where_nobody_looks(r)
+        r.prefill()
+        r.b.check_status(r.ws)
+        outs.append(r.out)
+    assert torch.equal(*outs)
+    r.c.write()
+    want, bound = r.c.want("prefill")
+    cu.hold(r.out, want, bound)
+
+
+@pytest.mark.parametrize("rows,chunk,kv_heads,launches", [(100, 42, 1, 4), (32, 40, 64, 3)])
+def test_windows_that_leave_gaps_in_calls_of_many_tokens(rows, chunk, kv_heads, launches):
+    # more tokens than the one-pass planner takes, and a call that is not cut along the keys
+    at = torch.tensor([*range(3, 3 + chunk // 2), *range(300 - chunk // 2, 300)]).repeat(rows)
+    outs = []
+    for dirty in (False, True):
+        c = cu.Case(kv_heads, kv_heads, 64, [300 - chunk] * rows, [chunk] * rows, theta=0.0, window=40)
+        r = Run(_moved(c, at))
+        if dirty:
+            _garbage_where_nobody_looks(r)
+        r.prefill()
+        assert r.b.last_launch_count() == launches
+        r.b.check_status(r.ws)
+        outs.append(r.out)
+    assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
