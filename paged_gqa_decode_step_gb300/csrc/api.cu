@@ -1,6 +1,7 @@
 // extern "C" entry points of libpdattn: host-side validation, TMA
 // descriptors and launches.  See include/pdattn.h for the contract.
 #include <atomic>
+#include <climits>
 #include <cstdarg>
 #include <cstdio>
 #include <cmath>
@@ -739,6 +740,13 @@ static pdattn_status check_status_ws(const void* ws, size_t bytes) {
     return PDATTN_OK;
 }
 
+// Positions of a call that rotates and attends lie in the page table and in
+// the rope table; every launch of the call skips the same rows.
+static int position_limit(const pdattn_params* p) {
+    const int pages = p->pages_per_row * kPageSize;
+    return p->rope_cos && p->rope_len < pages ? p->rope_len : pages;
+}
+
 static CodeArgs code_args(const pdattn_params* p, const pdattn_coded_cache* c, int32_t n_tokens, const void* k_new,
                           const void* v_new, const int32_t* positions, void* ws) {
     CodeArgs a = {};
@@ -748,7 +756,7 @@ static CodeArgs code_args(const pdattn_params* p, const pdattn_coded_cache* c, i
     a.head_dim = p->head_dim;
     a.pages_per_row = p->pages_per_row;
     a.num_pages = p->num_pages;
-    a.rope_len = p->rope_len;
+    a.max_pos = position_limit(p);
     a.scale_log2 = scale_log2(p);
     a.k_new = k_new;
     a.v_new = v_new;
@@ -783,6 +791,7 @@ pdattn_status pdattn_coded_write(const pdattn_params* p, const pdattn_coded_cach
     if (!aligned16(k_new) || !aligned16(v_new)) return fail(PDATTN_EINVAL, "k_new and v_new must be 16-byte aligned");
     if ((s = check_status_ws(workspace, workspace_bytes)) != PDATTN_OK) return s;
     CodeArgs a = code_args(p, cache, n_tokens, k_new, v_new, positions, workspace);
+    a.max_pos = p->rope_cos ? p->rope_len : INT_MAX;      // no table is read
     a.slots = slots;
     cudaError_t e = launch_code(a, p->dtype, cache->code, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded write launch");
@@ -941,6 +950,7 @@ pdattn_status pdattn_coded_decode(const pdattn_params* p, const pdattn_coded_cac
     aa.L = L;
     aa.k_scale = cache->k_scale;
     aa.v_scale = cache->v_scale;
+    aa.max_pos = position_limit(p);
     e = launch_attend_coded(aa, km, vm, p->dtype, cache->code, grid, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded attention launch");
     g_launches = 2;

@@ -922,11 +922,11 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // 2 b + 1) and of one it carries on (slot 2 b).  All from the
             // call's inputs: no wait, no plan launch (5 us) and no work cursor.
             // (The host keeps the units under 2^30.)
-            const int R = a.rows, max_pos = a.pages_per_row * kPageSize, b = blockIdx.x;
+            const int R = a.rows, b = blockIdx.x;
             constexpr int U = C::kItemUnits;
             auto row_at = [&](int v, int* pos, int* lo) -> int {
                 *pos = v < R ? __ldg(a.positions + v) : -1;
-                if (*pos < 0 || *pos >= max_pos) return 0;
+                if (*pos < 0 || *pos >= a.max_pos) return 0;
                 *lo = row_lo(*pos, a.window);
                 return *pos / kPageSize - *lo / kPageSize + 1;
             };

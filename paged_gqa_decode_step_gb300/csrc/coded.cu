@@ -141,9 +141,7 @@ __global__ void __launch_bounds__(kCodeThreads, 5) code_kernel(const __grid_cons
     const int j0 = threadIdx.x / kLanes, step = blockDim.x / kLanes;
     if (j0 < per) load(j0);
     const int pos = __ldg(a.positions + i);
-    // a token's position must lie in the rope table, and for the attention
-    // calls in the page table
-    const bool pos_ok = pos >= 0 && (!a.rope_cos || pos < a.rope_len) && (!a.q || pos < a.pages_per_row * kPageSize);
+    const bool pos_ok = pos >= 0 && pos < a.max_pos;
     int slot = -1;
     if (pos_ok) {
         if (a.slots) {

@@ -68,6 +68,7 @@ struct AttendArgs {
     WsLayout L;
     const float* k_scale;   // coded cache: [num_pages, kv_heads, 64]; q then holds code_kernel's rows
     const float* v_scale;
+    int max_pos;            // coded cache: rows at this position or past it are skipped (position_limit)
 };
 
 struct PrefillPrepArgs {
@@ -106,7 +107,8 @@ struct PrefillArgs {
 // D more that hold what the first round off, and the row's factor (after
 // them, or in q_factor).
 struct CodeArgs {
-    int n_tokens, heads, kv_heads, head_dim, pages_per_row, num_pages, rope_len;
+    int n_tokens, heads, kv_heads, head_dim, num_pages, pages_per_row;
+    int max_pos;            // tokens at this position or past it are skipped
     int after_plan;         // 1: a programmatic dependent of a planner launch
     int q_row_bytes;
     float scale_log2;

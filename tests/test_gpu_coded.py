@@ -661,3 +661,27 @@ def test_windows_that_leave_gaps_in_calls_of_many_tokens(rows, chunk, kv_heads, 
         r.b.check_status(r.ws)
         outs.append(r.out)
     assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
+# ---------------------------------------------------------------------------
+# positions past the rope table
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_row_past_the_rope_table_is_skipped(dtype):
+    c = cu.Case(8, 2, 128, [100, 5, 200, 70], [1, 1, 1, 1], dtype)
+    r = Run(c)
+    r.check("decode")                                    # leaves every row's query in the workspace
+    g = torch.Generator().manual_seed(2)
+    c.q, c.k_new, c.v_new = (torch.randn(x.shape, generator=g).to(dtype) for x in (c.q, c.k_new, c.v_new))
+    for dst, src in ((r.q, c.q), (r.k, c.k_new), (r.v, c.v_new)):
+        dst.copy_(src)
+    r.p.rope_len = 128                                   # rows 0, 1 and 3 lie in it
+    r.out.fill_(7.0)
+    r.decode()
+    with pytest.raises(r.b.PdattnError) as e:
+        r.b.check_status(r.ws)
+    assert e.value.status == EBADPOS
+    assert (r.out[2] == 7).all()
+    keep = torch.tensor([0, 1, 3])
+    c.cache.write(cu.rope(c.k_new.float(), c.cos, c.sin, c.positions)[keep], c.v_new.float()[keep], c.slots[keep])
+    c.cache.same(r.tensors)
+    want, bound = c.want("decode")
+    cu.hold(r.out[keep.cuda()], want[keep], bound[keep])
