@@ -125,6 +125,13 @@ pdattn_status check_ws(const pdattn_params* p, void* ws, size_t bytes, int grid,
     return PDATTN_OK;
 }
 
+// Positions of a call that rotates and attends lie in the page table and in
+// the rope table; every launch of the call skips the same rows.
+int position_limit(const pdattn_params* p) {
+    const int pages = p->pages_per_row * kPageSize;
+    return p->rope_cos && p->rope_len < pages ? p->rope_len : pages;
+}
+
 PrepArgs prep_args(const pdattn_params* p, const int32_t* positions, const int32_t* table, char* ws,
                    const WsLayout& L, int grid) {
     PrepArgs a = {};
@@ -135,7 +142,7 @@ PrepArgs prep_args(const pdattn_params* p, const int32_t* positions, const int32
     a.pages_per_row = p->pages_per_row;
     a.num_pages = p->num_pages;
     a.window = p->window;
-    a.rope_len = p->rope_len;
+    a.max_pos = p->pages_per_row * kPageSize;
     a.positions = positions;
     a.table = table;
     a.rope_cos = p->rope_cos;
@@ -154,7 +161,7 @@ float scale_log2(const pdattn_params* p) {
 
 pdattn_status attend_impl(const pdattn_params* p, const void* q_rot, const int32_t* positions, const int32_t* table,
                           const void* k_pool, const void* v_pool, void* out, char* ws,
-                          const WsLayout& L, int grid, bool programmatic, cudaStream_t stream) {
+                          const WsLayout& L, int grid, int max_pos, bool programmatic, cudaStream_t stream) {
     CUtensorMap km, vm;
     pdattn_status s = make_pool_map(&km, k_pool, p);
     if (s != PDATTN_OK) return s;
@@ -178,6 +185,7 @@ pdattn_status attend_impl(const pdattn_params* p, const void* q_rot, const int32
     a.out = out;
     a.ws = ws;
     a.L = L;
+    a.max_pos = max_pos;
     cudaError_t e = launch_attend(a, km, vm, p->dtype, grid, programmatic, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
     ++g_launches;
@@ -233,6 +241,7 @@ pdattn_status pdattn_rope_write_kv(const pdattn_params* p, const void* q, const 
     a.q_out = q_out;
     a.k_pool = k_pool;
     a.v_pool = v_pool;
+    a.max_pos = position_limit(p);
     a.rope_blocks = p->rows;
     a.do_plan = 0;
     int n = 0;
@@ -286,8 +295,8 @@ pdattn_status pdattn_attend(const pdattn_params* p, const void* q_rot, const int
     WsLayout L;
     s = check_ws(p, workspace, workspace_bytes, grid, &L);
     if (s != PDATTN_OK) return s;
-    return attend_impl(p, q_rot, positions, table, k_pool, v_pool, out, static_cast<char*>(workspace), L, grid, false,
-                       (cudaStream_t)stream);
+    return attend_impl(p, q_rot, positions, table, k_pool, v_pool, out, static_cast<char*>(workspace), L, grid,
+                       p->pages_per_row * kPageSize, false, (cudaStream_t)stream);
 }
 
 pdattn_status pdattn_decode(const pdattn_params* p, const void* q_rot, const int32_t* positions, const int32_t* table,
@@ -310,8 +319,8 @@ pdattn_status pdattn_decode(const pdattn_params* p, const void* q_rot, const int
     int n = 0;
     cudaError_t e = launch_prep(a, p->dtype, (cudaStream_t)stream, &n);
     if (e != cudaSuccess) return cuda_fail(e, "plan launch");
-    s = attend_impl(p, q_rot, positions, table, k_pool, v_pool, out, static_cast<char*>(workspace), L, grid, true,
-                    (cudaStream_t)stream);
+    s = attend_impl(p, q_rot, positions, table, k_pool, v_pool, out, static_cast<char*>(workspace), L, grid, a.max_pos,
+                    true, (cudaStream_t)stream);
     if (s == PDATTN_OK) g_launches = n + 1;
     return s;
 }
@@ -341,12 +350,14 @@ pdattn_status pdattn_decode_fused(const pdattn_params* p, const void* q, const v
     a.q_out = q_rot;
     a.k_pool = k_pool;
     a.v_pool = v_pool;
+    a.max_pos = position_limit(p);
     a.rope_blocks = p->rows;
     a.do_plan = 1;
     int n = 0;
     cudaError_t e = launch_prep(a, p->dtype, (cudaStream_t)stream, &n);
     if (e != cudaSuccess) return cuda_fail(e, "plan + rope/write launches");
-    s = attend_impl(p, q_rot, positions, table, k_pool, v_pool, out, ws, L, grid, true, (cudaStream_t)stream);
+    s = attend_impl(p, q_rot, positions, table, k_pool, v_pool, out, ws, L, grid, a.max_pos, true,
+                    (cudaStream_t)stream);
     if (s == PDATTN_OK) g_launches = n + 1;
     return s;
 }
@@ -414,6 +425,7 @@ pdattn_status pdattn_decode_layers(const pdattn_params* p, int32_t n_layers, con
         PrepArgs a = prep_args(&pv, positions, table, ws, L, grid);
         a.layer_rows = p->rows;
         a.q_out = ws + L.q_rot;
+        a.max_pos = position_limit(p);
         a.rope_blocks = pv.rows;
         a.do_plan = 1;
         PrepLayers pl = {};
@@ -453,6 +465,7 @@ pdattn_status pdattn_decode_layers(const pdattn_params* p, int32_t n_layers, con
         aa.table = table;
         aa.ws = ws;
         aa.L = L;
+        aa.max_pos = a.max_pos;
         e = launch_attend_layers(aa, al, p->dtype, grid, (cudaStream_t)stream);
         if (e != cudaSuccess) return cuda_fail(e, "multi-layer attention launch");
         launches += 1;
@@ -738,13 +751,6 @@ static pdattn_status check_status_ws(const void* ws, size_t bytes) {
     if (bytes < sizeof(Ctrl))
         return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", bytes, sizeof(Ctrl));
     return PDATTN_OK;
-}
-
-// Positions of a call that rotates and attends lie in the page table and in
-// the rope table; every launch of the call skips the same rows.
-static int position_limit(const pdattn_params* p) {
-    const int pages = p->pages_per_row * kPageSize;
-    return p->rope_cos && p->rope_len < pages ? p->rope_len : pages;
 }
 
 static CodeArgs code_args(const pdattn_params* p, const pdattn_coded_cache* c, int32_t n_tokens, const void* k_new,

@@ -743,7 +743,7 @@ struct Consumer<float, D, G, Uncoded> {
 template <typename Lay>
 __device__ bool first_wave_item(const AttendArgs& a, const Lay& lay, int b, int lane, int grid, int4* d0, int4* d1) {
     constexpr bool kMulti = std::is_same<Lay, AttendLayers>::value;
-    const int Hk = a.kv_heads, max_pos = a.pages_per_row * kPageSize;
+    const int Hk = a.kv_heads, max_pos = a.max_pos;
     auto pages_of = [&](int v, int* pos_out, int* lo_out) -> int {
         const int pos = __ldg(a.positions + (kMulti ? v % a.layer_rows : v));
         if (pos < 0 || pos >= max_pos) return 0;

@@ -34,7 +34,8 @@ struct AttendLayers {
 };
 
 struct PrepArgs {
-    int rows, heads, kv_heads, head_dim, pages_per_row, num_pages, window, rope_len;
+    int rows, heads, kv_heads, head_dim, pages_per_row, num_pages, window;
+    int max_pos;            // rows at this position or past it are skipped
     int layer_rows;         // multi-layer launches: rows per layer (rows = layers x layer_rows)
     const void* q;
     const void* k_new;
@@ -68,7 +69,7 @@ struct AttendArgs {
     WsLayout L;
     const float* k_scale;   // coded cache: [num_pages, kv_heads, 64]; q then holds code_kernel's rows
     const float* v_scale;
-    int max_pos;            // coded cache: rows at this position or past it are skipped (position_limit)
+    int max_pos;            // rows at this position or past it are skipped, as the planner does
 };
 
 struct PrefillPrepArgs {

@@ -201,7 +201,7 @@ __device__ void rope_write_row(const PrepArgs& a, const Lay& lay, int row) {
     }
     const int pos = __ldg(a.positions + r);
     const bool rope = a.rope_cos != nullptr;
-    if (pos < 0 || pos >= a.pages_per_row * kPageSize || (rope && pos >= a.rope_len)) {
+    if (pos < 0 || pos >= a.max_pos) {
         if (threadIdx.x == 0) set_error(ctrl, kErrBadPos);
         return;
     }
@@ -281,7 +281,7 @@ __device__ bool build_plan_small(const PrepArgs& a, const Lay& lay) {
     __shared__ int s_warp_max[16];
     __shared__ int s_scan[32];
     __shared__ int s_chunk;
-    const int tid = threadIdx.x, R = a.rows, Hk = a.kv_heads, max_pos = a.pages_per_row * kPageSize;
+    const int tid = threadIdx.x, R = a.rows, Hk = a.kv_heads, max_pos = a.max_pos;
     if (R > (int)blockDim.x || R > kFirstWaveRows) return false;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
     int4* row_info = reinterpret_cast<int4*>(a.ws + a.L.row_info);
@@ -405,7 +405,7 @@ __device__ void build_plan(const PrepArgs& a, const Lay& lay) {
     int4* row_info = reinterpret_cast<int4*>(a.ws + a.L.row_info);
     ItemDesc* items = reinterpret_cast<ItemDesc*>(a.ws + a.L.items);
     int* merge_cnt = reinterpret_cast<int*>(a.ws + a.L.merge_cnt);
-    const int tid = threadIdx.x, R = a.rows, Hk = a.kv_heads, max_pos = a.pages_per_row * kPageSize;
+    const int tid = threadIdx.x, R = a.rows, Hk = a.kv_heads, max_pos = a.max_pos;
 
     if (tid == 0) { s_work = 0; s_slots = 0; s_longest = 0; }
     for (int i = tid; i <= kChunkMax; i += blockDim.x) s_cnt[i] = 0;
