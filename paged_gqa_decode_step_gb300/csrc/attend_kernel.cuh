@@ -325,6 +325,8 @@ struct Consumer<__nv_bfloat16, D, G, Uncoded> {
 // kLazyCoded or a scale passes 2^(e + 1) (one vote for both instead of the
 // reductions), so a weight stays under 2^(kLazyCoded + kBias + 1) = 2^15 and
 // f16 holds 11 bits of all weights down to 2^-22 of the largest possible.
+// Past kFar a score's FMA with the rounded m could leave more than a weight may
+// grow by, for a score no larger than m: there products are rounded as m was.
 // For f32 inputs the products take a second pass with what f16 rounded off
 // the query and off the weights.  Groups of at most four heads (G = 4) need no
 // second pass: a tile's eight columns hold both parts of each head, columns 2h
@@ -339,6 +341,7 @@ struct Consumer {
     static constexpr float kLazyCoded = 6.f;
     static constexpr int kBias = 8;
     static constexpr float kRMax = 1.7014118e38f;   // 2^127: scales down to 2^(kBias - 127) count in full
+    static constexpr float kFar = 4194304.f;        // 2^22
     uint32_t qf[KS][2];
     uint32_t ql[kSplit ? KS : 1][2];
     float o[KS][4];
@@ -483,11 +486,15 @@ struct Consumer {
             m0 = n0;
             m1 = n1;
             r = rn;
-            x0 = va ? fmaf(c[0], k0, -m0) : -INFINITY;
-            x2 = vb ? fmaf(c[2], k2, -m0) : -INFINITY;
+            auto above = [&](bool visible, float dot, float k, float m) {
+                const float x = fabsf(m) > kFar ? __fadd_rn(__fmul_rn(dot, k), -m) : fmaf(dot, k, -m);
+                return visible ? x : -INFINITY;
+            };
+            x0 = above(va, c[0], k0, m0);
+            x2 = above(vb, c[2], k2, m0);
             if constexpr (!kPairs) {
-                x1 = va ? fmaf(c[1], k1, -m1) : -INFINITY;
-                x3 = vb ? fmaf(c[3], k3, -m1) : -INFINITY;
+                x1 = above(va, c[1], k1, m1);
+                x3 = above(vb, c[3], k3, m1);
             }
         }
         const float e0 = exp2_approx(x0), e2 = exp2_approx(x2);

@@ -20,7 +20,8 @@
 //     key that a query does not see must not take bits off those it sees.
 //     There K' and V' are the codes themselves, and a row takes its V ref from
 //     the keys it sees.  Rows that come to a block of another V ref than their
-//     own go the same way.
+//     own, or whose scores may be too large for the exponent's FMA (kFarFactor),
+//     go the same way.
 //   * Types.  Q comes as f16 rows with a factor each (code_kernel), P is f16
 //     kept 2^7 above the usual scale: f16's 11 bits hold all weights above
 //     2^-21 of the largest.
@@ -51,6 +52,10 @@ namespace {
 constexpr int kCpThreads = 512;
 constexpr float kRescale = 8.0f;    // lazy rescale threshold (log2 units)
 constexpr float kPBias = 7.0f;      // weights are kept 2^7 up: at most 2^(kRescale + kPBias) = 2^15
+// A product of f16 query and K' is below 2^17 (elements below 2 and 448, D up to
+// 128), so a score is below 2^22 for factors up to this.  Beyond, an FMA with the
+// rounded maximum could leave more than the half by which a weight may grow.
+constexpr float kFarFactor = 32.f;
 constexpr int kDescs = 8;           // ring of block descriptors, longer than any stage ring
 constexpr int kSpread = 13;         // a scale's exponent below its block's ref, at most: f16 ratios have 14 below 1
 constexpr int kRoom = 3;            // a unit's first V ref above its block's scales, in exponents
@@ -610,7 +615,7 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
         // (a row that holds no query must not keep its warp from skipping masks)
         const int pos = active ? max(pos_next, 0) : INT_MAX;
         const int lo = active && W > 0 && pos - W + 1 > 0 ? pos - W + 1 : 0;
-        const float qf = f_next;
+        const float qf = active ? f_next : 0.f;
         float m_run = -INFINITY, l = 0.f, v_ref = kScaleMin;
         const int first = alt ? half : 0, stride = alt ? 2 : 1;
         for (int b = first; b < nb; b += stride) {
@@ -636,11 +641,11 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
             const int c_lo = lo - key0, c_hi = min(pos - key0, npb * kPageSize - 1);
             // (per chunk: 0 wholly visible to the warp, 1 not, 2 wholly hidden)
             int state = 0;
-            if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 2 * kPageSize - 1 && dq.z == 0 && v_ref == v_blk)) {
+            if (!__all_sync(0xffffffffu, c_lo <= 0 && c_hi >= 2 * kPageSize - 1 && dq.z == 0 && v_ref == v_blk && f <= kFarFactor)) {
                 const bool sees = active && c_hi >= max(c_lo, 0);
                 // a row takes the V ref of its first keys (its O is zero)
                 if (dq.z == 0 && (!active || (sees && m_run == -INFINITY))) v_ref = v_blk;
-                if (__any_sync(0xffffffffu, dq.z != 0 || (sees && v_ref != v_blk))) {
+                if (__any_sync(0xffffffffu, dq.z != 0 || (sees && v_ref != v_blk) || f > kFarFactor)) {
                     const RowState st = wide_block<D>(s_addr, o_addr, ca.k_scale, ca.v_scale, &s_desc[di], qf, c_lo, c_hi,
                                                       b > first, lane, RowState{m_run, l, v_ref});
                     m_run = st.m;

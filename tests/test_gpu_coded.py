@@ -685,3 +685,35 @@ def test_a_row_past_the_rope_table_is_skipped(dtype):
     c.cache.same(r.tensors)
     want, bound = c.want("decode")
     cu.hold(r.out[keep.cuda()], want[keep], bound[keep])
+# ---------------------------------------------------------------------------
+# scores far beyond the exponential's precision
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("power", [20, 30, 40])
+@pytest.mark.parametrize("what,dtype,kind", [("decode", BF16, E4M3), ("decode", F32, INT8), ("decode", F32, E4M3),
+                                             ("prefill", BF16, INT8)])
+def test_keys_of_any_size_pick_the_largest_score(what, dtype, kind, power):
+    heads = 8 if kind == INT8 else 4                     # f32 groups of four and of eight
+    c = cu.Case(heads, 1, 64, [100, 300], [1, 1] if what == "decode" else [9, 30], dtype, kind, 0.0, seed=power)
+    c.cache.ks *= 2.0 ** power
+    c.k_new = c.k_new * 2.0 ** power
+    r = Run(c)
+    getattr(r, what)()
+    r.b.check_status(r.ws)
+    c.write()
+    out = r.out.cpu().double()
+    assert torch.isfinite(out).all()
+    sure = 0
+    for i, (row, pos) in enumerate(zip(c.rows.tolist(), c.positions.tolist())):
+        t = torch.arange(pos + 1)
+        slots = c.table[row].long()[t // 64] * 64 + t % 64
+        k, v = (c.cache.meant(a, s, slots)[:, 0] for a, s in ((c.cache.k, c.cache.ks), (c.cache.v, c.cache.vs)))
+        s = c.q[i].double() @ k.T / 8.0
+        # q, K's ratio and code * ratio in 11 bits, f32 sums: scores closer than this may change places
+        off = 2 * (3 * 2.0 ** -11 + 72 * 2.0 ** -24) * (c.q[i].double().abs() @ k.abs().T / 8.0).amax(-1)
+        top2 = s.topk(2, -1)
+        for h in range(heads):
+            if top2.values[h, 0] - top2.values[h, 1] > off[h] + 200:      # the others' weights are nothing
+                sure += 1
+                want = v[top2.indices[h, 0]]
+                assert ((out[i, h] - want).abs() <= want.abs() * 2.0 ** -7 + 2.0 ** -20).all()
+    assert sure >= len(c.q) * heads // 2
