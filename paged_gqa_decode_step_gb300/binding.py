@@ -416,6 +416,8 @@ def _check_coded(p, cache, ws, n, heads, ints, table, **named):
                 and table.get_device() == here and table.is_contiguous()):
             _expect("table", table, shape, torch.int32)
             _same_device(table)
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("workspace must be a torch tensor")
     if cache._device != here or ws.get_device() != here or not ws.is_contiguous():
         _ws(ws)
         _same_device(cache._tensors[0], ws)

@@ -717,3 +717,44 @@ def test_keys_of_any_size_pick_the_largest_score(what, dtype, kind, power):
                 want = v[top2.indices[h, 0]]
                 assert ((out[i, h] - want).abs() <= want.abs() * 2.0 ** -7 + 2.0 ** -20).all()
     assert sure >= len(c.q) * heads // 2
+# ---------------------------------------------------------------------------
+# more of what a call may be given
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("what,dtype", [("decode", BF16), ("decode", F32), ("prefill", BF16)])
+def test_a_query_that_is_not_finite_spoils_its_own_head_only(what, dtype, value):
+    c = cu.Case(8, 2, 64, [70, 300, 10], [1, 1, 1] if what == "decode" else [20, 3, 40], dtype)
+    n = 1 if what == "decode" else 12
+    c.q[n, 5, 17] = value
+    r = Run(c)
+    getattr(r, what)()
+    r.b.check_status(r.ws)
+    out = r.out.cpu()
+    assert torch.isnan(out[n, 5]).all()
+    out[n, 5] = 0
+    assert torch.isfinite(out).all()
+
+
+def test_workspaces_of_other_types_and_wrong_ones():
+    c = cu.Case(8, 2, 128, [10], [1])
+    r = Run(c)
+    r.ws = torch.zeros(r.ws.numel() // 4, dtype=torch.int32, device="cuda")
+    r.check("decode")
+    b = r.b
+    for bad in (None, r.ws.cpu(), r.ws[::2], 7):
+        with pytest.raises((ValueError, TypeError)):
+            b.coded_decode(r.p, r.cache, r.q, r.k, r.v, r.pos, r.table, r.out, bad)
+        with pytest.raises((ValueError, TypeError)):
+            b.coded_write(r.p, r.cache, r.k, r.v, r.pos, r.slots, bad)
+
+
+@pytest.mark.parametrize("heads,kv_heads,D,prefix,chunk,split", [
+    (8, 2, 128, [0], [1], False), (4, 4, 64, [0, 10], [129, 260], False), (2, 2, 128, [3000], [2], True),
+    (8, 2, 64, [0, 2500], [40, 3], True)])
+def test_which_calls_are_cut_along_the_keys(heads, kv_heads, D, prefix, chunk, split):
+    r = Run(cu.Case(heads, kv_heads, D, prefix, chunk))
+    r.prefill()
+    assert r.b.last_launch_count() == 4                  # few tiles: they may be cut, and a merge follows
+    last_cut = int(r.ws[9 * 4:10 * 4].view(torch.int32))  # the control block's count of tiles up to the last one cut
+    r.b.check_status(r.ws)
+    assert (last_cut > 0) == split
