@@ -127,6 +127,10 @@ def make_params(rows, heads, kv_heads, head_dim, pages_per_row, num_pages, dtype
         p.rope_cos, p.rope_sin, p.rope_len = rope_cos.data_ptr(), rope_sin.data_ptr(), rope_cos.shape[0]
         # the block holds raw pointers: keep the tables alive as long as it lives
         p._tables = (rope_cos, rope_sin)
+    devices = {t.get_device() for t in (sinks, rope_cos, rope_sin) if t is not None}
+    if len(devices) > 1:
+        raise ValueError("rope tables and sinks are on different devices")
+    p._device = devices.pop() if devices else None
     return p
 
 
@@ -396,6 +400,8 @@ def _check_coded(p, cache, ws, n, heads, ints, table, **named):
     if cache._pool != (p.num_pages, p.kv_heads, 64, p.head_dim):
         raise ValueError(f"cache has pools {cache._pool}, the parameters another shape")
     here = torch.cuda.current_device()
+    if getattr(p, "_device", None) not in (None, here):
+        raise ValueError(f"rope tables or sinks are on cuda:{p._device}, the current device is cuda:{here}")
     dt, D, Hk, Hq = _dt(p), p.head_dim, p.kv_heads, p.heads
     kv, qs = (n, Hk, D), (n, Hq, D)
     # one pass over each tensor's attributes; _expect names what is wrong

@@ -130,6 +130,35 @@ def test_the_binding_wants_a_cache_that_it_made(b):
             b.coded_write(_p(b), cache, x, x, x, x, x)
 
 
+class _Table:
+    """Stands for a rope table or sinks on a device."""
+    shape = (256, 64)
+
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.mark.parametrize("what", [("rope_cos", "rope_sin"), ("sinks",)])
+def test_tables_on_another_device_are_refused(b, monkeypatch, what):
+    monkeypatch.setattr(b, "_expect", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    cache = _cache(b)
+    cache._pool, cache._device, cache._tensors = (8, 2, 64, 64), 0, ()
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    for call in (b.coded_write, b.coded_read, b.coded_decode, b.coded_prefill):
+        n = {b.coded_write: 5, b.coded_read: 4, b.coded_decode: 7, b.coded_prefill: 9}[call]
+        with pytest.raises(ValueError, match="cuda:1"):
+            call(_p(b, **{k: _Table(1) for k in what}), cache, *[x] * n)
+    with pytest.raises(ValueError, match="different devices"):
+        _p(b, rope_cos=_Table(0), rope_sin=_Table(0), sinks=_Table(1))
+
+
 @pytest.mark.parametrize("kind", [torch.float8_e4m3fn, torch.int8])
 def test_the_reference_codes(kind):
     x = torch.randn(50, 64, generator=torch.Generator().manual_seed(1))
