@@ -32,6 +32,9 @@
 //     end of a prompt) alternates: both halves hold its queries, half A takes
 //     the even blocks and half B the odd ones, so that one softmax still runs
 //     under the other half's MMAs; half A's epilogue merges the two sums.
+//   * What the coding launch writes (codes, scales, query factors) is read past
+//     L1: this grid may have started before that launch ended, so the data is
+//     not constant while it runs.
 //   * A key or value that stands for NaN makes its K' row NaN and its V' row
 //     zero: the weights of exactly the queries that see it become NaN.
 //
@@ -269,8 +272,8 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
                 if (2 * bk + 1 < npg) y1 = page_row(2 * bk + 1);
                 const int y = lane < 16 ? y0 : y1;
                 if (y >= 0) {
-                    const float4 kq = __ldg(reinterpret_cast<const float4*>(ca.k_scale + y) + (lane & 15));
-                    const float4 vq = __ldg(reinterpret_cast<const float4*>(ca.v_scale + y) + (lane & 15));
+                    const float4 kq = __ldcg(reinterpret_cast<const float4*>(ca.k_scale + y) + (lane & 15));
+                    const float4 vq = __ldcg(reinterpret_cast<const float4*>(ca.v_scale + y) + (lane & 15));
                     ks[0] = kq.x; ks[1] = kq.y; ks[2] = kq.z; ks[3] = kq.w;
                     vs[0] = vq.x; vs[1] = vq.y; vs[2] = vq.z; vs[3] = vq.w;
                 }
@@ -385,7 +388,7 @@ __device__ __forceinline__ void convert_warp(const CodedPrefillArgs& ca, int cw,
     auto fetch = [&](int i, const uint8_t* p0, const uint8_t* p1, bool two) {
         const int j = i / C::kBoxes;
         if (j < kKeys / 2 || two)
-            r[i] = __ldg(reinterpret_cast<const uint4*>((j < kKeys / 2 ? p0 : p1) + (j & 1) * 32 * D + (i % C::kBoxes) * 64));
+            r[i] = __ldcg(reinterpret_cast<const uint4*>((j < kKeys / 2 ? p0 : p1) + (j & 1) * 32 * D + (i % C::kBoxes) * 64));
     };
     if (!cwait(smem_u32(&bars.desc_full[0]), 0, abort, ctrl)) return;
     uint4 d = lds128(smem_u32(&s_desc[0]));     // y0, y1, all_in
@@ -596,7 +599,7 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
         pos_next = -1;
         if (tq < Tq && tok < tt.ntok) {
             pos_next = __ldg(a.positions + tt.t0 + tok);
-            f_next = __ldg(ca.q_factor + (size_t)(tt.t0 + tok) * a.heads + (uu % Hk) * g + jh);
+            f_next = __ldcg(ca.q_factor + (size_t)(tt.t0 + tok) * a.heads + (uu % Hk) * g + jh);
         }
     };
     if (u >= 0) row_inputs(t, u);
