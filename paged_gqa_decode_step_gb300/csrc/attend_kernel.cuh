@@ -7,25 +7,27 @@
 // attention), with the cache addressed through the page table of the paged
 // entries (llama-3.1-8b-instruct architecture page, `decode_paged`).
 //
-// Design (one persistent CTA per SM, 6 warps):
-//   * warp 5 (scheduler) takes (row, kv head, chunk) items from the plan with
-//     an atomic cursor, loads each item's descriptor and page ids, and queues
+// Design (one persistent CTA per SM; kCW consumer warps, four or, for a coded
+// cache, eight, then producer, scheduler and two epilogue warps):
+//   * the scheduler warp takes (row, kv head, chunk) items from the plan with
+//     an atomic cursor (coded cache: from its CTA's share of the rows), loads each item's descriptor and page ids, and queues
 //     them in shared memory a few items ahead, so that no global-memory
 //     latency sits between two TMA issues.
-//   * warp 4 (producer) pops items and, for every page, issues TMA loads of
+//   * the producer warp pops items and, for every page, issues TMA loads of
 //     the page's K and V tiles (64 tokens x D, 128-byte swizzled) into a ring
 //     of shared-memory stages, plus a bulk copy of the item's query group on
 //     its first page.  Full / empty mbarriers hand stages over.
-//   * warps 0-3 (consumers) each take 16 of the page's 64 tokens.  bf16:
+//   * the consumer warps each take 16 of a page's 64 tokens.  bf16:
 //     S^T = K Q^T on m16n8k16 tensor-core tiles (tokens as M, the <= 8 query
 //     heads of the group as N, so each K/V byte is read from shared memory
 //     once for the whole group), fp32 online softmax in registers, P^T moved
 //     into the B-operand layout with movmatrix, O^T += V^T P^T on the same
 //     tiles.  f32: the same dataflow on FP32 FMAs (lane per token for scores,
-//     lane per dimension for values).  Coded cache (8-bit codes): eight
-//     consumer warps, the same tiles on f16 with codes widened in registers.
-//   * at an item's last page the four warps merge their (max, sum, out)
-//     through shared memory; a single-chunk row writes its output, otherwise
+//     lane per dimension for values).  Coded cache (8-bit codes): two groups
+//     of four warps on every other page, the same tiles on f16 with codes
+//     widened in registers.
+//   * after an item's last page the epilogue warps merge the consumers'
+//     (max, sum, out); a single-chunk row writes its output, otherwise
 //     the chunk writes an fp32 partial and the last chunk to finish merges
 //     all partials of the (row, kv head) and writes the output.
 // Every mbarrier wait is bounded; a wait that runs out records
@@ -40,7 +42,7 @@
 
 namespace pdattn {
 
-// Consumer warps: four, each with 16 of a page's 64 tokens (the rows of the
+// Consumer warps of a page: four, each with 16 of its 64 tokens (the rows of the
 // bf16 MMA tile; the f32 consumer uses the same split).
 constexpr int kConsumerWarps = 4;
 constexpr int kEpilogueWarps = 2;
@@ -111,8 +113,8 @@ struct Cfg {
     static constexpr int kOffItems = kOffWarpP + kWarpPBytes;    // kItemSlots x (ItemDesc + 64 page ids)
     static constexpr int kItemBytes = (int)sizeof(ItemDesc) + kChunkMax * 4;
     // Epilogue slots: Meta, then each consumer warp's (m, l) per head and
-    // its O[head][kORow] (fp32, unnormalised); the epilogue warps merge the
-    // four warps.  Two slots per epilogue warp at head dim 64, one at 128.
+    // its O[head][kORow] (fp32, unnormalised); the epilogue warps merge
+    // them.  Two slots per epilogue warp at head dim 64, one at 128.
     static constexpr int kEpiSlots = D == 128 ? 2 : 4;
     static constexpr int kEpiHeads = kElem == 2 ? kMaxGroup : G;   // heads each warp stashes
     static constexpr int kEpiOffO = (int)sizeof(Meta) + kCW * kEpiHeads * 8;
@@ -1321,7 +1323,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             if (mt.flags & kTerm) break;
             const float2* eml = reinterpret_cast<const float2*>(ep + sizeof(Meta));   // [warp][head]
             const float* eo = reinterpret_cast<const float*>(ep + C::kEpiOffO);        // [warp][head][kORow]
-            // The four consumer warps' (m, l, o) of head j, dims d0 .. d0 + 7,
+            // The kCW consumer warps' (m, l, o) of head j, dims d0 .. d0 + 7,
             // merged: M = max m_w, L = sum e^(m_w - M) l_w, O = sum e^(m_w - M) o_w.
             auto merge4 = [&](int j, int d0, float& M, float& L, float (&O)[8]) {
                 M = kNegBig;
@@ -1488,7 +1490,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
 
         // ---- item done: this warp's (m, l, o) into the next epilogue slot,
         // with no wait on the other consumer warps (the epilogue warps merge
-        // the four); the slot is handed over once all 128 threads arrived.
+        // them); the slot is handed over once all kCW * 32 threads arrived.
         if (!mbar_wait(bar_eempty + 8 * eslot, ephase ^ 1)) {
             if (lane == 0) fail_timeout(ctrl);
             ok = false;
