@@ -123,6 +123,18 @@ int main(void) {
     assert got == [ctypes.sizeof(C), C.v_scale.offset, C.code.offset, C.reserved.offset, b.E4M3, b.INT8]
 
 
+@pytest.mark.parametrize("source", ["attend_coded.cu", "prefill_coded.cu"])
+def test_the_attention_kernels_compile_without_spills(source):
+    import re
+    from paged_gqa_decode_step_gb300 import build
+    with tempfile.TemporaryDirectory() as d:
+        r = subprocess.run([build.nvcc(), "-c", os.path.join(build.CSRC, source), "-o", os.path.join(d, "k.o"), "-Xptxas",
+                            "-v"] + build._flags(), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    spills = re.findall(r"(\d+) bytes spill stores, (\d+) bytes spill loads", r.stdout + r.stderr)
+    assert spills and all(s == ("0", "0") for s in spills), f"{source}: register spills {spills}"
+
+
 def test_the_binding_wants_a_cache_that_it_made(b):
     x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
     for cache in (_cache(b), None):                      # a bare block names no tensors and no pool shape
