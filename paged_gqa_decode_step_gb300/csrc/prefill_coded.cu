@@ -7,10 +7,10 @@
 //
 //   * Codes.  Four converter warps read a block's codes straight from the
 //     cache (contiguous pages, one block ahead, in registers) and store
-//     K' = code * r as f16 where the MMA reads it; r = scale / ref in (0, 1]
-//     with ref a power of two at or above the block's scales.  The block's
+//     K' = code * r as f16 where the MMA reads it; r = scale / ref in (0, 2^7]
+//     with ref a power of two (448 * 2^7 is an f16).  The block's
 //     scores are multiplied by K's ref; a row's O is in units of V's, which
-//     seldom changes along a unit.  r and code * r round to f16's 11 bits
+//     seldom changes along a unit (O is rescaled when it grows).  r and code * r round to f16's 11 bits
 //     (2^-12 of the value, against 2^-9 for bf16).  Converting once per unit
 //     and block costs each SM 12 codes per clock at full MMA rate.
 //     Multiplying the scales into S and P instead would put two more
@@ -18,10 +18,10 @@
 //   * Blocks with a scale further than 2^kSpread below its ref do just that
 //     (wide_block): ratios to one ref would run out of f16's exponents, and a
 //     key that a query does not see must not take bits off those it sees.
-//     There K' and V' are the codes themselves, and a row takes its V ref from
-//     the keys it sees.  Rows that come to a block of another V ref than their
-//     own, or whose scores may be too large for the exponent's FMA (kFarFactor),
-//     go the same way.
+//     There K' and V' are the codes (V' times 2^7), and a row takes its V ref
+//     from the keys it sees.  Rows that come to a block of a lower V ref than
+//     their own, or whose scores may be too large for the exponent's FMA
+//     (kFarFactor), go the same way.
 //   * Types.  Q comes as f16 rows with a factor each (code_kernel), P is f16
 //     kept 2^7 above the usual scale: f16's 11 bits hold all weights above
 //     2^-21 of the largest.
@@ -55,13 +55,16 @@ namespace {
 constexpr int kCpThreads = 512;
 constexpr float kRescale = 8.0f;    // lazy rescale threshold (log2 units)
 constexpr float kPBias = 7.0f;      // weights are kept 2^7 up: at most 2^(kRescale + kPBias) = 2^15
-// A product of f16 query and K' is below 2^17 (elements below 2 and 448, D up to
-// 128), so a score is below 2^22 for factors up to this.  Beyond, an FMA with the
-// rounded maximum could leave more than the half by which a weight may grow.
-constexpr float kFarFactor = 32.f;
+// A product of f16 query and K' is below 2^24 (elements below 2 and 448 * 2^7, D
+// up to 128), so a score is below 2^22 for factors up to this.  Beyond, an FMA
+// with the rounded maximum could leave more than the half by which a weight may
+// grow.
+constexpr float kFarFactor = 0.25f;
 constexpr int kDescs = 8;           // ring of block descriptors, longer than any stage ring
 constexpr int kSpread = 13;         // a scale's exponent below its block's ref, at most: f16 ratios have 14 below 1
-constexpr int kRoom = 3;            // a unit's first V ref above its block's scales, in exponents
+constexpr int kUp = 7;              // ratios reach 2^kUp
+constexpr float kVWide = 128.f;     // V ratio of a wide block, so that its rows' refs are like those of others
+constexpr int kRoom = 3;            // room that a unit's first V ref leaves, in exponents
 
 template <int D>
 struct CpCfg {
@@ -224,11 +227,12 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint3
 constexpr uint32_t kAboveZeros = 0x00800001u;   // the scale after 2^-126
 constexpr uint32_t kScaleEnd = 0x7e000000u;     // 2^125: no scale of a finite key or value reaches it
 
-// A scale's power of two at or above it, as a biased exponent in [1, 250] (finite
-// keys and values have scales of at most 2^122).
-__device__ __forceinline__ int exp_above(uint32_t bits) {
+// The lowest ref for a scale, 2^-kUp of the power of two at or above it, as a
+// biased exponent in [1, 243] (finite keys and values have scales of at most
+// 2^122).
+__device__ __forceinline__ int ref_exp(uint32_t bits) {
     const int e = (int)(bits >> 23) + ((bits & 0x7fffffu) != 0);
-    return min(max(e, 1), 250);
+    return min(max(e - kUp, 1), 243);
 }
 
 template <int D>
@@ -318,14 +322,20 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
             }
             const uint32_t kmin = min(min(kb[0] - kAboveZeros, kb[1] - kAboveZeros), min(kb[2] - kAboveZeros, kb[3] - kAboveZeros));
             const uint32_t vmin = min(min(vb[0] - kAboveZeros, vb[1] - kAboveZeros), min(vb[2] - kAboveZeros, vb[3] - kAboveZeros));
-            const int k_exp = exp_above(kmax);
+            const int k_exp = ref_exp(kmax);
             // V keeps the ref of the block before unless its own scales are larger or
-            // much smaller, and a new ref leaves them room to grow
-            int v_exp = exp_above(vmax);
-            v_exp = v_run >= v_exp && v_run <= v_exp + 2 * kRoom ? v_run : v_exp + kRoom;
+            // the smallest much smaller; a new ref leaves them room to grow
+            const int v_own = ref_exp(vmax);
+            int v_exp = v_run >= v_own ? v_run : v_own + kRoom;
+            auto far_below = [&](uint32_t least, int ref) { return least < (uint32_t)max(ref - kSpread - 1, 0) << 23; };
+            bool wide = __any_sync(0xffffffffu, far_below(kmin, k_exp) || far_below(vmin, v_exp));
+            if (__builtin_expect(wide, 0)) {
+                // the highest ref that V's smallest scale allows, if it serves the largest
+                const int most = (int)((__reduce_min_sync(0xffffffffu, vmin) + kAboveZeros) >> 23) + kSpread - 1;
+                if (most >= v_own) v_exp = min(v_exp, most);
+                wide = __any_sync(0xffffffffu, far_below(kmin, k_exp) || far_below(vmin, v_exp));
+            }
             v_run = v_exp;
-            const bool wide = __any_sync(0xffffffffu, kmin < (uint32_t)max(k_exp - kSpread - 1, 0) << 23 ||
-                                                          vmin < (uint32_t)max(v_exp - kSpread - 1, 0) << 23);
             const float k_down = __uint_as_float((uint32_t)(254 - k_exp) << 23);
             const float v_down = __uint_as_float((uint32_t)(254 - v_exp) << 23);
             uint32_t own[4];
@@ -334,7 +344,7 @@ __device__ __forceinline__ void block_warp(const CodedPrefillArgs& ca, int lane,
                 own[e] = pack_f16x2(__uint_as_float(kb[e]) * k_down, __uint_as_float(vb[e]) * v_down);
             if (__builtin_expect(wide, 0)) {
                 #pragma unroll
-                for (int e = 0; e < 4; ++e) own[e] = outside >> e & 1 ? 0u : 0x3c003c00u;   // the codes themselves
+                for (int e = 0; e < 4; ++e) own[e] = outside >> e & 1 ? 0u : 0x58003c00u;   // K 1, V kVWide
             }
             if (__builtin_expect(bad != 0, 0)) {
                 #pragma unroll
@@ -488,12 +498,26 @@ struct RowState {
     float m, l, v_ref;
 };
 
+// Multiplies the rows' O by a factor each, where that seldom comes (whole warp).
+template <int D>
+__device__ __noinline__ void scale_o(uint32_t o_addr, float f) {
+    #pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 8) {
+        uint32_t o[8];
+        tmem_ld8_wait(o_addr + c0, o);
+        #pragma unroll
+        for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+        tmem_st8(o_addr + c0, o);
+    }
+    tmem_wait_st();
+}
+
 // The softmax of a block with the scales applied here (whole warp).  Wide: S
 // holds the products of queries and K codes, and every key's scales are read
 // from the cache, by one lane for its column; otherwise all keys have the
 // block's refs for scales.  Scores take K's in f32; a weight takes V's relative
-// to the row's V ref, a power of two at or above every V scale the row has
-// seen, on its way to f16.  Out of line and of 8 columns at a time: it must not
+// to the row's V ref, at least what every V scale that the row has seen takes, on
+// its way to f16.  Out of line and of 8 columns at a time: it must not
 // crowd the loops that other blocks run in, and a call's first such block finds
 // none of it in the caches.
 template <int D>
@@ -502,16 +526,17 @@ __device__ __noinline__ RowState wide_block(uint32_t s_addr, uint32_t o_addr, co
                                             bool has_o, int lane, RowState st) {
     const uint4 dy = lds128(smem_u32(desc)), dq = lds128(smem_u32(&desc->k_ref));   // y0, y1; k_ref, v_ref, wide
     // the scales of columns 32 q4 + lane
-    auto scale_of = [&](const float* scales, uint32_t ref, int q4) {
+    const float k_blk = __uint_as_float(dq.x), v_blk = __uint_as_float(dq.y) * kVWide;
+    auto scale_of = [&](const float* scales, float ref, int q4) {
         const int y = (int)(q4 < 2 ? dy.x : dy.y);
-        return dq.z == 0 ? __uint_as_float(ref) : y >= 0 ? __ldcg(scales + y + (q4 & 1) * 32 + lane) : 0.f;
+        return dq.z == 0 ? ref : y >= 0 ? __ldcg(scales + y + (q4 & 1) * 32 + lane) : 0.f;
     };
     float ks = 0.f, vs = 0.f, top = -INFINITY, big = 0.f;
     #pragma unroll 1
     for (int c0 = 0; c0 < 128; c0 += 8) {
         if (c0 % 32 == 0) {
-            ks = scale_of(k_scale, dq.x, c0 / 32);
-            vs = scale_of(v_scale, dq.y, c0 / 32);
+            ks = scale_of(k_scale, k_blk, c0 / 32);
+            vs = scale_of(v_scale, v_blk, c0 / 32);
         }
         uint32_t x[8];
         tmem_ld8_wait(s_addr + c0, x);
@@ -531,25 +556,16 @@ __device__ __noinline__ RowState wide_block(uint32_t s_addr, uint32_t o_addr, co
         st.m = top;
         st.l *= alpha;
     }
-    const float ref = fmaxf(st.v_ref, __uint_as_float((uint32_t)exp_above(__float_as_uint(big)) << 23));
+    const float ref = fmaxf(st.v_ref, __uint_as_float((uint32_t)ref_exp(__float_as_uint(big)) << 23));
     alpha *= st.v_ref / ref;
     st.v_ref = ref;
-    if (has_o && __any_sync(0xffffffffu, alpha != 1.f)) {
-        #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 8) {
-            uint32_t o[8];
-            tmem_ld8_wait(o_addr + c0, o);
-            #pragma unroll
-            for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tmem_st8(o_addr + c0, o);
-        }
-    }
-    const float down = 1.f / ref;
+    if (has_o && __any_sync(0xffffffffu, alpha != 1.f)) scale_o<D>(o_addr, alpha);
+    const float down = 1.f / (ref * kVWide);
     #pragma unroll 1
     for (int c0 = 0; c0 < 128; c0 += 8) {
         if (c0 % 32 == 0) {
-            ks = scale_of(k_scale, dq.x, c0 / 32);
-            vs = scale_of(v_scale, dq.y, c0 / 32);
+            ks = scale_of(k_scale, k_blk, c0 / 32);
+            vs = scale_of(v_scale, v_blk, c0 / 32);
         }
         uint32_t x[8];
         float w[8];
@@ -648,17 +664,22 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
                 const bool sees = active && c_hi >= max(c_lo, 0);
                 // a row takes the V ref of its first keys (its O is zero)
                 if (dq.z == 0 && (!active || (sees && m_run == -INFINITY))) v_ref = v_blk;
-                if (__any_sync(0xffffffffu, dq.z != 0 || (sees && v_ref != v_blk) || f > kFarFactor)) {
-                    const RowState st = wide_block<D>(s_addr, o_addr, ca.k_scale, ca.v_scale, &s_desc[di], qf, c_lo, c_hi,
-                                                      b > first, lane, RowState{m_run, l, v_ref});
-                    m_run = st.m;
-                    l = st.l;
-                    v_ref = st.v_ref;
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full);
-                    continue;
+                const bool apply = dq.z != 0 || f > kFarFactor, other = sees && v_ref != v_blk;
+                if (__any_sync(0xffffffffu, apply || other)) {
+                    if (__any_sync(0xffffffffu, apply || (other && v_ref > v_blk))) {
+                        const RowState st = wide_block<D>(s_addr, o_addr, ca.k_scale, ca.v_scale, &s_desc[di], qf, c_lo,
+                                                          c_hi, b > first, lane, RowState{m_run, l, v_ref});
+                        m_run = st.m;
+                        l = st.l;
+                        v_ref = st.v_ref;
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full);
+                        continue;
+                    }
+                    if (b > first) scale_o<D>(o_addr, other ? v_ref / v_blk : 1.f);   // powers of two: exact
+                    if (other) v_ref = v_blk;
                 }
                 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {

@@ -758,3 +758,16 @@ def test_which_calls_are_cut_along_the_keys(heads, kv_heads, D, prefix, chunk, s
     last_cut = int(r.ws[9 * 4:10 * 4].view(torch.int32))  # the control block's count of tiles up to the last one cut
     r.b.check_status(r.ws)
     assert (last_cut > 0) == split
+
+
+@pytest.mark.parametrize("spread", [9, 14, 19, 22])
+@pytest.mark.parametrize("heads,kv_heads,D,prefix,chunk,window", [(4, 1, 128, [1500], [6], 0), (8, 1, 64, [700], [70], 0),
+                                                                 (2, 2, 128, [200, 40], [300, 5], 90)])
+def test_scales_that_lie_far_apart(heads, kv_heads, D, prefix, chunk, window, spread):
+    # up to where ratios still hold them, at the border and past it; whole blocks of larger and smaller ones
+    g = torch.Generator().manual_seed(spread)
+    c = cu.Case(heads, kv_heads, D, prefix, chunk, BF16, INT8, 0.0, window)
+    for scales in (c.cache.ks, c.cache.vs):
+        scales *= 2.0 ** torch.randint(-spread, 1, scales.shape, generator=g)
+    c.cache.vs *= 2.0 ** torch.randint(-8, 9, c.cache.vs.shape[:1], generator=g)[:, None, None]
+    Run(c).check("prefill")
