@@ -56,10 +56,10 @@ constexpr int kCpThreads = 512;
 constexpr float kRescale = 8.0f;    // lazy rescale threshold (log2 units)
 constexpr float kPBias = 7.0f;      // weights are kept 2^7 up: at most 2^(kRescale + kPBias) = 2^15
 // A product of f16 query and K' is below 2^24 (elements below 2 and 448 * 2^7, D
-// up to 128), so a score is below 2^22 for factors up to this.  Beyond, an FMA
-// with the rounded maximum could leave more than the half by which a weight may
-// grow.
-constexpr float kFarFactor = 0.25f;
+// up to 128), so a score is below 2^23 for factors up to this.  Beyond, an FMA
+// with the rounded maximum could leave more than the half by which a weight's
+// exponent may grow (2^16 is no f16).
+constexpr float kFarFactor = 0.5f;
 constexpr int kDescs = 8;           // ring of block descriptors, longer than any stage ring
 constexpr int kSpread = 13;         // a scale's exponent below its block's ref, at most: f16 ratios have 14 below 1
 constexpr int kUp = 7;              // ratios reach 2^kUp
