@@ -15,8 +15,9 @@
 // f16 row holds what the first one rounds off.
 //
 // Bound by the latency of the loads: position, slot and rope row one after the
-// other (8192 tokens, 8 kv heads of 128, bf16: 55 MB in 18.4 us, of measured
-// copy bandwidth 0.44; issue slots half used).
+// other (8192 tokens, 8 kv heads of 128, bf16: 55 MB in 17.8 us, of measured
+// copy bandwidth 0.45; issue slots half used).  48 registers a thread, for five
+// blocks per SM, spill some (24 bytes stored for bf16, 120 for f32).
 #include <type_traits>
 
 #include "coded.cuh"
@@ -321,9 +322,12 @@ static cudaError_t by_types(int dtype, int D, int code, F f) {
 
 cudaError_t launch_code(const CodeArgs& a, int dtype, int code, cudaStream_t stream) {
     // As many lanes as the token's vectors can use, in whole warps; with many
-    // tokens blocks of 64 threads, which come and go one by one (8192 cold
-    // tokens of 16 vectors: 64 threads 20.5 us, 128 24.6), with few all of the
-    // token's vectors at once.
+    // tokens blocks of 64 threads, which come and go one by one, with few all of
+    // the token's vectors at once.  Up to 2048 tokens the call hides the
+    // difference (8 kv heads of 128, bf16: 512 tokens 8.3 us with 64 threads and
+    // 8.5 with 256, 2048 tokens 8.1 and 8.8); 8192 take 17.8 and 20.2 us.  For
+    // f32 it is the other way round (4096 tokens of 12 heads of 64: 12.3 and
+    // 10.3 us).
     const long long most = a.n_tokens >= 1024 ? 64 : kCodeThreads;
     const long long lanes = (long long)((a.q ? a.heads : 0) + 2 * a.kv_heads) * (a.head_dim / 16);
     cudaLaunchConfig_t cfg = {};
