@@ -762,7 +762,7 @@ static CodeArgs code_args(const pdattn_params* p, const pdattn_coded_cache* c, i
     a.head_dim = p->head_dim;
     a.pages_per_row = p->pages_per_row;
     a.num_pages = p->num_pages;
-    a.max_pos = position_limit(p);
+    a.last_pos = position_limit(p) - 1;
     a.scale_log2 = scale_log2(p);
     a.k_new = k_new;
     a.v_new = v_new;
@@ -797,7 +797,7 @@ pdattn_status pdattn_coded_write(const pdattn_params* p, const pdattn_coded_cach
     if (!aligned16(k_new) || !aligned16(v_new)) return fail(PDATTN_EINVAL, "k_new and v_new must be 16-byte aligned");
     if ((s = check_status_ws(workspace, workspace_bytes)) != PDATTN_OK) return s;
     CodeArgs a = code_args(p, cache, n_tokens, k_new, v_new, positions, workspace);
-    a.max_pos = p->rope_cos ? p->rope_len : INT_MAX;      // no table is read
+    a.last_pos = p->rope_cos ? p->rope_len - 1 : INT_MAX;      // no page table is read
     a.slots = slots;
     cudaError_t e = launch_code(a, p->dtype, cache->code, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "coded write launch");

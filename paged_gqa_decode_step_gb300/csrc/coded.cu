@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kCodeThreads, 5) code_kernel(const __grid_cons
     const int j0 = threadIdx.x / kLanes, step = blockDim.x / kLanes;
     if (j0 < per) load(j0);
     const int pos = __ldg(a.positions + i);
-    const bool pos_ok = pos >= 0 && pos < a.max_pos;
+    const bool pos_ok = pos >= 0 && pos <= a.last_pos;
     int slot = -1;
     if (pos_ok) {
         if (a.slots) {

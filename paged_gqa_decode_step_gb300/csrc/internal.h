@@ -109,7 +109,7 @@ struct PrefillArgs {
 // them, or in q_factor).
 struct CodeArgs {
     int n_tokens, heads, kv_heads, head_dim, num_pages, pages_per_row;
-    int max_pos;            // tokens at this position or past it are skipped
+    int last_pos;           // tokens past this position are skipped
     int after_plan;         // 1: a programmatic dependent of a planner launch
     int q_row_bytes;
     float scale_log2;

@@ -771,3 +771,13 @@ def test_scales_that_lie_far_apart(heads, kv_heads, D, prefix, chunk, window, sp
         scales *= 2.0 ** torch.randint(-spread, 1, scales.shape, generator=g)
     c.cache.vs *= 2.0 ** torch.randint(-8, 9, c.cache.vs.shape[:1], generator=g)[:, None, None]
     Run(c).check("prefill")
+
+
+def test_a_write_without_rotation_takes_any_position():
+    c = cu.Case(2, 2, 64, [0], [3], theta=0.0)
+    r = Run(c)
+    pos = torch.tensor([0, 10 ** 9, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    r.b.coded_write(r.p, r.cache, r.k, r.v, pos, r.slots, r.ws)
+    r.b.check_status(r.ws)
+    c.write()
+    c.cache.same(r.tensors)
