@@ -26,7 +26,7 @@
 //     kept 2^7 above the usual scale: f16's 11 bits hold all weights above
 //     2^-21 of the largest.
 //   * Long rows in few tiles are split along their keys (the planner's
-//     sub-tiles): a piece writes its unnormalised O, maximum and sum, and a
+//     sub-tiles): a piece writes its own output, maximum and sum, and a
 //     second kernel merges them.
 //   * A tile that fits one half (up to 128 / g tokens: drafted tokens, the
 //     end of a prompt) alternates: both halves hold its queries, half A takes
@@ -824,12 +824,11 @@ __device__ __forceinline__ void softmax_half(const CodedPrefillArgs& ca, int hal
                 const int h = kvh * g + jh;
                 float sk = 0.f;
                 if (sinks != nullptr && active && t.pad == 0) sk = __bfloat162float(sinks[h]) * 1.4426950408889634f;
-                if (t.pad == 0) {
-                    const float inv = sink_scale(M, L, sinks != nullptr, sk);
-                    fa *= inv;
-                    fb *= inv;
-                }
-                // a piece of a split tile leaves its unnormalised O, maximum and sum
+                // a piece of a split tile leaves its own output (an unnormalised one
+                // could leave f32), maximum and sum
+                const float inv = sink_scale(M, L, t.pad == 0 && sinks != nullptr, sk);
+                fa *= inv;
+                fb *= inv;
                 const size_t at = ((size_t)(t.pad - 1) * Hk + kvh) * ca.slot_rows + tok * g + jh;
                 if (t.pad != 0 && active) ca.part_ml[at] = make_float2(M, L);
                 __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + tok) * a.heads + h) * D;
@@ -1168,7 +1167,7 @@ __global__ void __launch_bounds__(kCpThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of split tiles: out = sum_c 2^(mu_c - M) o_c / sum_c 2^(mu_c - M) l_c
+// Merge of split tiles: out = sum_c w_c o_c / sum_c w_c, w_c = 2^(mu_c - M) l_c,
 // over a tile's pieces, with the sink's share of the denominator.  A warp
 // takes a row of a (tile, kv head), a lane D / 32 dimensions.
 // ---------------------------------------------------------------------------
@@ -1206,15 +1205,17 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Code
                 x[0] = v.x; x[1] = v.y;
             }
             const float Mn = fmaxf(M, ml.x);
-            const float fa = exp2_approx(M - Mn), fc = exp2_approx(ml.x - Mn);
+            const float fa = exp2_approx(M - Mn), fc = exp2_approx(ml.x - Mn) * ml.y;
+            const float fo = L * fa;
             M = Mn;
-            L = L * fa + fc * ml.y;
+            L = fo + fc;
+            const float inv = L == 0.f ? 0.f : 1.f / L;      // O stays an average
             #pragma unroll
-            for (int e = 0; e < N; ++e) O[e] = O[e] * fa + fc * x[e];
+            for (int e = 0; e < N; ++e) O[e] = O[e] * (fo * inv) + x[e] * (fc * inv);
         }
         const int h = kvh * g + r % g;
         const float sk = sinks != nullptr ? __bfloat162float(sinks[h]) * 1.4426950408889634f : 0.f;
-        const float inv = sink_scale(M, L, sinks != nullptr, sk);
+        const float inv = L * sink_scale(M, L, sinks != nullptr, sk);
         __nv_bfloat16* dst =
             static_cast<__nv_bfloat16*>(a.out) + ((size_t)(t.t0 + r / g) * a.heads + h) * D + lane * N;
         if constexpr (N == 4)

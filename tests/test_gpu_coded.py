@@ -781,3 +781,11 @@ def test_a_write_without_rotation_takes_any_position():
     r.b.check_status(r.ws)
     c.write()
     c.cache.same(r.tensors)
+
+
+@pytest.mark.parametrize("what,prefix,chunk", [("prefill", [3000], [2]), ("prefill", [300], [40]), ("decode", [3000], [1])])
+def test_values_near_the_end_of_the_range(what, prefix, chunk):
+    # values of 2^124: outputs are averages of values, and no sum on the way may leave f32
+    c = cu.Case(2, 2, 128, prefix, chunk, BF16, E4M3, 0.0, seed=1)
+    c.cache.vs[:, :, ::7] = 2.0 ** 115
+    Run(c).check(what)
