@@ -789,3 +789,57 @@ def test_values_near_the_end_of_the_range(what, prefix, chunk):
     c = cu.Case(2, 2, 128, prefix, chunk, BF16, E4M3, 0.0, seed=1)
     c.cache.vs[:, :, ::7] = 2.0 ** 115
     Run(c).check(what)
+
+
+@pytest.mark.parametrize("what,prefix,chunk", [("prefill", [8000], [2]), ("prefill", [9, 2000], [70, 130]), ("decode", [8000], [1])])
+def test_values_near_the_lower_end_of_the_range(what, prefix, chunk):
+    # values of about 2^-110: averages of many of them are still normal numbers
+    c = cu.Case(2, 2, 64, prefix, chunk, BF16, E4M3, 0.0, seed=1)
+    c.cache.vs.fill_(2.0 ** -118)
+    c.v_new = c.v_new * 2.0 ** -112
+    Run(c).check(what)
+
+
+def test_prefills_on_two_streams_at_once():
+    cases = [cu.Case(8, 2, 128, [900, 30], [5, 200], seed=i, window=(0, 70)[i]) for i in range(2)]
+    runs = [Run(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for r, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                r.prefill()
+    torch.cuda.synchronize()
+    for r in runs:
+        r.b.check_status(r.ws)
+        r.c.write()
+        r.c.cache.same(r.tensors)
+        want, bound = r.c.want("prefill")
+        cu.hold(r.out, want, bound)
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Captured calls of both kinds on one workspace, replayed in turn in both orders."""
+    pre, dec = cu.Case(8, 2, 128, [300, 20], [6, 90]), cu.Case(8, 2, 128, [700, 64], [1, 1], seed=2)
+    runs = [(Run(pre), "prefill"), (Run(dec), "decode")]
+    ws = max((r.ws for r, _ in runs), key=lambda t: t.numel())
+    graphs = []
+    for r, kind in runs:
+        r.ws = ws
+        getattr(r, kind)()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            getattr(r, kind)()
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+        for r, _ in runs:
+            r.out.fill_(0)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for r, kind in runs:
+            r.b.check_status(ws)
+            r.c.write()
+            want, bound = r.c.want(kind)
+            cu.hold(r.out, want, bound, f"{kind} {order}")
