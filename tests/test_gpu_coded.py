@@ -843,3 +843,20 @@ def test_two_graphs_that_share_a_workspace():
             r.c.write()
             want, bound = r.c.want(kind)
             cu.hold(r.out, want, bound, f"{kind} {order}")
+
+
+@pytest.mark.parametrize("which", ["k_new", "v_new"])
+def test_a_non_finite_token_beside_a_huge_one(which):
+    c = cu.Case(8, 2, 128, [70], [30])
+    getattr(c, which)[9, 1, 3] = math.nan
+    c.v_new[20] *= 2.0 ** 60
+    c.k_new[25] *= 2.0 ** 30
+    r = Run(c)
+    r.prefill()
+    r.b.check_status(r.ws)
+    out = r.out.cpu()
+    assert torch.isfinite(out[:, :4]).all() and torch.isfinite(out[:9]).all() and torch.isnan(out[9:, 4:]).all()
+    c.write()
+    want, bound = c.want("prefill")
+    cu.hold(out[:9], want[:9], bound[:9])
+    cu.hold(out[:20, :4], want[:20, :4], bound[:20, :4])
