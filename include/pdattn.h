@@ -350,8 +350,9 @@ pdattn_status pdattn_packed_attend(const pdattn_params* p, int32_t n_tokens, con
  * not used.  Codes and scales are 16-byte aligned.  Codes and scales that no
  * call has written may hold anything where no output sees them.
  *
- * A value whose V scale is more than 2^14 below the largest V scale that its
- * token sees loses bits (2^-24 of that largest scale is the finest step).
+ * A value whose V scale is more than 2^14 (for f32: 2^10) below the largest V
+ * scale that its token sees loses bits (2^-24 of that largest scale is the
+ * finest step).
  * Keys and values that a token does not see take nothing from its output,
  * whatever their size.
  */
