@@ -8,12 +8,12 @@
 //   * Codes.  Four converter warps read a block's codes straight from the
 //     cache (contiguous pages, one block ahead, in registers) and store
 //     K' = code * r as f16 where the MMA reads it; r = scale / ref in (0, 2^7]
-//     with ref a power of two (448 * 2^7 is an f16).  The block's
-//     scores are multiplied by K's ref; a row's O is in units of V's, which
-//     seldom changes along a unit (O is rescaled when it grows).  r and code * r round to f16's 11 bits
-//     (2^-12 of the value, against 2^-9 for bf16).  Converting once per unit
-//     and block costs each SM 12 codes per clock at full MMA rate.
-//     Multiplying the scales into S and P instead would put two more
+//     with ref a power of two (448 * 2^7 is an f16).  The block's scores are
+//     multiplied by K's ref; a row's O is in units of V's, which seldom changes
+//     along a unit (O is rescaled when it grows).  r and code * r round to
+//     f16's 11 bits (2^-12 of the value, against 2^-9 for bf16).  Converting
+//     once per unit and block costs each SM 12 codes per clock at full MMA
+//     rate.  Multiplying the scales into S and P instead would put two more
 //     instructions per score into the softmax, which bounds the kernel.
 //   * Blocks with a scale further than 2^kSpread below its ref do just that
 //     (wide_block): ratios to one ref would run out of f16's exponents, and a
