@@ -63,7 +63,8 @@ typedef enum {
     PDATTN_ECUDA = 3,         /* a CUDA call failed */
     PDATTN_EBADPAGE = 4,      /* device: page id outside [0, num_pages) */
     PDATTN_ETIMEOUT = 5,      /* device: a bounded wait ran out */
-    PDATTN_EBADPOS = 6        /* device: position outside the table or the rope table */
+    PDATTN_EBADPOS = 6,       /* device: position outside the table or the rope table */
+    PDATTN_ENOPAGES = 7       /* device: more pages wanted than are free */
 } pdattn_status;
 
 typedef enum { PDATTN_BF16 = 0, PDATTN_F32 = 1 } pdattn_dtype;
@@ -434,6 +435,149 @@ pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_ca
                                    const void* q, const void* k_new, const void* v_new, const int32_t* positions,
                                    const int32_t* rows, const int32_t* slots, const int32_t* table, void* out,
                                    void* workspace, size_t workspace_bytes, pdattn_stream stream);
+
+/*
+ * Rotary positions for long contexts.  Pair i (of rot_dim / 2) of a head
+ * vector at position pos turns by the angle pos * w_i, in 64 bits:
+ *   y0 = x0 cos - x1 sin,  y1 = x1 cos + x0 sin,  cos and sin times a gain;
+ * the pair is (i, i + rot_dim / 2), or with `interleaved` (2i, 2i + 1), and
+ * dimensions from rot_dim on are left as they are.  With f_i =
+ * theta^(-2i / rot_dim), m = 2 pi / f_i and c = original_len:
+ *   NONE        w_i = f_i
+ *   LINEAR      w_i = f_i / factor
+ *   WAVELENGTH  pairs of more than `high` turns over c positions keep f_i,
+ *               pairs of fewer than `low` get f_i / factor, and between
+ *               w_i = (1 - s) f_i / factor + s f_i, s = (c / m - low) / (high - low)
+ *   RAMP        the same two ends, joined by the pair's index: s falls from 1
+ *               at a(high) to 0 at a(low), a(t) = (rot_dim / 2) log(c / (2 pi t)) /
+ *               log(theta) (with whole_pairs a(high) is rounded down, a(low)
+ *               up, both into [0, rot_dim - 1]); an interval under 0.001 counts as 0.001
+ * The gain is `gain`, or where that is 0: 1, with RAMP 0.1 log(factor) + 1.
+ */
+typedef enum {
+    PDATTN_ROTARY_NONE = 0, PDATTN_ROTARY_LINEAR = 1, PDATTN_ROTARY_WAVELENGTH = 2, PDATTN_ROTARY_RAMP = 3
+} pdattn_rotary_scaling;
+
+typedef struct {
+    int32_t head_dim;       /* 64 or 128 */
+    int32_t rot_dim;        /* a multiple of 16, at most head_dim */
+    int32_t interleaved;    /* 0: pairs (i, i + rot_dim / 2); 1: (2i, 2i + 1) */
+    int32_t scaling;        /* pdattn_rotary_scaling */
+    int32_t original_len;   /* WAVELENGTH and RAMP: > 0 */
+    int32_t whole_pairs;    /* RAMP: 0 or 1 */
+    double theta;           /* > 1 */
+    double factor;          /* >= 1 */
+    double low, high;       /* WAVELENGTH and RAMP: 0 < low < high */
+    double gain;            /* 0: by the scaling; else > 0 */
+} pdattn_rotary_spec;
+
+/* Frequencies: a HOST block that pdattn_rotary_make fills and the calls read. */
+typedef struct {
+    int32_t head_dim, rot_dim, interleaved;
+    float gain;
+    uint32_t made;          /* set by pdattn_rotary_make; other blocks are refused */
+    uint32_t reserved;
+    uint64_t turns[64];     /* w_i / (2 pi) in 2^-64 turns per position */
+} pdattn_rotary;
+
+/* On the host, in double; touches no device. */
+pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* out);
+
+/*
+ * cos and sin [length, head_dim] of T as pdattn_rope_tables lays them out,
+ * for the rope tables of pdattn_params: half pairs over the whole head only
+ * (PDATTN_EUNSUPPORTED otherwise; pdattn_rotary_apply does the others).  The
+ * angles are not rounded to f32, as those of pdattn_rope_tables are.
+ * Outputs are 16-byte aligned.
+ */
+pdattn_status pdattn_rotary_tables(const pdattn_rotary* rotary, int32_t length, int32_t dtype, void* cos_out,
+                                   void* sin_out, pdattn_stream stream);
+
+/*
+ * Rotates q [n_tokens, heads, head_dim] and k [n_tokens, kv_heads, head_dim]
+ * of T at positions[i] (f32 arithmetic, one rounding to T); with `inverse` it
+ * turns back, which is also the gradient: of q and k from those of q_out and
+ * k_out (the gain is applied in both directions).  Strides are elements from
+ * one token to the next (q and k may be slices of one projection); a token's
+ * heads are contiguous.  q_out may be q, k_out may be k, with the same
+ * stride; nothing else may overlap.  kv_heads 0: no k (its pointers are not
+ * read).  Pointers are 16-byte aligned and strides multiples of 16 bytes.
+ * Any position from 0 on is valid; a negative one is recorded as
+ * PDATTN_EBADPOS and that token's outputs stay as they were.  Of the
+ * workspace only the status word is used (256 bytes are enough).  Attention
+ * calls over keys rotated here take parameters without rope tables.
+ */
+pdattn_status pdattn_rotary_apply(const pdattn_rotary* rotary, int32_t n_tokens, int32_t dtype, int32_t inverse,
+                                  int32_t heads, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                  int32_t kv_heads, const void* k, int64_t k_stride, void* k_out,
+                                  int64_t k_out_stride, const int32_t* positions, void* workspace,
+                                  size_t workspace_bytes, pdattn_stream stream);
+
+/*
+ * Page bookkeeping of a cache: the table, how many positions each row holds,
+ * and how many holders each page has.
+ *   table   [rows, pages_per_row]  a row's pages in its first
+ *                                  ceil(lengths[r] / 64) entries
+ *   lengths [rows]                 positions the row holds
+ *   refs    [num_pages]            rows whose held entries name the page, plus
+ *                                  one for each holder outside the table
+ *                                  (a prefix kept for later); 0: free
+ * A pool is any array of pages [num_pages, heads, 64, row_bytes]: the pools of
+ * T, and the codes and the scales (row_bytes 4) of a coded cache, of every
+ * layer that shares the table.  Pools are 16-byte aligned and must not
+ * overlap.  `pools` is a HOST array, read during the call.  Of p only rows,
+ * pages_per_row, num_pages and page_size are read.  Errors found on the
+ * device (below) leave the outputs and the pools as they were.
+ */
+typedef struct {
+    void* data;
+    int32_t heads;
+    int32_t row_bytes;      /* 1 to 4096 */
+} pdattn_pool;
+
+/* Bytes of workspace for the two calls below (0 if the parameters are invalid). */
+size_t pdattn_pages_workspace_size(const pdattn_params* p);
+
+/*
+ * One step of the table.  Row r becomes a continuation of row parents[r]
+ * (itself, another row, or -1: of nothing): it keeps the first
+ * k = min(lengths[parents[r]], new_lengths[r]) positions of it and gets pages
+ * for new_lengths[r] positions, so that the positions from k on may be
+ * written.  So rows grow (own parent, larger length), give positions back
+ * (smaller length), fork (another row's number), and are freed (-1 and 0).
+ * Full pages are shared.  A partly filled last page (k % 64 != 0) is shared
+ * by rows with new_lengths[r] == k; of the rows that will write into it, the
+ * lowest keeps the page if nobody else holds it, and every other one gets a
+ * copy of its first k % 64 positions (only those are written) in all pools.
+ * New pages are the lowest free ids, in order of row and position; pages that
+ * this call frees count as free.  table_out gets the pages, -1 after them;
+ * refs_out the counts, holders outside the table included.  table_out may be
+ * table and refs_out may be refs.  new_lengths is the next call's `lengths`.
+ * Errors, which change nothing: a parent outside [-1, rows) or a length
+ * outside [0, 64 * pages_per_row] is PDATTN_EBADPOS; a held entry outside the
+ * pool, or fewer refs than rows that hold the page, PDATTN_EBADPAGE; too few
+ * free pages PDATTN_ENOPAGES.  Two launches for up to 128 pools, and one more
+ * for each further 128.
+ */
+pdattn_status pdattn_pages_update(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools,
+                                  const int32_t* table, const int32_t* lengths, const int32_t* refs,
+                                  const int32_t* parents, const int32_t* new_lengths, int32_t* table_out,
+                                  int32_t* refs_out, void* workspace, size_t workspace_bytes, pdattn_stream stream);
+
+/*
+ * Moves the pages in use (refs > 0; n of them) to ids [0, n), so that the
+ * pools' tail is free: the k-th page in use from id n on goes to the k-th
+ * free id below n, the others stay.  page_map [num_pages] gets each page's new
+ * id, -1 for a free one (for holders outside the table).  Held table entries
+ * are renamed, entries after them copied.  table_out may be table and
+ * refs_out may be refs.  Errors, which change nothing: a held entry that is
+ * outside the pool or free, or a negative count, is PDATTN_EBADPAGE; a bad
+ * length PDATTN_EBADPOS.
+ */
+pdattn_status pdattn_pages_compact(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools,
+                                   const int32_t* table, const int32_t* lengths, const int32_t* refs,
+                                   int32_t* table_out, int32_t* refs_out, int32_t* page_map, void* workspace,
+                                   size_t workspace_bytes, pdattn_stream stream);
 
 /*
  * Synchronises `stream`, reads the workspace's device status word, clears

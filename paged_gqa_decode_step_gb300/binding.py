@@ -14,7 +14,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpdattn.so")
 
-OK, EINVAL, EUNSUPPORTED, ECUDA, EBADPAGE, ETIMEOUT, EBADPOS = range(7)
+OK, EINVAL, EUNSUPPORTED, ECUDA, EBADPAGE, ETIMEOUT, EBADPOS, ENOPAGES = range(8)
 BF16, F32 = 0, 1
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 
@@ -51,7 +51,30 @@ class CodedCache(ctypes.Structure):
     ]
 
 
+class RotarySpec(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("scaling", ctypes.c_int32), ("original_len", ctypes.c_int32), ("whole_pairs", ctypes.c_int32),
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+        ("gain", ctypes.c_double),
+    ]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("gain", ctypes.c_float), ("made", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+        ("turns", ctypes.c_uint64 * 64),
+    ]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int32), ("row_bytes", ctypes.c_int32)]
+
+
 LAYERS_PER_LAUNCH = 32
+SCALINGS = {"none": 0, "linear": 1, "wavelength": 2, "ramp": 3}
+STATUS_BYTES = 256
 E4M3, INT8 = 0, 1
 _CODES = {torch.float8_e4m3fn: E4M3, torch.int8: INT8}
 
@@ -62,6 +85,7 @@ def _load():
                           "`python -m paged_gqa_decode_step_gb300.build` (nvcc, sm_103a)")
     L = ctypes.CDLL(LIB_PATH)
     vp, sz, i32, P = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.POINTER(Params)
+    i64 = ctypes.c_int64
     sig = {
         "pdattn_workspace_size": (sz, [P]),
         "pdattn_rope_tables": (i32, [ctypes.c_float, i32, i32, i32, vp, vp, vp]),
@@ -84,6 +108,13 @@ def _load():
         "pdattn_coded_read": (i32, [P, ctypes.POINTER(CodedCache), i32] + [vp] * 4 + [sz, vp]),
         "pdattn_coded_decode": (i32, [P, ctypes.POINTER(CodedCache)] + [vp] * 7 + [sz, vp]),
         "pdattn_coded_prefill": (i32, [P, ctypes.POINTER(CodedCache), i32] + [vp] * 9 + [sz, vp]),
+        "pdattn_rotary_make": (i32, [ctypes.POINTER(RotarySpec), ctypes.POINTER(Rotary)]),
+        "pdattn_rotary_tables": (i32, [ctypes.POINTER(Rotary), i32, i32, vp, vp, vp]),
+        "pdattn_rotary_apply": (i32, [ctypes.POINTER(Rotary), i32, i32, i32, i32, vp, i64, vp, i64, i32, vp, i64, vp,
+                                      i64, vp, vp, sz, vp]),
+        "pdattn_pages_workspace_size": (sz, [P]),
+        "pdattn_pages_update": (i32, [P, i32, ctypes.POINTER(Pool)] + [vp] * 8 + [sz, vp]),
+        "pdattn_pages_compact": (i32, [P, i32, ctypes.POINTER(Pool)] + [vp] * 7 + [sz, vp]),
         "pdattn_check_status": (i32, [vp, vp]),
         "pdattn_last_error": (ctypes.c_char_p, []),
         "pdattn_last_launch_count": (i32, []),
@@ -473,6 +504,159 @@ def coded_prefill(p, cache, q, k_new, v_new, positions, rows, slots, table, out,
     _check(lib.pdattn_coded_prefill(p, cache, n, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
                                     positions.data_ptr(), rows.data_ptr(), slots.data_ptr(), table.data_ptr(),
                                     out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+
+
+def new_status(device="cuda"):
+    """A workspace of the status word alone, for calls that use no more (rotary_apply, coded_write, coded_read)."""
+    return torch.zeros(STATUS_BYTES, dtype=torch.uint8, device=device)
+
+
+def _check_ws(ws):
+    """A contiguous workspace tensor on the current device."""
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("workspace must be a torch tensor")
+    _ws(ws)
+    _same_device(ws)
+
+
+def make_rotary(head_dim, theta, rot_dim=None, interleaved=False, scaling="none", factor=1.0, low=1.0, high=1.0,
+                original_len=0, whole_pairs=False, gain=0.0):
+    """Rotary frequencies (host only): pairs over the first rot_dim dimensions (all by default), halves apart or
+    interleaved, scaled for long contexts ("none", "linear", "wavelength" or "ramp")."""
+    if scaling not in SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(SCALINGS)}")
+    spec = RotarySpec(head_dim, head_dim if rot_dim is None else rot_dim, int(bool(interleaved)), SCALINGS[scaling],
+                      int(original_len), int(bool(whole_pairs)), theta, factor, low, high, gain)
+    r = Rotary()
+    _check(lib.pdattn_rotary_make(spec, r))
+    return r
+
+
+def _check_rotary(rotary):
+    if not isinstance(rotary, Rotary):
+        raise TypeError("rotary must come from make_rotary")
+
+
+def rotary_tables(rotary, length, dtype, device="cuda", stream=None):
+    """cos and sin [length, head_dim] for make_params: half pairs over the whole head."""
+    _check_rotary(rotary)
+    cos, sin = (torch.empty(length, rotary.head_dim, dtype=dtype, device=device) for _ in range(2))
+    _same_device(cos)
+    _check(lib.pdattn_rotary_tables(rotary, length, _DTYPES[dtype], cos.data_ptr(), sin.data_ptr(), _raw_stream(stream)))
+    return cos, sin
+
+
+def _heads_of(name, t, n, D, dtype):
+    """(heads, token stride) of t [n, heads, D], its heads contiguous within a token."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.shape[0] != n or t.shape[2] != D:
+        raise ValueError(f"{name} must be a CUDA tensor [{n}, heads, {D}] of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    h = t.shape[1]
+    if n and h and (t.stride(2) != 1 or (h > 1 and t.stride(1) != D)):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return h, (t.stride(0) if n > 1 else h * D)
+
+
+def rotary_apply(rotary, q, k, positions, q_out, k_out, ws, inverse=False, stream=None):
+    """q [n, heads, D] and k [n, kv_heads, D] (or None, with k_out None) turned at positions [n] int32, or with
+    inverse turned back (the gradient).  Tokens may be strided; q_out may be q and k_out k."""
+    _check_rotary(rotary)
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES or q.dim() != 3:
+        raise ValueError("q must be a bf16 or f32 tensor [n, heads, D]")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out must be both given or both None")
+    n, D = q.shape[0], rotary.head_dim
+    hq, sq = _heads_of("q", q, n, D, q.dtype)
+    ho, so = _heads_of("q_out", q_out, n, D, q.dtype)
+    hk, sk, hl, sl = 0, 0, 0, 0
+    if k is not None:
+        hk, sk = _heads_of("k", k, n, D, q.dtype)
+        hl, sl = _heads_of("k_out", k_out, n, D, q.dtype)
+        _same_device(k, k_out)
+    if ho != hq or hl != hk:
+        raise ValueError("q_out and k_out must have the heads of q and k")
+    _expect("positions", positions, (n,), torch.int32)
+    _same_device(q, q_out, positions)
+    _check_ws(ws)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(lib.pdattn_rotary_apply(rotary, n, _DTYPES[q.dtype], int(bool(inverse)), hq, q.data_ptr(), sq,
+                                   q_out.data_ptr(), so, hk, ptr(k), sk, ptr(k_out), sl, positions.data_ptr(),
+                                   ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+
+
+class Pages:
+    """The pools of a cache that share one page table, as pages_update and pages_compact take them."""
+
+    def __init__(self, pools, num_pages):
+        self.tensors, self.num_pages, self.device = tuple(pools), num_pages, pools[0].get_device()
+        self.array = (Pool * len(self.tensors))()
+        for i, t in enumerate(self.tensors):
+            self.array[i] = Pool(t.data_ptr(), t.shape[1], t.element_size() * (t.shape[3] if t.dim() == 4 else 1))
+
+
+def make_pages(p, pools):
+    """Pools [num_pages, heads, 64, D] of any type (keys, values, codes) and [num_pages, heads, 64] (scales), of every
+    layer that shares p's table; keeps the tensors alive."""
+    pools = list(pools)
+    if not pools:
+        raise ValueError("at least one pool is needed")
+    for i, t in enumerate(pools):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"pool {i} must be a torch tensor")
+        if not t.is_cuda or not t.is_contiguous() or t.dim() not in (3, 4) or t.shape[0] != p.num_pages or t.shape[2] != 64:
+            raise ValueError(f"pool {i} must be a contiguous CUDA tensor [{p.num_pages}, heads, 64(, D)], "
+                             f"got {tuple(t.shape)}")
+    _same_device(*pools)
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in pools)
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("the pools overlap")
+    return Pages(pools, p.num_pages)
+
+
+def pages_workspace_size(p):
+    n = lib.pdattn_pages_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise PdattnError(EINVAL, lib.pdattn_last_error().decode() or "invalid parameters")
+    return n
+
+
+def new_pages_workspace(p, device="cuda"):
+    return torch.zeros(pages_workspace_size(p), dtype=torch.uint8, device=device)
+
+
+def _check_pages(p, pages, ws, **named):
+    if not isinstance(pages, Pages):
+        raise TypeError("pages must come from make_pages")
+    if pages.num_pages != p.num_pages:
+        raise ValueError(f"the pools have {pages.num_pages} pages, the parameters {p.num_pages}")
+    for name, t in named.items():
+        shape = ((p.rows, p.pages_per_row) if name.startswith("table") else
+                 (p.num_pages,) if name.startswith("refs") or name == "page_map" else (p.rows,))
+        _expect(name, t, shape, torch.int32)
+    _check_ws(ws)
+    _same_device(*pages.tensors[:1], *named.values())
+
+
+def pages_update(p, pages, table, lengths, refs, parents, new_lengths, ws, table_out=None, refs_out=None, stream=None):
+    """Row r continues row parents[r] (-1: nothing) with room for new_lengths[r] positions; see pdattn_pages_update.
+    table and refs are updated in place, or written to table_out and refs_out."""
+    table_out, refs_out = table if table_out is None else table_out, refs if refs_out is None else refs_out
+    _check_pages(p, pages, ws, table=table, lengths=lengths, refs=refs, parents=parents, new_lengths=new_lengths,
+                 table_out=table_out, refs_out=refs_out)
+    _check(lib.pdattn_pages_update(p, len(pages.array), pages.array, table.data_ptr(), lengths.data_ptr(),
+                                   refs.data_ptr(), parents.data_ptr(), new_lengths.data_ptr(), table_out.data_ptr(),
+                                   refs_out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+
+
+def pages_compact(p, pages, table, lengths, refs, page_map, ws, table_out=None, refs_out=None, stream=None):
+    """Moves the pages in use to the lowest ids; page_map [num_pages] gets every page's new id or -1."""
+    table_out, refs_out = table if table_out is None else table_out, refs if refs_out is None else refs_out
+    _check_pages(p, pages, ws, table=table, lengths=lengths, refs=refs, page_map=page_map, table_out=table_out,
+                 refs_out=refs_out)
+    _check(lib.pdattn_pages_compact(p, len(pages.array), pages.array, table.data_ptr(), lengths.data_ptr(),
+                                    refs.data_ptr(), table_out.data_ptr(), refs_out.data_ptr(), page_map.data_ptr(),
+                                    ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 def check_status(ws, stream=None):

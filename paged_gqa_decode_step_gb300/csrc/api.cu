@@ -1066,6 +1066,246 @@ pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_ca
     return PDATTN_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------
+namespace {
+constexpr uint32_t kRotaryMade = 0x70647274u;
+constexpr double kTwoPi = 6.283185307179586476925;
+}  // namespace
+
+pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* out) {
+    g_launches = 0;
+    if (!spec || !out) return fail(PDATTN_EINVAL, "spec or out is NULL");
+    const pdattn_rotary_spec& c = *spec;
+    if (c.head_dim != 64 && c.head_dim != 128) return fail(PDATTN_EUNSUPPORTED, "head_dim must be 64 or 128");
+    if (c.rot_dim <= 0 || c.rot_dim % 16 != 0 || c.rot_dim > c.head_dim)
+        return fail(PDATTN_EINVAL, "rot_dim (%d) must be a multiple of 16 in [16, head_dim]", c.rot_dim);
+    if (c.interleaved != 0 && c.interleaved != 1) return fail(PDATTN_EINVAL, "interleaved must be 0 or 1");
+    if (c.scaling < PDATTN_ROTARY_NONE || c.scaling > PDATTN_ROTARY_RAMP)
+        return fail(PDATTN_EINVAL, "unknown scaling %d", c.scaling);
+    if (!(c.theta > 1.0) || !std::isfinite(c.theta)) return fail(PDATTN_EINVAL, "theta must be > 1");
+    if (!(c.factor >= 1.0) || !std::isfinite(c.factor)) return fail(PDATTN_EINVAL, "factor must be >= 1");
+    if (!(c.gain >= 0.0) || !std::isfinite(c.gain)) return fail(PDATTN_EINVAL, "gain must be >= 0");
+    if (c.scaling >= PDATTN_ROTARY_WAVELENGTH) {
+        if (!(c.low > 0.0) || !(c.high > c.low) || !std::isfinite(c.high))
+            return fail(PDATTN_EINVAL, "low and high must be 0 < low < high");
+        if (c.original_len <= 0) return fail(PDATTN_EINVAL, "original_len must be > 0");
+        if (c.whole_pairs != 0 && c.whole_pairs != 1) return fail(PDATTN_EINVAL, "whole_pairs must be 0 or 1");
+    }
+    const double pairs = c.rot_dim / 2, log_theta = std::log(c.theta);
+    // the ramp's ends, in pairs
+    double a = 0.0, b = 0.0;
+    if (c.scaling == PDATTN_ROTARY_RAMP) {
+        a = pairs * std::log(c.original_len / (kTwoPi * c.high)) / log_theta;
+        b = pairs * std::log(c.original_len / (kTwoPi * c.low)) / log_theta;
+        if (c.whole_pairs) {
+            a = std::fmin(std::fmax(std::floor(a), 0.0), c.rot_dim - 1);
+            b = std::fmin(std::fmax(std::ceil(b), 0.0), c.rot_dim - 1);
+        }
+        b = std::fmax(b, a + 1e-3);
+    }
+    pdattn_rotary r = {};
+    r.head_dim = c.head_dim;
+    r.rot_dim = c.rot_dim;
+    r.interleaved = c.interleaved;
+    r.gain = (float)(c.gain > 0.0 ? c.gain : c.scaling == PDATTN_ROTARY_RAMP ? 0.1 * std::log(c.factor) + 1.0 : 1.0);
+    r.made = kRotaryMade;
+    for (int i = 0; i < c.rot_dim / 2; ++i) {
+        const double f = std::exp(-(double)i / pairs * log_theta);
+        double s = 1.0;                                 // share of f, the rest of f / factor
+        if (c.scaling == PDATTN_ROTARY_LINEAR) s = 0.0;
+        if (c.scaling == PDATTN_ROTARY_WAVELENGTH) s = (c.original_len * f / kTwoPi - c.low) / (c.high - c.low);
+        if (c.scaling == PDATTN_ROTARY_RAMP) s = 1.0 - (i - a) / (b - a);
+        s = std::fmin(std::fmax(s, 0.0), 1.0);
+        // at most 1 / (2 pi) turn: below 2^62
+        r.turns[i] = (uint64_t)std::llrint(std::ldexp((f * s + f / c.factor * (1.0 - s)) / kTwoPi, 64));
+    }
+    *out = r;
+    return PDATTN_OK;
+}
+
+static pdattn_status check_rotary(const pdattn_rotary* r, int32_t dtype) {
+    if (!r) return fail(PDATTN_EINVAL, "rotary is NULL");
+    if (r->made != kRotaryMade || (r->head_dim != 64 && r->head_dim != 128) || r->rot_dim <= 0 ||
+        r->rot_dim % 16 != 0 || r->rot_dim > r->head_dim)
+        return fail(PDATTN_EINVAL, "rotary was not filled by pdattn_rotary_make");
+    if (dtype != PDATTN_BF16 && dtype != PDATTN_F32) return fail(PDATTN_EINVAL, "unknown dtype %d", dtype);
+    return PDATTN_OK;
+}
+
+static RotaryArgs rotary_args(const pdattn_rotary* r) {
+    RotaryArgs a = {};
+    a.head_dim = r->head_dim;
+    a.rot_dim = r->rot_dim;
+    a.interleaved = r->interleaved;
+    a.gain = r->gain;
+    static_assert(sizeof a.turns == sizeof r->turns, "pairs of a head");
+    memcpy(a.turns, r->turns, sizeof a.turns);
+    return a;
+}
+
+pdattn_status pdattn_rotary_tables(const pdattn_rotary* rotary, int32_t length, int32_t dtype, void* cos_out,
+                                   void* sin_out, pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_rotary(rotary, dtype);
+    if (s != PDATTN_OK) return s;
+    if (rotary->interleaved || rotary->rot_dim != rotary->head_dim)
+        return fail(PDATTN_EUNSUPPORTED, "rope tables hold half pairs over the whole head; use pdattn_rotary_apply");
+    if (length < 0) return fail(PDATTN_EINVAL, "length must be >= 0");
+    if (length == 0) return PDATTN_OK;
+    if (!cos_out || !sin_out) return fail(PDATTN_EINVAL, "NULL table pointer");
+    if (!aligned16(cos_out) || !aligned16(sin_out)) return fail(PDATTN_EINVAL, "rope tables must be 16-byte aligned");
+    cudaError_t e = launch_rotary_tables(rotary_args(rotary), length, dtype, cos_out, sin_out, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "rotary table launch");
+    g_launches = 1;
+    return PDATTN_OK;
+}
+
+pdattn_status pdattn_rotary_apply(const pdattn_rotary* rotary, int32_t n_tokens, int32_t dtype, int32_t inverse,
+                                  int32_t heads, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                  int32_t kv_heads, const void* k, int64_t k_stride, void* k_out,
+                                  int64_t k_out_stride, const int32_t* positions, void* workspace,
+                                  size_t workspace_bytes, pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_rotary(rotary, dtype);
+    if (s != PDATTN_OK) return s;
+    if (n_tokens < 0) return fail(PDATTN_EINVAL, "n_tokens < 0");
+    if (heads <= 0 || kv_heads < 0 || heads > 32767 || kv_heads > 32767)
+        return fail(PDATTN_EINVAL, "heads must be in [1, 32767], kv_heads in [0, 32767]");
+    if (inverse != 0 && inverse != 1) return fail(PDATTN_EINVAL, "inverse must be 0 or 1");
+    if (n_tokens == 0) return PDATTN_OK;
+    const int64_t D = rotary->head_dim, wide = dtype == PDATTN_BF16 ? 8 : 4;
+    auto check = [&](const char* what, const void* x, int64_t stride, int64_t h, const void* y, int64_t out_stride) {
+        if (!x || !y) return fail(PDATTN_EINVAL, "NULL %s pointer", what);
+        if (!aligned16(x) || !aligned16(y)) return fail(PDATTN_EINVAL, "%s must be 16-byte aligned", what);
+        if (stride < h * D || out_stride < h * D || stride % wide != 0 || out_stride % wide != 0)
+            return fail(PDATTN_EINVAL, "token strides of %s must cover its heads and be multiples of 16 bytes", what);
+        if (x == y && stride != out_stride)
+            return fail(PDATTN_EINVAL, "%s rotated in place must have one token stride", what);
+        return PDATTN_OK;
+    };
+    s = check("q", q, q_stride, heads, q_out, q_out_stride);
+    if (s == PDATTN_OK && kv_heads > 0) s = check("k", k, k_stride, kv_heads, k_out, k_out_stride);
+    if (s != PDATTN_OK) return s;
+    if (!positions) return fail(PDATTN_EINVAL, "NULL positions");
+    s = check_status_ws(workspace, workspace_bytes);
+    if (s != PDATTN_OK) return s;
+    RotaryArgs a = rotary_args(rotary);
+    a.inverse = inverse;
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.positions = positions;
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_stride = kv_heads > 0 ? k_stride : 0;
+    a.k_out_stride = kv_heads > 0 ? k_out_stride : 0;
+    a.ws = static_cast<char*>(workspace);
+    cudaError_t e = launch_rotary(a, n_tokens, dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+    g_launches = 1;
+    return PDATTN_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Page bookkeeping
+// ---------------------------------------------------------------------------
+static pdattn_status check_pages_params(const pdattn_params* p) {
+    if (!p) return fail(PDATTN_EINVAL, "params is NULL");
+    if (p->rows < 0) return fail(PDATTN_EINVAL, "rows < 0");
+    if (p->pages_per_row <= 0 || p->num_pages <= 0) return fail(PDATTN_EINVAL, "pages_per_row and num_pages must be > 0");
+    if (p->page_size != kPageSize) return fail(PDATTN_EUNSUPPORTED, "page_size must be 64");
+    if ((long long)p->pages_per_row * kPageSize >= (1ll << 30)) return fail(PDATTN_EUNSUPPORTED, "pages_per_row too large");
+    // the pages wanted are counted in 32 bits
+    if ((long long)p->rows * p->pages_per_row >= (1ll << 31)) return fail(PDATTN_EUNSUPPORTED, "the table is too large");
+    return PDATTN_OK;
+}
+
+size_t pdattn_pages_workspace_size(const pdattn_params* p) {
+    if (check_pages_params(p) != PDATTN_OK) return 0;
+    return pages_layout(p->rows, p->pages_per_row, p->num_pages).total;
+}
+
+static pdattn_status pages_impl(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools, PagesArgs a,
+                                bool compact, void* workspace, size_t workspace_bytes, pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_pages_params(p);
+    if (s != PDATTN_OK) return s;
+    if (n_pools <= 0 || !pools) return fail(PDATTN_EINVAL, "at least one pool is needed");
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i].data || !aligned16(pools[i].data))
+            return fail(PDATTN_EINVAL, "pool %d must be non-NULL and 16-byte aligned", i);
+        if (pools[i].heads <= 0 || pools[i].heads > 32767 || pools[i].row_bytes <= 0 || pools[i].row_bytes > 4096)
+            return fail(PDATTN_EINVAL, "pool %d: heads must be in [1, 32767], row_bytes in [1, 4096]", i);
+    }
+    if (p->rows == 0) return PDATTN_OK;
+    if (!a.table || !a.lengths || !a.refs || !a.table_out || !a.refs_out ||
+        (compact ? !a.map : !a.parents || !a.new_lengths))
+        return fail(PDATTN_EINVAL, "NULL data pointer");
+    if (!workspace) return fail(PDATTN_EINVAL, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+        return fail(PDATTN_EINVAL, "workspace must be 256-byte aligned");
+    a.L = pages_layout(p->rows, p->pages_per_row, p->num_pages);
+    if (workspace_bytes < a.L.total)
+        return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, a.L.total);
+    const int sms = sm_count();
+    if (sms <= 0) return fail(PDATTN_ECUDA, "no CUDA device");
+    a.rows = p->rows;
+    a.pages_per_row = p->pages_per_row;
+    a.num_pages = p->num_pages;
+    a.ws = static_cast<char*>(workspace);
+    cudaError_t e = launch_pages(a, compact, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "page table launch");
+    int launches = 1;
+    for (int i0 = 0; i0 < n_pools; i0 += kPoolsPerLaunch) {
+        PoolList l = {};
+        for (l.n = 0; l.n < kPoolsPerLaunch && i0 + l.n < n_pools; ++l.n) {
+            l.data[l.n] = pools[i0 + l.n].data;
+            l.row_bytes[l.n] = pools[i0 + l.n].row_bytes;
+            l.first[l.n] = l.slabs;
+            l.slabs += pools[i0 + l.n].heads;
+        }
+        e = launch_pages_copy(a, l, 8 * sms, i0 == 0, (cudaStream_t)stream);
+        if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
+        ++launches;
+    }
+    g_launches = launches;
+    return PDATTN_OK;
+}
+
+pdattn_status pdattn_pages_update(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools,
+                                  const int32_t* table, const int32_t* lengths, const int32_t* refs,
+                                  const int32_t* parents, const int32_t* new_lengths, int32_t* table_out,
+                                  int32_t* refs_out, void* workspace, size_t workspace_bytes, pdattn_stream stream) {
+    PagesArgs a = {};
+    a.table = table;
+    a.lengths = lengths;
+    a.refs = refs;
+    a.parents = parents;
+    a.new_lengths = new_lengths;
+    a.table_out = table_out;
+    a.refs_out = refs_out;
+    return pages_impl(p, n_pools, pools, a, false, workspace, workspace_bytes, stream);
+}
+
+pdattn_status pdattn_pages_compact(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools,
+                                   const int32_t* table, const int32_t* lengths, const int32_t* refs,
+                                   int32_t* table_out, int32_t* refs_out, int32_t* page_map, void* workspace,
+                                   size_t workspace_bytes, pdattn_stream stream) {
+    PagesArgs a = {};
+    a.table = table;
+    a.lengths = lengths;
+    a.refs = refs;
+    a.table_out = table_out;
+    a.refs_out = refs_out;
+    a.map = page_map;
+    return pages_impl(p, n_pools, pools, a, true, workspace, workspace_bytes, stream);
+}
+
 pdattn_status pdattn_check_status(void* workspace, pdattn_stream stream) {
     if (!workspace) return fail(PDATTN_EINVAL, "workspace is NULL");
     cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
@@ -1081,6 +1321,7 @@ pdattn_status pdattn_check_status(void* workspace, pdattn_stream stream) {
     if (status & kErrTimeout) return fail(PDATTN_ETIMEOUT, "a device wait ran past its limit (status 0x%x)", status);
     if (status & kErrBadPage) return fail(PDATTN_EBADPAGE, "a page id outside the pool (status 0x%x)", status);
     if (status & kErrBadPos) return fail(PDATTN_EBADPOS, "a position outside the table or rope table (status 0x%x)", status);
+    if (status & kErrNoPages) return fail(PDATTN_ENOPAGES, "more pages wanted than are free (status 0x%x)", status);
     if (status & kErrBadPlan) return fail(PDATTN_EINVAL, "attention ran without a matching plan (status 0x%x)", status);
     return PDATTN_OK;
 }

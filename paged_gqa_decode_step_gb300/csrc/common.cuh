@@ -23,6 +23,7 @@ constexpr int kErrBadPage = 1;
 constexpr int kErrBadPos = 2;
 constexpr int kErrTimeout = 4;
 constexpr int kErrBadPlan = 8;
+constexpr int kErrNoPages = 16;
 
 // Control block at the start of the workspace (256 bytes).
 struct Ctrl {
@@ -393,5 +394,45 @@ __device__ __forceinline__ void fail_timeout(Ctrl* ctrl) {
     set_error(ctrl, kErrTimeout);
     atomicExch(&ctrl->magic, 0u);
 }
+
+// ---------------------------------------------------------------------------
+// 16-byte vectors of T, widened to f32 and back (one rounding).
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void to_f32(const uint4& v, float (&f)[8]) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float2 t = __bfloat1622float2(h[k]);
+            f[2 * k] = t.x;
+            f[2 * k + 1] = t.y;
+        }
+    }
+    __device__ static uint4 from_f32(const float (&f)[8]) {
+        uint4 v;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+        return v;
+    }
+};
+template <>
+struct Vec16<float> {
+    static constexpr int N = 4;
+    __device__ static void to_f32(const uint4& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+    __device__ static uint4 from_f32(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+    }
+};
 
 }  // namespace pdattn

@@ -158,6 +158,67 @@ struct CodedPrefillArgs {
     float2* part_ml;        // [slot, kv head, slot_rows] (maximum, sum)
 };
 
+// Rotary frequencies (csrc/rotary.cu): turns per position of every pair in
+// 2^-64, and what cos and sin are multiplied by.
+constexpr int kRotaryPairs = 64;
+
+struct RotaryArgs {
+    int head_dim, rot_dim, interleaved, inverse, heads, kv_heads;
+    float gain;
+    const int* positions;   // [n_tokens]
+    const void* q;          // token t's heads at q + t * q_stride elements
+    const void* k;
+    void* q_out;
+    void* k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+    char* ws;               // status word only
+    uint64_t turns[kRotaryPairs];
+};
+
+// Page bookkeeping (csrc/pages.cu).
+struct PagesLayout {
+    size_t info, table, rows, jobs, a, b, c, total;
+};
+
+inline PagesLayout pages_layout(int rows, int pages_per_row, int num_pages) {
+    PagesLayout L;
+    const size_t jobs = rows > num_pages ? rows : num_pages;
+    size_t off = 256;                                   // Ctrl
+    L.info = off; off += 256;
+    L.table = off; off = align256(off + sizeof(int) * (size_t)rows * pages_per_row);
+    L.rows = off; off = align256(off + sizeof(int2) * (size_t)rows);
+    L.jobs = off; off = align256(off + sizeof(int4) * jobs);
+    L.a = off; off = align256(off + sizeof(int) * (size_t)num_pages);
+    L.b = off; off = align256(off + sizeof(int) * (size_t)num_pages);
+    L.c = off; off = align256(off + sizeof(int) * (size_t)num_pages);
+    L.total = off;
+    return L;
+}
+
+struct PagesArgs {
+    int rows, pages_per_row, num_pages;
+    const int* table;       // [rows, pages_per_row]
+    const int* lengths;     // [rows]
+    const int* refs;        // [num_pages]
+    const int* parents;     // update: [rows]
+    const int* new_lengths; // update: [rows]
+    int* table_out;         // may be table
+    int* refs_out;          // may be refs
+    int* map;               // compact: [num_pages]
+    char* ws;
+    PagesLayout L;
+};
+
+// Pools of one copy launch; pool i's heads are slabs [first[i], first[i + 1]).
+constexpr int kPoolsPerLaunch = 128;
+
+struct PoolList {
+    int n, slabs;
+    void* data[kPoolsPerLaunch];
+    int first[kPoolsPerLaunch];
+    int row_bytes[kPoolsPerLaunch];
+};
+
 cudaError_t launch_rope_tables(float theta, int D, int S, int dtype, void* cos_out, void* sin_out,
                                cudaStream_t stream);
 // The split planner (one block, if a.do_plan), then the rope + cache write of
@@ -197,6 +258,14 @@ cudaError_t launch_prefill_plan(const PrefillPrepArgs& a, cudaStream_t stream);
 // Attention of the units, then, where tiles may be split, their merge.
 cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int code, int grid, bool merge,
                                  cudaStream_t stream);
+// Rotary tables of `length` positions; rotation of n_tokens tokens.
+cudaError_t launch_rotary_tables(const RotaryArgs& a, int length, int dtype, void* cos_out, void* sin_out,
+                                 cudaStream_t stream);
+cudaError_t launch_rotary(const RotaryArgs& a, int n_tokens, int dtype, cudaStream_t stream);
+// The table's part of an update or a compaction (one cluster), then the page
+// copies it listed (after_plan: a programmatic dependent of it).
+cudaError_t launch_pages(const PagesArgs& a, bool compact, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PagesArgs& a, const PoolList& pools, int grid, bool after_plan, cudaStream_t stream);
 cudaError_t launch_code(const CodeArgs& a, int dtype, int code, cudaStream_t stream);
 cudaError_t launch_read(const ReadArgs& a, int dtype, int code, cudaStream_t stream);
 

@@ -52,45 +52,8 @@ __global__ void rope_tables_kernel(float theta, int D, int S, T* __restrict__ co
 }
 
 // ---------------------------------------------------------------------------
-// 16-byte vectors of T and the rotation of one pair of them.
+// The rotation of one pair of 16-byte vectors of T.
 // ---------------------------------------------------------------------------
-template <typename T>
-struct Vec16;
-template <>
-struct Vec16<__nv_bfloat16> {
-    static constexpr int N = 8;
-    __device__ static void to_f32(const uint4& v, float (&f)[8]) {
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float2 t = __bfloat1622float2(h[k]);
-            f[2 * k] = t.x;
-            f[2 * k + 1] = t.y;
-        }
-    }
-    __device__ static uint4 from_f32(const float (&f)[8]) {
-        uint4 v;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
-        return v;
-    }
-};
-template <>
-struct Vec16<float> {
-    static constexpr int N = 4;
-    __device__ static void to_f32(const uint4& v, float (&f)[4]) {
-        f[0] = __uint_as_float(v.x);
-        f[1] = __uint_as_float(v.y);
-        f[2] = __uint_as_float(v.z);
-        f[3] = __uint_as_float(v.w);
-    }
-    __device__ static uint4 from_f32(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
-    }
-};
-
 // y_lo = x_lo * c_lo - x_hi * s_lo, y_hi = x_hi * c_hi + x_lo * s_hi: the
 // pages' x * cos + rotate_half(x) * sin with rotate_half(x) = [-x_hi, x_lo].
 // Separate f32 products and one f32 add (no fused multiply-add), then one
