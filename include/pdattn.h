@@ -247,6 +247,41 @@ pdattn_status pdattn_decode_fused_noalloc(const pdattn_params* p, const void* q,
                                           void* out, pdattn_stream stream);
 
 /*
+ * Bytes of workspace pdattn_decode_shared needs for up to n_groups groups (0
+ * if the parameters are invalid).
+ */
+size_t pdattn_shared_workspace_size(const pdattn_params* p, int32_t n_groups);
+
+/*
+ * pdattn_decode_fused where groups of rows hold the same leading pages: rows
+ * [group_start[i], group_start[i + 1]) have the same first group_pages[i]
+ * entries in their tables (as pdattn_pages_update leaves those of forked
+ * rows), and the attention reads those pages once for the group, on the
+ * tensor cores, where pdattn_decode_fused reads them once per row.  The
+ * result is that of pdattn_decode_fused (the same sums in another order).
+ * group_start [n_groups + 1] and group_pages [n_groups] are DEVICE arrays of
+ * int32, read when the call runs; group_start begins with 0, ends with rows
+ * and does not fall.  A group may be empty, hold one row or share no page
+ * (group_pages 0).  Shared pages are full: a row whose new position lies
+ * in them (positions[r] / 64 < group_pages) is recorded as PDATTN_EBADPOS and
+ * skipped, as is one whose position is outside the table or the rope table;
+ * another list that is not a partition is PDATTN_EBADPOS too, and the call
+ * attends nothing (it may have written rows' new keys and values).  The
+ * entries of any row of a group may be read for its shared pages, and a bad
+ * one is PDATTN_EBADPAGE.  Groups of one row, of fewer than four pages, or of
+ * which a window hides some position from some row are attended row by row.
+ * dtype bf16 (PDATTN_EUNSUPPORTED otherwise; f32 rows may share pages in
+ * pdattn_decode_fused).  n_groups is at most the one the workspace was sized
+ * for; a workspace of this call holds no plan for pdattn_attend.  Four launches,
+ * each a programmatic dependent of the one before.
+ */
+pdattn_status pdattn_decode_shared(const pdattn_params* p, int32_t n_groups, const int32_t* group_start,
+                                   const int32_t* group_pages, const void* q, const void* k_new,
+                                   const void* v_new, const int32_t* positions, const int32_t* table,
+                                   void* k_pool, void* v_pool, void* out, void* workspace,
+                                   size_t workspace_bytes, pdattn_stream stream);
+
+/*
  * Bytes of workspace pdattn_prefill_paged needs for n_tokens packed tokens
  * (256-byte aligned; 0 if the parameters are invalid).
  */

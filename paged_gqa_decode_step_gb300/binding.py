@@ -97,6 +97,8 @@ def _load():
         "pdattn_decode_fused_noalloc": (i32, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "pdattn_layers_workspace_size": (sz, [P, i32]),
         "pdattn_decode_layers": (i32, [P, i32, ctypes.POINTER(Layer), vp, vp, vp, sz, vp]),
+        "pdattn_shared_workspace_size": (sz, [P, i32]),
+        "pdattn_decode_shared": (i32, [P, i32] + [vp] * 11 + [sz, vp]),
         "pdattn_prefill_workspace_size": (sz, [P, i32]),
         "pdattn_prefill_paged": (i32, [P, i32] + [vp] * 11 + [sz, vp]),
         "pdattn_prefill_attend": (i32, [P, i32] + [vp] * 6 + [sz, vp]),
@@ -583,6 +585,35 @@ def rotary_apply(rotary, q, k, positions, q_out, k_out, ws, inverse=False, strea
     _check(lib.pdattn_rotary_apply(rotary, n, _DTYPES[q.dtype], int(bool(inverse)), hq, q.data_ptr(), sq,
                                    q_out.data_ptr(), so, hk, ptr(k), sk, ptr(k_out), sl, positions.data_ptr(),
                                    ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+
+
+def shared_workspace_size(p, n_groups):
+    n = lib.pdattn_shared_workspace_size(ctypes.byref(p), n_groups)
+    if n == 0:
+        raise PdattnError(EINVAL, lib.pdattn_last_error().decode() or "invalid parameters")
+    return n
+
+
+def new_shared_workspace(p, n_groups, device="cuda"):
+    """A workspace for decode_shared of p.rows rows in up to n_groups groups."""
+    return torch.zeros(shared_workspace_size(p, n_groups), dtype=torch.uint8, device=device)
+
+
+def decode_shared(p, q, k_new, v_new, positions, table, group_start, group_pages, k_pool, v_pool, out, ws, stream=None):
+    """decode_fused (bf16) where rows [group_start[i], group_start[i + 1]) hold the same first group_pages[i] pages,
+    which are read once for the group; group_start [n + 1] and group_pages [n] int32."""
+    n = _tokens(group_pages)
+    _check_common(p, positions, table, k_pool, v_pool)
+    _check_q(p, q=q, k_new=k_new, v_new=v_new, out=out)
+    _expect("group_pages", group_pages, (n,), torch.int32)
+    _expect("group_start", group_start, (n + 1,), torch.int32)
+    if getattr(p, "_device", None) not in (None, torch.cuda.current_device()):
+        raise ValueError(f"rope tables or sinks are on cuda:{p._device}, not on the current device")
+    _same_device(q, k_new, v_new, positions, table, group_start, group_pages, k_pool, v_pool, out)
+    _check_ws(ws)
+    _check(lib.pdattn_decode_shared(p, n, group_start.data_ptr(), group_pages.data_ptr(), q.data_ptr(), k_new.data_ptr(),
+                                    v_new.data_ptr(), positions.data_ptr(), table.data_ptr(), k_pool.data_ptr(),
+                                    v_pool.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 class Pages:

@@ -474,6 +474,137 @@ pdattn_status pdattn_decode_layers(const pdattn_params* p, int32_t n_layers, con
     return PDATTN_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Decode over shared prefixes
+// ---------------------------------------------------------------------------
+static pdattn_status check_shared(const pdattn_params* p, int32_t n_groups, int grid, ShLayout* S) {
+    if (n_groups <= 0) return fail(PDATTN_EINVAL, "n_groups must be > 0");
+    if (p->dtype != PDATTN_BF16)
+        return fail(PDATTN_EUNSUPPORTED, "shared pages are attended on the tensor cores: dtype must be bf16");
+    *S = shared_layout(p->rows, p->heads, p->kv_heads, p->head_dim, p->pages_per_row, p->chunk_pages, n_groups, grid);
+    // tiles of two rows or more, in blocks of two pages, are counted in 32 bits, and so are merge slots
+    if ((long long)(p->rows / 2 + 1) * (p->pages_per_row / 2 + 1) * p->kv_heads >= (1ll << 30) ||
+        S->max_slots >= (1ll << 31) || (long long)p->rows * p->kv_heads >= (1ll << 31))
+        return fail(PDATTN_EUNSUPPORTED, "rows x pages_per_row x kv_heads too large for one call");
+    return PDATTN_OK;
+}
+
+size_t pdattn_shared_workspace_size(const pdattn_params* p, int32_t n_groups) {
+    if (check_params(p) != PDATTN_OK) return 0;
+    const int grid = sm_count();
+    ShLayout S;
+    if (grid <= 0 || check_shared(p, n_groups, grid, &S) != PDATTN_OK) return 0;
+    return S.total;
+}
+
+pdattn_status pdattn_decode_shared(const pdattn_params* p, int32_t n_groups, const int32_t* group_start,
+                                   const int32_t* group_pages, const void* q, const void* k_new, const void* v_new,
+                                   const int32_t* positions, const int32_t* table, void* k_pool, void* v_pool,
+                                   void* out, void* workspace, size_t workspace_bytes, pdattn_stream stream) {
+    g_launches = 0;
+    pdattn_status s = check_params(p);
+    if (s != PDATTN_OK) return s;
+    ShLayout S;
+    s = check_shared(p, n_groups, 1, &S);
+    if (s != PDATTN_OK) return s;
+    if (p->rows == 0) return PDATTN_OK;
+    if (!group_start || !group_pages) return fail(PDATTN_EINVAL, "NULL group pointer");
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
+        return fail(PDATTN_EINVAL, "k_new and v_new must be non-NULL and 16-byte aligned");
+    s = check_attend_ptrs(q, positions, table, k_pool, v_pool, out);
+    if (s != PDATTN_OK) return s;
+    if (!workspace) return fail(PDATTN_EINVAL, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+        return fail(PDATTN_EINVAL, "workspace must be 256-byte aligned");
+    const int grid = sm_count();
+    if (grid <= 0) return fail(PDATTN_ECUDA, "no CUDA device");
+    s = check_shared(p, n_groups, grid, &S);
+    if (s != PDATTN_OK) return s;
+    if (workspace_bytes < S.total)
+        return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, S.total);
+    char* ws = static_cast<char*>(workspace);
+    const int g = p->heads / p->kv_heads, tile_tokens = 2 * (kPfRows / g);
+
+    auto fn = encode_fn();
+    if (!fn) return fail(PDATTN_ECUDA, "cuTensorMapEncodeTiled is not available");
+    CUtensorMap qm, km, vm;
+    {
+        // rotated queries (D, heads, rows): one box = the g heads of a kv head for half a tile's rows, 64 columns wide
+        cuuint64_t dims[3] = {(cuuint64_t)p->head_dim, (cuuint64_t)p->heads, (cuuint64_t)p->rows};
+        cuuint64_t strides[2] = {(cuuint64_t)p->head_dim * 2, (cuuint64_t)p->heads * p->head_dim * 2};
+        cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)(tile_tokens / 2)};
+        cuuint32_t estr[3] = {1, 1, 1};
+        CUresult r = fn(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ws + S.w.q_rot, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(PDATTN_ECUDA, "cuTensorMapEncodeTiled (queries) failed (%d)", (int)r);
+    }
+    if ((s = make_pool_map(&km, k_pool, p)) != PDATTN_OK) return s;
+    if ((s = make_pool_map(&vm, v_pool, p)) != PDATTN_OK) return s;
+
+    PrepArgs a = prep_args(p, positions, table, ws, S.w, grid);
+    a.q = q;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.q_out = ws + S.w.q_rot;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.max_pos = position_limit(p);
+    a.rope_blocks = p->rows;
+    a.do_plan = 1;
+    PrepShared ps = {};
+    ps.n_groups = n_groups;
+    ps.tile_tokens = tile_tokens;
+    ps.max_slots = (int)S.max_slots;
+    ps.start = group_start;
+    ps.pages = group_pages;
+    ps.groups = S.groups;
+    ps.row_pre = S.row_pre;
+    ps.tiles = S.tiles;
+    cudaError_t e = launch_shared_prep(a, ps, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "shared plan + rope/write launches");
+
+    SharedArgs sa = {};
+    sa.kv_heads = p->kv_heads;
+    sa.group = g;
+    sa.tile_tokens = tile_tokens;
+    sa.head_dim = p->head_dim;
+    sa.pages_per_row = p->pages_per_row;
+    sa.num_pages = p->num_pages;
+    sa.scale_log2 = scale_log2(p);
+    sa.table = table;
+    sa.ws = ws;
+    sa.L = S.w;
+    sa.tiles = S.tiles;
+    e = launch_shared_prefix(sa, qm, km, vm, grid, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+
+    AttendArgs aa = {};
+    aa.rows = p->rows;
+    aa.heads = p->heads;
+    aa.kv_heads = p->kv_heads;
+    aa.group = g;
+    aa.head_dim = p->head_dim;
+    aa.pages_per_row = p->pages_per_row;
+    aa.num_pages = p->num_pages;
+    aa.window = p->window;
+    aa.chunk_pages = p->chunk_pages;
+    aa.scale_log2 = sa.scale_log2;
+    aa.q = ws + S.w.q_rot;
+    aa.positions = positions;
+    aa.table = table;
+    aa.sinks = p->sinks;
+    aa.out = out;
+    aa.ws = ws;
+    aa.L = S.w;
+    aa.max_pos = a.max_pos;
+    AttendShared as = {(int)S.max_slots};
+    e = launch_attend_shared(aa, as, km, vm, grid, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    g_launches = 4;
+    return PDATTN_OK;
+}
+
 size_t pdattn_prefill_workspace_size(const pdattn_params* p, int32_t n_tokens) {
     if (check_params(p) != PDATTN_OK || n_tokens < 0) return 0;
     return pf_layout(n_tokens, p->heads, p->head_dim, elem_bytes(p)).total;

@@ -803,6 +803,10 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     // Multi-layer launch: item row v is row v % layer_rows of layer
     // v / layer_rows, whose pools, output and sinks come from `lay`.
     constexpr bool kMulti = std::is_same<Lay, AttendLayers>::value;
+    // Shared prefixes: items are the rows' own pages; the shared pages'
+    // partials are chunks too, done before this launch (merge counters start
+    // at their number).
+    constexpr bool kShared = std::is_same<Lay, AttendShared>::value;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -872,7 +876,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     float2* part_ml = reinterpret_cast<float2*>(a.ws + a.L.part_ml);
     float* part_o = reinterpret_cast<float*>(a.ws + a.L.part_o);
     const int g = a.group, Hk = a.kv_heads;
-    const int nf = first_wave(a.rows, Hk, gridDim.x);
+    const int nf = kShared ? 0 : first_wave(a.rows, Hk, gridDim.x);
 
     // Coded decode has no planner: every CTA finds its own share of the work
     // (below) and the coding launch clears the merge counters.
@@ -887,7 +891,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         const int4 h3 = __ldcg(reinterpret_cast<const int4*>(ctrl) + 3);
         *n_items = h0.w;
         *chunk_pages = h1.x;
-        return (uint32_t)h1.y == kPlanMagic && h1.z == a.rows && h1.w == Hk && h2.x == a.pages_per_row &&
+        return (uint32_t)h1.y == (kShared ? kSharedPlanMagic : kPlanMagic) && h1.z == a.rows && h1.w == Hk && h2.x == a.pages_per_row &&
                h2.y == a.L.max_items && h2.z == g && h2.w == D && h3.x == (int)gridDim.x && h1.x >= 1 &&
                h1.x <= kChunkMax && h0.w <= a.L.max_items;
     };
@@ -1072,7 +1076,9 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 if (d1.y == 0) { first = false; continue; }   // an empty first-wave item (a bad row)
                 const int row = d0.x, kvh = d0.y >> 16, chunk = d0.y & 0xffff, nch = d0.z, slot = d0.w;
                 const int first = d1.x, npg = d1.y, pos = d1.z, lo = d1.w;
-                good = row >= 0 && row < a.rows && kvh < Hk && chunk < nch && slot >= 0 && slot < n_items &&
+                int slots = n_items;
+                if constexpr (kShared) slots = lay.max_slots;
+                good = row >= 0 && row < a.rows && kvh < Hk && chunk < nch && slot >= 0 && slot < slots &&
                        npg >= 1 && npg <= chunk_pages && first >= 0 && pos >= 0 && lo >= 0 && lo <= pos &&
                        pos < a.pages_per_row * kPageSize && first + npg - 1 <= pos / kPageSize &&
                        first >= lo / kPageSize;

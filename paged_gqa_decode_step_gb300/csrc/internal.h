@@ -72,6 +72,32 @@ struct AttendArgs {
     int max_pos;            // rows at this position or past it are skipped, as the planner does
 };
 
+// Groups of rows whose tables begin with the same pages: rows [start[i],
+// start[i + 1]) share their first pages[i] pages.  The other fields are places
+// in the workspace.
+struct PrepShared {
+    int n_groups, tile_tokens, max_slots;
+    const int* start;       // [n_groups + 1]
+    const int* pages;       // [n_groups]
+    size_t groups;          // int4 per group: first unit, first tile, hidden by a window
+    size_t row_pre;         // int2 per row: its tile's first unit and blocks (0: nothing shared)
+    size_t tiles;           // SharedTile
+};
+
+// Decode attention of the rows' own pages, the shared ones being chunks too.
+struct AttendShared {
+    int max_slots;
+};
+
+struct SharedArgs {
+    int kv_heads, group, tile_tokens, head_dim, pages_per_row, num_pages;
+    float scale_log2;
+    const int* table;
+    char* ws;
+    WsLayout L;
+    size_t tiles;
+};
+
 struct PrefillPrepArgs {
     int n_tokens, rows, heads, kv_heads, head_dim, pages_per_row, num_pages, window, rope_len;
     int tile_tokens;        // tokens per tile: two halves of 128 / (heads / kv_heads)
@@ -237,6 +263,15 @@ cudaError_t launch_attend_layers(const AttendArgs& a, const AttendLayers& lay, i
 // The same over a coded cache (code 0: e4m3, 1: int8); maps over the codes.
 cudaError_t launch_attend_coded(const AttendArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
                                 int code, int grid, cudaStream_t stream);
+// The same where shared pages are chunks of the rows (csrc/attend_shared.cu; bf16).
+cudaError_t launch_attend_shared(const AttendArgs& a, const AttendShared& sh, const CUtensorMap& k_map,
+                                 const CUtensorMap& v_map, int grid, cudaStream_t stream);
+// Plan of a decode over shared prefixes (one block), then its rope + cache
+// write: two launches (bf16).
+cudaError_t launch_shared_prep(const PrepArgs& a, const PrepShared& sh, cudaStream_t stream);
+// Partial results of the shared pages (bf16), a programmatic dependent.
+cudaError_t launch_shared_prefix(const SharedArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map,
+                                 const CUtensorMap& v_map, int grid, cudaStream_t stream);
 size_t attend_smem_bytes(int dtype, int head_dim);
 // The tile list (one block), then the rope + write of every token at its
 // slot (programmatic launch that ends after the tile list): two launches.

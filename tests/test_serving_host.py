@@ -178,3 +178,41 @@ def test_pools_are_checked(b):
         b.make_pages(p, [torch.zeros(8, 2, 64, 64)])                 # not on a GPU
     with pytest.raises(TypeError):
         b.pages_update(p, None, *[None] * 6)
+
+
+def test_equal_runs_of_shared_units_fit_their_slots():
+    """The bound the workspace is sized by: merge slots of the pieces of every (tile, kv head)."""
+    import random
+    from shared_util import shared_plan
+    rng = random.Random(1)
+    for _ in range(400):
+        kv, g = rng.choice([1, 2, 3, 8, 12, 48]), rng.choice([1, 2, 3, 4, 5, 6, 7, 8])
+        groups = [(rng.choice([0, 1, 2, 3, 30, 64, 65, 300]), rng.choice([0, 3, 4, 5, 9, 100, 2000]))
+                  for _ in range(rng.choice([1, 2, 9, 40]))]
+        rows = sum(n for n, _ in groups)
+        for grid in (1, 2, 148, 152):
+            total, share, slots = shared_plan(groups, g, kv, grid)
+            assert slots <= 2 * (128 // g) * grid + 2 * rows * kv and share * grid >= total
+
+
+def test_shared_decode_is_checked(b):
+    def p(**kw):
+        base = dict(rows=2, heads=8, kv_heads=2, head_dim=64, pages_per_row=4, num_pages=8, dtype=torch.bfloat16)
+        base.update(kw)
+        return b.make_params(**base)
+
+    def call(q, n=1, at=AT, groups=AT, ws=AT, nb=1 << 40):
+        return b.lib.pdattn_decode_shared(q, n, groups, groups, at, at, at, at, at, at, at, at, ws, nb, NULL)
+
+    for kw, status in ((dict(rows=-1), 1), (dict(heads=6, kv_heads=4), 1), (dict(head_dim=96), 2),
+                       (dict(heads=32, kv_heads=2), 2), (dict(dtype=torch.float32), 2),
+                       (dict(rows=2 ** 20, pages_per_row=2 ** 12), 2)):
+        assert call(p(**kw)) == status, kw
+        assert b.lib.pdattn_last_error() and b.last_launch_count() == 0
+    assert call(p(), n=0) == b.EINVAL and call(p(), n=-1) == b.EINVAL
+    assert call(p(), groups=NULL) == b.EINVAL and call(p(), at=NULL) == b.EINVAL
+    assert call(p(), at=ctypes.c_void_p(4104)) == b.EINVAL
+    assert call(p(), ws=NULL) == b.EINVAL and call(p(), ws=ctypes.c_void_p(4096 + 128)) == b.EINVAL
+    assert call(p(rows=0), at=NULL, groups=NULL, ws=NULL) == b.OK
+    if torch.cuda.is_available():
+        assert call(p(), nb=b.lib.pdattn_shared_workspace_size(p(), 1) - 1) == b.EINVAL
