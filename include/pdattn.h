@@ -265,15 +265,17 @@ size_t pdattn_shared_workspace_size(const pdattn_params* p, int32_t n_groups);
  * (group_pages 0).  Shared pages are full: a row whose new position lies
  * in them (positions[r] / 64 < group_pages) is recorded as PDATTN_EBADPOS and
  * skipped, as is one whose position is outside the table or the rope table;
- * another list that is not a partition is PDATTN_EBADPOS too, and the call
- * attends nothing (it may have written rows' new keys and values).  The
- * entries of any row of a group may be read for its shared pages, and a bad
- * one is PDATTN_EBADPAGE.  Groups of one row, of fewer than four pages, or of
- * which a window hides some position from some row are attended row by row.
+ * a list that is not a partition of the rows is PDATTN_EBADPOS too, and the
+ * call then writes nothing.  The entries of any row of a group may be read for
+ * its shared pages, and a bad one is PDATTN_EBADPAGE.  Groups that share little
+ * (fewer than 6 pages, or 24 page reads saved in all) and groups of which a
+ * window hides some position from some row are attended row by row.
  * dtype bf16 (PDATTN_EUNSUPPORTED otherwise; f32 rows may share pages in
- * pdattn_decode_fused).  n_groups is at most the one the workspace was sized
- * for; a workspace of this call holds no plan for pdattn_attend.  Four launches,
- * each a programmatic dependent of the one before.
+ * pdattn_decode_fused).  chunk_pages is not used.  n_groups is at most the one
+ * the workspace was sized for; a plan that the workspace held is withdrawn
+ * (pdattn_attend then records PDATTN_EINVAL).  The same call on the same inputs
+ * gives the same bits.  Three launches, each a programmatic dependent of the
+ * one before.
  */
 pdattn_status pdattn_decode_shared(const pdattn_params* p, int32_t n_groups, const int32_t* group_start,
                                    const int32_t* group_pages, const void* q, const void* k_new,

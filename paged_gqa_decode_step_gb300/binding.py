@@ -462,6 +462,11 @@ def _check_coded(p, cache, ws, n, heads, ints, table, **named):
         _same_device(cache._tensors[0], ws)
 
 
+def _here():
+    """The current device, -1 without a GPU."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+
+
 def _tokens(t):
     return t.shape[0] if isinstance(t, torch.Tensor) and t.dim() else -1
 
@@ -521,6 +526,18 @@ def _check_ws(ws):
     _same_device(ws)
 
 
+def _check_all(here, ws, specs):
+    """(name, tensor, shape, dtype) of every argument and the workspace, on device `here`: one pass over each tensor's
+    attributes (0.5 us), and _expect to name what is wrong."""
+    for name, t, shape, dtype in specs:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == here >= 0
+                and t.is_contiguous()):
+            _expect(name, t, shape, dtype)
+            _same_device(t)
+    if not (isinstance(ws, torch.Tensor) and ws.get_device() == here and ws.is_contiguous()):
+        _check_ws(ws)
+
+
 def make_rotary(head_dim, theta, rot_dim=None, interleaved=False, scaling="none", factor=1.0, low=1.0, high=1.0,
                 original_len=0, whole_pairs=False, gain=0.0):
     """Rotary frequencies (host only): pairs over the first rot_dim dimensions (all by default), halves apart or
@@ -542,22 +559,28 @@ def _check_rotary(rotary):
 def rotary_tables(rotary, length, dtype, device="cuda", stream=None):
     """cos and sin [length, head_dim] for make_params: half pairs over the whole head."""
     _check_rotary(rotary)
-    cos, sin = (torch.empty(length, rotary.head_dim, dtype=dtype, device=device) for _ in range(2))
-    _same_device(cos)
+    cos = torch.empty((length, rotary.head_dim), dtype=dtype, device=device)
+    sin = torch.empty((length, rotary.head_dim), dtype=dtype, device=device)
+    if cos.get_device() != _here():
+        _same_device(cos)
     _check(lib.pdattn_rotary_tables(rotary, length, _DTYPES[dtype], cos.data_ptr(), sin.data_ptr(), _raw_stream(stream)))
     return cos, sin
 
 
-def _heads_of(name, t, n, D, dtype):
+def _heads_of(name, t, n, D, dtype, here):
     """(heads, token stride) of t [n, heads, D], its heads contiguous within a token."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.shape[0] != n or t.shape[2] != D:
-        raise ValueError(f"{name} must be a CUDA tensor [{n}, heads, {D}] of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-    h = t.shape[1]
-    if n and h and (t.stride(2) != 1 or (h > 1 and t.stride(1) != D)):
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[0] != n or shape[2] != D or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor [{n}, heads, {D}] of {dtype}, got {tuple(shape)} of {t.dtype}")
+    if t.get_device() != here:
+        _same_device(t)
+    h = shape[1]
+    token, head, one = t.stride()
+    if n and h and (one != 1 or (h > 1 and head != D)):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return h, (t.stride(0) if n > 1 else h * D)
+    return h, (token if n > 1 else h * D)
 
 
 def rotary_apply(rotary, q, k, positions, q_out, k_out, ws, inverse=False, stream=None):
@@ -568,23 +591,20 @@ def rotary_apply(rotary, q, k, positions, q_out, k_out, ws, inverse=False, strea
         raise ValueError("q must be a bf16 or f32 tensor [n, heads, D]")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out must be both given or both None")
-    n, D = q.shape[0], rotary.head_dim
-    hq, sq = _heads_of("q", q, n, D, q.dtype)
-    ho, so = _heads_of("q_out", q_out, n, D, q.dtype)
-    hk, sk, hl, sl = 0, 0, 0, 0
+    n, D, dt, here = q.shape[0], rotary.head_dim, q.dtype, _here()
+    hq, sq = _heads_of("q", q, n, D, dt, here)
+    ho, so = _heads_of("q_out", q_out, n, D, dt, here)
+    hk = sk = hl = sl = kp = kop = 0
     if k is not None:
-        hk, sk = _heads_of("k", k, n, D, q.dtype)
-        hl, sl = _heads_of("k_out", k_out, n, D, q.dtype)
-        _same_device(k, k_out)
+        hk, sk = _heads_of("k", k, n, D, dt, here)
+        hl, sl = _heads_of("k_out", k_out, n, D, dt, here)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     if ho != hq or hl != hk:
         raise ValueError("q_out and k_out must have the heads of q and k")
-    _expect("positions", positions, (n,), torch.int32)
-    _same_device(q, q_out, positions)
-    _check_ws(ws)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    _check(lib.pdattn_rotary_apply(rotary, n, _DTYPES[q.dtype], int(bool(inverse)), hq, q.data_ptr(), sq,
-                                   q_out.data_ptr(), so, hk, ptr(k), sk, ptr(k_out), sl, positions.data_ptr(),
-                                   ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+    _check_all(here, ws, (("positions", positions, (n,), torch.int32),))
+    _check(lib.pdattn_rotary_apply(rotary, n, _DTYPES[dt], 1 if inverse else 0, hq, q.data_ptr(), sq, q_out.data_ptr(), so,
+                                   hk, kp, sk, kop, sl, positions.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                   _raw_stream(stream)))
 
 
 def shared_workspace_size(p, n_groups):
@@ -602,15 +622,17 @@ def new_shared_workspace(p, n_groups, device="cuda"):
 def decode_shared(p, q, k_new, v_new, positions, table, group_start, group_pages, k_pool, v_pool, out, ws, stream=None):
     """decode_fused (bf16) where rows [group_start[i], group_start[i + 1]) hold the same first group_pages[i] pages,
     which are read once for the group; group_start [n + 1] and group_pages [n] int32."""
-    n = _tokens(group_pages)
-    _check_common(p, positions, table, k_pool, v_pool)
-    _check_q(p, q=q, k_new=k_new, v_new=v_new, out=out)
-    _expect("group_pages", group_pages, (n,), torch.int32)
-    _expect("group_start", group_start, (n + 1,), torch.int32)
-    if getattr(p, "_device", None) not in (None, torch.cuda.current_device()):
-        raise ValueError(f"rope tables or sinks are on cuda:{p._device}, not on the current device")
-    _same_device(q, k_new, v_new, positions, table, group_start, group_pages, k_pool, v_pool, out)
-    _check_ws(ws)
+    n, here, T, i32 = _tokens(group_pages), _here(), torch.bfloat16, torch.int32
+    if p.dtype != BF16:
+        raise PdattnError(EUNSUPPORTED, "shared pages are attended on the tensor cores: dtype must be bf16")
+    if getattr(p, "_device", None) not in (None, here):
+        raise ValueError(f"rope tables or sinks are on cuda:{p._device}, the current device is cuda:{here}")
+    R, D = p.rows, p.head_dim
+    qs, kv, pool = (R, p.heads, D), (R, p.kv_heads, D), (p.num_pages, p.kv_heads, 64, D)
+    _check_all(here, ws, (("q", q, qs, T), ("k_new", k_new, kv, T), ("v_new", v_new, kv, T), ("out", out, qs, T),
+                          ("positions", positions, (R,), i32), ("table", table, (R, p.pages_per_row), i32),
+                          ("k_pool", k_pool, pool, T), ("v_pool", v_pool, pool, T),
+                          ("group_pages", group_pages, (n,), i32), ("group_start", group_start, (n + 1,), i32)))
     _check(lib.pdattn_decode_shared(p, n, group_start.data_ptr(), group_pages.data_ptr(), q.data_ptr(), k_new.data_ptr(),
                                     v_new.data_ptr(), positions.data_ptr(), table.data_ptr(), k_pool.data_ptr(),
                                     v_pool.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
@@ -621,7 +643,8 @@ class Pages:
 
     def __init__(self, pools, num_pages):
         self.tensors, self.num_pages, self.device = tuple(pools), num_pages, pools[0].get_device()
-        self.array = (Pool * len(self.tensors))()
+        self.n = len(self.tensors)
+        self.array = (Pool * self.n)()
         for i, t in enumerate(self.tensors):
             self.array[i] = Pool(t.data_ptr(), t.shape[1], t.element_size() * (t.shape[3] if t.dim() == 4 else 1))
 
@@ -656,38 +679,42 @@ def new_pages_workspace(p, device="cuda"):
     return torch.zeros(pages_workspace_size(p), dtype=torch.uint8, device=device)
 
 
-def _check_pages(p, pages, ws, **named):
+def _check_pages(p, pages, here):
     if not isinstance(pages, Pages):
         raise TypeError("pages must come from make_pages")
     if pages.num_pages != p.num_pages:
         raise ValueError(f"the pools have {pages.num_pages} pages, the parameters {p.num_pages}")
-    for name, t in named.items():
-        shape = ((p.rows, p.pages_per_row) if name.startswith("table") else
-                 (p.num_pages,) if name.startswith("refs") or name == "page_map" else (p.rows,))
-        _expect(name, t, shape, torch.int32)
-    _check_ws(ws)
-    _same_device(*pages.tensors[:1], *named.values())
+    if pages.device != here:
+        _same_device(pages.tensors[0])
 
 
 def pages_update(p, pages, table, lengths, refs, parents, new_lengths, ws, table_out=None, refs_out=None, stream=None):
     """Row r continues row parents[r] (-1: nothing) with room for new_lengths[r] positions; see pdattn_pages_update.
     table and refs are updated in place, or written to table_out and refs_out."""
+    here, i32 = _here(), torch.int32
+    _check_pages(p, pages, here)
     table_out, refs_out = table if table_out is None else table_out, refs if refs_out is None else refs_out
-    _check_pages(p, pages, ws, table=table, lengths=lengths, refs=refs, parents=parents, new_lengths=new_lengths,
-                 table_out=table_out, refs_out=refs_out)
-    _check(lib.pdattn_pages_update(p, len(pages.array), pages.array, table.data_ptr(), lengths.data_ptr(),
-                                   refs.data_ptr(), parents.data_ptr(), new_lengths.data_ptr(), table_out.data_ptr(),
+    tab, row, num = (p.rows, p.pages_per_row), (p.rows,), (p.num_pages,)
+    _check_all(here, ws, (("table", table, tab, i32), ("lengths", lengths, row, i32), ("refs", refs, num, i32),
+                          ("parents", parents, row, i32), ("new_lengths", new_lengths, row, i32),
+                          ("table_out", table_out, tab, i32), ("refs_out", refs_out, num, i32)))
+    _check(lib.pdattn_pages_update(p, pages.n, pages.array, table.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
+                                   parents.data_ptr(), new_lengths.data_ptr(), table_out.data_ptr(),
                                    refs_out.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
 
 
 def pages_compact(p, pages, table, lengths, refs, page_map, ws, table_out=None, refs_out=None, stream=None):
     """Moves the pages in use to the lowest ids; page_map [num_pages] gets every page's new id or -1."""
+    here, i32 = _here(), torch.int32
+    _check_pages(p, pages, here)
     table_out, refs_out = table if table_out is None else table_out, refs if refs_out is None else refs_out
-    _check_pages(p, pages, ws, table=table, lengths=lengths, refs=refs, page_map=page_map, table_out=table_out,
-                 refs_out=refs_out)
-    _check(lib.pdattn_pages_compact(p, len(pages.array), pages.array, table.data_ptr(), lengths.data_ptr(),
-                                    refs.data_ptr(), table_out.data_ptr(), refs_out.data_ptr(), page_map.data_ptr(),
-                                    ws.data_ptr(), ws.nbytes, _raw_stream(stream)))
+    tab, num = (p.rows, p.pages_per_row), (p.num_pages,)
+    _check_all(here, ws, (("table", table, tab, i32), ("lengths", lengths, (p.rows,), i32), ("refs", refs, num, i32),
+                          ("page_map", page_map, num, i32), ("table_out", table_out, tab, i32),
+                          ("refs_out", refs_out, num, i32)))
+    _check(lib.pdattn_pages_compact(p, pages.n, pages.array, table.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
+                                    table_out.data_ptr(), refs_out.data_ptr(), page_map.data_ptr(), ws.data_ptr(),
+                                    ws.nbytes, _raw_stream(stream)))
 
 
 def check_status(ws, stream=None):

@@ -11,9 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpdattn.so")
 SOURCES = ["api.cu", "prep.cu", "attend.cu", "prefill.cu", "coded.cu", "attend_coded.cu",
-           "prefill_coded.cu", "rotary.cu", "pages.cu", "shared.cu",
-           "attend_shared.cu"]
-HEADERS = ["common.cuh", "internal.h", "attend_kernel.cuh", "coded.cuh", "umma.cuh"]
+           "prefill_coded.cu", "rotary.cu", "pages.cu", "shared.cu"]
+HEADERS = ["common.cuh", "internal.h", "attend_kernel.cuh", "coded.cuh", "umma.cuh", "shared.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

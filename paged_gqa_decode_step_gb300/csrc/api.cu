@@ -481,11 +481,11 @@ static pdattn_status check_shared(const pdattn_params* p, int32_t n_groups, int 
     if (n_groups <= 0) return fail(PDATTN_EINVAL, "n_groups must be > 0");
     if (p->dtype != PDATTN_BF16)
         return fail(PDATTN_EUNSUPPORTED, "shared pages are attended on the tensor cores: dtype must be bf16");
-    *S = shared_layout(p->rows, p->heads, p->kv_heads, p->head_dim, p->pages_per_row, p->chunk_pages, n_groups, grid);
-    // tiles of two rows or more, in blocks of two pages, are counted in 32 bits, and so are merge slots
-    if ((long long)(p->rows / 2 + 1) * (p->pages_per_row / 2 + 1) * p->kv_heads >= (1ll << 30) ||
-        S->max_slots >= (1ll << 31) || (long long)p->rows * p->kv_heads >= (1ll << 31))
-        return fail(PDATTN_EUNSUPPORTED, "rows x pages_per_row x kv_heads too large for one call");
+    *S = shared_layout(p->rows, p->heads, p->kv_heads, p->head_dim, n_groups, grid);
+    // the device counts shares of the work and partials in 32 bits
+    if ((long long)p->rows * p->kv_heads * ((long long)p->pages_per_row + 8) >= (1ll << 30) ||
+        S->pre_slots >= (1ll << 30) || S->own_slots >= (1ll << 30))
+        return fail(PDATTN_EUNSUPPORTED, "rows x kv_heads x pages_per_row too large for one decode call");
     return PDATTN_OK;
 }
 
@@ -541,7 +541,6 @@ pdattn_status pdattn_decode_shared(const pdattn_params* p, int32_t n_groups, con
     }
     if ((s = make_pool_map(&km, k_pool, p)) != PDATTN_OK) return s;
     if ((s = make_pool_map(&vm, v_pool, p)) != PDATTN_OK) return s;
-
     PrepArgs a = prep_args(p, positions, table, ws, S.w, grid);
     a.q = q;
     a.k_new = k_new;
@@ -550,34 +549,33 @@ pdattn_status pdattn_decode_shared(const pdattn_params* p, int32_t n_groups, con
     a.k_pool = k_pool;
     a.v_pool = v_pool;
     a.max_pos = position_limit(p);
-    a.rope_blocks = p->rows;
-    a.do_plan = 1;
-    PrepShared ps = {};
-    ps.n_groups = n_groups;
-    ps.tile_tokens = tile_tokens;
-    ps.max_slots = (int)S.max_slots;
-    ps.start = group_start;
-    ps.pages = group_pages;
-    ps.groups = S.groups;
-    ps.row_pre = S.row_pre;
-    ps.tiles = S.tiles;
-    cudaError_t e = launch_shared_prep(a, ps, (cudaStream_t)stream);
-    if (e != cudaSuccess) return cuda_fail(e, "shared plan + rope/write launches");
+    SharedScan sc = {};
+    sc.n_groups = n_groups;
+    sc.rows = p->rows;
+    sc.kv_heads = p->kv_heads;
+    sc.tile_tokens = tile_tokens;
+    sc.pages_per_row = p->pages_per_row;
+    sc.window = p->window;
+    sc.max_pos = a.max_pos;
+    sc.start = group_start;
+    sc.pages = group_pages;
+    sc.positions = positions;
+    cudaError_t e = launch_shared_rope(a, sc, S.row_pre, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "rope/write launch");
 
     SharedArgs sa = {};
-    sa.kv_heads = p->kv_heads;
+    sa.sc = sc;
+    sa.heads = p->heads;
     sa.group = g;
-    sa.tile_tokens = tile_tokens;
     sa.head_dim = p->head_dim;
-    sa.pages_per_row = p->pages_per_row;
     sa.num_pages = p->num_pages;
+    sa.grid = grid;
     sa.scale_log2 = scale_log2(p);
     sa.table = table;
+    sa.sinks = p->sinks;
+    sa.out = out;
     sa.ws = ws;
-    sa.L = S.w;
-    sa.tiles = S.tiles;
-    e = launch_shared_prefix(sa, qm, km, vm, grid, (cudaStream_t)stream);
-    if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+    sa.S = S;
 
     AttendArgs aa = {};
     aa.rows = p->rows;
@@ -588,7 +586,6 @@ pdattn_status pdattn_decode_shared(const pdattn_params* p, int32_t n_groups, con
     aa.pages_per_row = p->pages_per_row;
     aa.num_pages = p->num_pages;
     aa.window = p->window;
-    aa.chunk_pages = p->chunk_pages;
     aa.scale_log2 = sa.scale_log2;
     aa.q = ws + S.w.q_rot;
     aa.positions = positions;
@@ -598,10 +595,11 @@ pdattn_status pdattn_decode_shared(const pdattn_params* p, int32_t n_groups, con
     aa.ws = ws;
     aa.L = S.w;
     aa.max_pos = a.max_pos;
-    AttendShared as = {(int)S.max_slots};
-    e = launch_attend_shared(aa, as, km, vm, grid, (cudaStream_t)stream);
+    e = launch_shared_attend(sa, aa, qm, km, vm, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-    g_launches = 4;
+    e = launch_shared_join(sa, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "join launch");
+    g_launches = 3;
     return PDATTN_OK;
 }
 

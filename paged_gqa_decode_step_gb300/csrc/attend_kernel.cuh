@@ -792,10 +792,10 @@ __device__ bool first_wave_item(const AttendArgs& a, const Lay& lay, int b, int 
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
+// CTA `cta` of `n_ctas` (the whole grid, but for launches with other CTAs too).
 template <typename T, int D, int G, typename Lay, typename Code = Uncoded>
-__global__ void __launch_bounds__(Cfg<T, D, G, Code>::kThreads, 1)
-attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-              const __grid_constant__ AttendArgs a, const __grid_constant__ Lay lay) {
+__device__ __forceinline__ void attend_cta(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs& a,
+                                           const Lay& lay, const int cta, const int n_ctas) {
     using C = Cfg<T, D, G, Code>;
     constexpr bool kCoded = C::kCoded;
     constexpr int kThreads = C::kThreads, kCW = C::kCW;
@@ -803,10 +803,12 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     // Multi-layer launch: item row v is row v % layer_rows of layer
     // v / layer_rows, whose pools, output and sinks come from `lay`.
     constexpr bool kMulti = std::is_same<Lay, AttendLayers>::value;
-    // Shared prefixes: items are the rows' own pages; the shared pages'
-    // partials are chunks too, done before this launch (merge counters start
-    // at their number).
+    // Rows that share pages: the items are the rows' own pages, whose partials
+    // a later launch joins with those of the shared ones (which other CTAs of
+    // this launch attend).
     constexpr bool kShared = std::is_same<Lay, AttendShared>::value;
+    // No plan: every CTA finds its own share of the work.
+    constexpr bool kStatic = kCoded || kShared;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -864,11 +866,14 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         const size_t tbytes = (size_t)(kMulti ? a.layer_rows : a.rows) * a.pages_per_row * sizeof(int);
         if (tbytes <= kTablePrefetchMax) {
             const char* tb = reinterpret_cast<const char*>(a.table);
-            for (size_t off = ((size_t)blockIdx.x * 32 + lane) * 128; off < tbytes; off += (size_t)gridDim.x * 32 * 128)
+            for (size_t off = ((size_t)cta * 32 + lane) * 128; off < tbytes; off += (size_t)n_ctas * 32 * 128)
                 prefetch_l2(tb + off);
         }
     }
     __syncthreads();
+    if constexpr (kShared) {
+        if (warp >= kThreads / 32) return;      // the other CTAs of the launch have more warps
+    }
 
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
     const ItemDesc* items = reinterpret_cast<const ItemDesc*>(a.ws + a.L.items);
@@ -876,23 +881,23 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     float2* part_ml = reinterpret_cast<float2*>(a.ws + a.L.part_ml);
     float* part_o = reinterpret_cast<float*>(a.ws + a.L.part_o);
     const int g = a.group, Hk = a.kv_heads;
-    const int nf = kShared ? 0 : first_wave(a.rows, Hk, gridDim.x);
+    const int nf = first_wave(a.rows, Hk, n_ctas);
 
-    // Coded decode has no planner: every CTA finds its own share of the work
-    // (below) and the coding launch clears the merge counters.
+    // Coded decode and shared prefixes have no planner: every CTA finds its own
+    // share of the work (below).  (The coding launch clears the merge counters.)
     // The plan header in one round trip: four independent 16-byte loads
     // (fields status .. test_hold; see Ctrl), checked in registers.  Only
     // after the wait for the preceding launch (the planner's).
     auto read_plan = [&](int* n_items, int* chunk_pages) -> bool {
-        if constexpr (kCoded) return true;
+        if constexpr (kStatic) return true;
         const int4 h0 = __ldcg(reinterpret_cast<const int4*>(ctrl));
         const int4 h1 = __ldcg(reinterpret_cast<const int4*>(ctrl) + 1);
         const int4 h2 = __ldcg(reinterpret_cast<const int4*>(ctrl) + 2);
         const int4 h3 = __ldcg(reinterpret_cast<const int4*>(ctrl) + 3);
         *n_items = h0.w;
         *chunk_pages = h1.x;
-        return (uint32_t)h1.y == (kShared ? kSharedPlanMagic : kPlanMagic) && h1.z == a.rows && h1.w == Hk && h2.x == a.pages_per_row &&
-               h2.y == a.L.max_items && h2.z == g && h2.w == D && h3.x == (int)gridDim.x && h1.x >= 1 &&
+        return (uint32_t)h1.y == kPlanMagic && h1.z == a.rows && h1.w == Hk && h2.x == a.pages_per_row &&
+               h2.y == a.L.max_items && h2.z == g && h2.w == D && h3.x == n_ctas && h1.x >= 1 &&
                h1.x <= kChunkMax && h0.w <= a.L.max_items;
     };
 
@@ -937,7 +942,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // 2 b + 1) and of one it carries on (slot 2 b).  All from the
             // call's inputs: no wait, no plan launch (5 us) and no work cursor.
             // (The host keeps the units under 2^30.)
-            const int R = a.rows, b = blockIdx.x;
+            const int R = a.rows, b = cta;
             constexpr int U = C::kItemUnits;
             auto row_at = [&](int v, int* pos, int* lo) -> int {
                 *pos = v < R ? __ldg(a.positions + v) : -1;
@@ -952,7 +957,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 W += n ? n + U : 0;
             }
             W = (int)__reduce_add_sync(0xffffffffu, (unsigned)W) * Hk;
-            const int share = max((W + (int)gridDim.x - 1) / (int)gridDim.x, U + 1);
+            const int share = max((W + n_ctas - 1) / n_ctas, U + 1);
             const int x0 = b * share, x1 = min(W, x0 + share);
             // Shared pairs go first, so that their merges run under the pairs
             // the CTA has to itself.
@@ -999,14 +1004,109 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             if (!ok && lane == 0) fail_timeout(ctrl);
             return;
         }
+        if constexpr (kShared) {
+            // The pairs in order, as above, cut into runs that are handed out:
+            // a long one per CTA, then short ones from a cursor, since SMs
+            // that stream from HBM side by side do not advance alike (equal
+            // shares ended between 82 and 151 us in a batch of 256 rows).  A
+            // run's partial results are at most two: of a pair it starts (slot
+            // 2 k + 1) and of one it carries on (slot 2 k); a pair with shared
+            // pages that is not cut has a slot of its own, after the runs'.
+            const int R = a.rows;
+            constexpr int U = C::kItemUnits;
+            griddep_wait();
+            const int4* row_info = reinterpret_cast<const int4*>(a.ws + a.L.row_info);
+            int W = 0;
+            #pragma unroll 4
+            for (int v = lane; v < R; v += 32) {
+                const int4 ri = __ldcg(row_info + v);
+                W += ri.x >= 0 ? ri.x / kPageSize - ri.y + 1 + U : 0;
+            }
+            W = (int)__reduce_add_sync(0xffffffffu, (unsigned)W) * Hk;
+            const int share = (W + n_ctas - 1) / n_ctas;
+            const bool even = share <= 6 * (U + 1);                 // little work: one run per CTA
+            const int big = even ? max(share, U + 1) : share / 4 * 3, small = even ? big : max((share + 15) / 16, 5 * (U + 1));
+            const int x_small = min(W, big * n_ctas);
+            const int n_runs = (x_small + big - 1) / big + (W - x_small + small - 1) / small;
+            auto run_of = [&](int x) { return x < x_small ? x / big : n_ctas + (x - x_small) / small; };
+            if (cta == 0 && lane == 0) ctrl->sh_runs = n_runs;
+            // the 32 rows from r0 on: lane's pages, position, and its units with those before
+            int r0 = -32, before = 0, upto = 0, n = 0;
+            int4 ri = make_int4(-1, 0, 0, 0);
+            auto next_rows = [&]() {
+                before += __shfl_sync(0xffffffffu, upto, 31);
+                r0 += 32;
+                ri = r0 + lane < R ? __ldcg(row_info + r0 + lane) : make_int4(-1, 0, 0, 0);
+                n = ri.x >= 0 ? ri.x / kPageSize - ri.y + 1 : 0;
+                upto = n ? n + U : 0;
+                #pragma unroll
+                for (int sh = 1; sh < 32; sh <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, upto, sh);
+                    if (lane >= sh) upto += up;
+                }
+            };
+            next_rows();
+            for (int k = cta; k < n_runs && ok;) {
+                const int x0 = k < n_ctas ? k * big : x_small + (k - n_ctas) * small;
+                const int x1 = min(k < n_ctas ? x_small : W, x0 + (k < n_ctas ? big : small));
+                while (r0 < R && ok) {
+                    const int end = (before + __shfl_sync(0xffffffffu, upto, 31)) * Hk;
+                    const int start = (before + upto - (n ? n + U : 0)) * Hk;
+                    uint32_t mine = __ballot_sync(0xffffffffu, n > 0 && start < x1 && start + (n + U) * Hk > x0);
+                    while (mine && ok) {
+                        const int l = __ffs(mine) - 1;
+                        mine &= mine - 1;
+                        const int row = r0 + l, nr = __shfl_sync(0xffffffffu, n, l), rs = __shfl_sync(0xffffffffu, start, l);
+                        const int pos = __shfl_sync(0xffffffffu, ri.x, l), first = __shfl_sync(0xffffffffu, ri.y, l);
+                        const int common = __shfl_sync(0xffffffffu, ri.z, l), lo = row_lo(pos, a.window);
+                        for (int h = x0 > rs ? (x0 - rs) / (nr + U) : 0; h < Hk && ok; ++h) {
+                            const int u0 = rs + h * (nr + U) + U;       // unit of the pair's first page
+                            if (u0 >= x1) break;
+                            const int p0 = max(x0, u0) - u0, p1 = min(x1, u0 + nr) - u0;
+                            if (p0 >= p1) continue;
+                            const bool cut = p1 - p0 != nr;
+                            const int slot = cut ? 2 * k + (p0 == 0 ? 1 : 0) : common ? 2 * n_runs + row * Hk + h : -1;
+                            if (p0 == 0 && lane == 0)
+                                reinterpret_cast<int2*>(a.ws + lay.pairs)[(size_t)row * Hk + h] =
+                                    make_int2(cut ? k : slot < 0 ? -2 : -1, run_of(u0 + nr - 1) - k + 1);
+                            for (int q = p0; q < p1 && ok; q += kChunkMax) {
+                                const int npg = min(kChunkMax, p1 - q);
+                                int pid0, pid1;
+                                load_pids(row, first + q, npg, &pid0, &pid1);
+                                ok = queue_item(make_int4(row, h << 16, 1 | (q > p0 ? kCarriesOn : 0) |
+                                                                            (q + npg < p1 ? kCarriedOn : 0), slot),
+                                                make_int4(first + q, npg, pos, lo), pid0, pid1);
+                                queued += npg;
+                            }
+                        }
+                    }
+                    if (end >= x1) break;
+                    next_rows();
+                }
+                // The next run is taken when few queued pages wait to be issued.
+                if (lane == 0) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (queued - *s_issued >= C::kBacklogPages) {
+                        __nanosleep(32);
+                        if (globaltimer_ns() - t0 > 2000000000ull) { ok = false; break; }
+                    }
+                    k = ok ? n_ctas + atomicAdd(&ctrl->sh_next, 1) : n_runs;
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                k = __shfl_sync(0xffffffffu, k, 0);
+            }
+            if (ok) ok = queue_item(make_int4(0, 0, 0, 0), make_int4(0, -1, 0, 0), -1, -1);
+            if (!ok && lane == 0) fail_timeout(ctrl);
+            return;
+        }
         // The first-wave item comes from the call's inputs (positions, the
         // table), which no launch of this call writes: it is queued before
         // the wait, so that its pages load while the planner and the rope
         // launch finish.
         int4 sd0 = make_int4(0, 0, 0, 0), sd1 = make_int4(0, 0, 0, 0);
         bool static_item = false;
-        if ((int)blockIdx.x < nf) {
-            static_item = first_wave_item(a, lay, (int)blockIdx.x, lane, (int)gridDim.x, &sd0, &sd1);
+        if (cta < nf) {
+            static_item = first_wave_item(a, lay, cta, lane, n_ctas, &sd0, &sd1);
             if (static_item) {
                 int pid0, pid1;
                 load_pids(sd0.x, sd1.x, sd1.y, &pid0, &pid1);
@@ -1019,9 +1119,9 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         // Everything below reads what the preceding launch wrote.
         griddep_wait();
         int4 first_d0 = make_int4(0, 0, 0, 0), first_d1 = make_int4(0, 0, 0, 0);
-        if ((int)blockIdx.x < a.L.max_items) {
-            first_d0 = __ldcg(reinterpret_cast<const int4*>(items + blockIdx.x));
-            first_d1 = __ldcg(reinterpret_cast<const int4*>(items + blockIdx.x) + 1);
+        if (cta < a.L.max_items) {
+            first_d0 = __ldcg(reinterpret_cast<const int4*>(items + cta));
+            first_d1 = __ldcg(reinterpret_cast<const int4*>(items + cta) + 1);
         }
         int n_items = 0, chunk_pages = 0;
         const bool plan_ok = read_plan(&n_items, &chunk_pages);
@@ -1039,12 +1139,12 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // the planner's item b must be the one derived above
             const bool same = first_d0.x == sd0.x && first_d0.y == sd0.y && first_d0.z == sd0.z &&
                               first_d0.w == sd0.w && first_d1.x == sd1.x && first_d1.y == sd1.y &&
-                              first_d1.z == sd1.z && first_d1.w == sd1.w && (int)blockIdx.x < n_items;
+                              first_d1.z == sd1.z && first_d1.w == sd1.w && cta < n_items;
             if (!same && lane == 0) set_error(ctrl, kErrBadPlan);
         }
         bool first = !static_item;
         while (true) {
-            int it = (int)blockIdx.x;
+            int it = cta;
             if (!first) {
                 // Reserve the next item only when fewer than kBacklogPages
                 // queued pages wait to be issued: short items pipeline, long
@@ -1076,9 +1176,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 if (d1.y == 0) { first = false; continue; }   // an empty first-wave item (a bad row)
                 const int row = d0.x, kvh = d0.y >> 16, chunk = d0.y & 0xffff, nch = d0.z, slot = d0.w;
                 const int first = d1.x, npg = d1.y, pos = d1.z, lo = d1.w;
-                int slots = n_items;
-                if constexpr (kShared) slots = lay.max_slots;
-                good = row >= 0 && row < a.rows && kvh < Hk && chunk < nch && slot >= 0 && slot < slots &&
+                good = row >= 0 && row < a.rows && kvh < Hk && chunk < nch && slot >= 0 && slot < n_items &&
                        npg >= 1 && npg <= chunk_pages && first >= 0 && pos >= 0 && lo >= 0 && lo <= pos &&
                        pos < a.pages_per_row * kPageSize && first + npg - 1 <= pos / kPageSize &&
                        first >= lo / kPageSize;
@@ -1097,8 +1195,8 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // The last CTA to finish fetching rewinds the cursor for the next
             // launch (after a timeout too: every scheduler has left its loop).
             __threadfence();
-            if (atomicAdd(&ctrl->done_ctas, 1) == (int)gridDim.x - 1) {
-                ctrl->next_item = (int)gridDim.x;
+            if (atomicAdd(&ctrl->done_ctas, 1) == n_ctas - 1) {
+                ctrl->next_item = n_ctas;
                 ctrl->done_ctas = 0;
             }
         }
@@ -1136,7 +1234,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             int issued = 0;
             bool ok = true, aborted = false;
             // test hook, written (if at all) before the call
-            bool hold = blockIdx.x == 0 && __ldcg(&ctrl->test_hold) != 0;
+            bool hold = cta == 0 && __ldcg(&ctrl->test_hold) != 0;
             // Until the wait for the preceding launch, only the first-wave
             // item's pages are loaded: not the row's last page (this call
             // writes a slot there) and not its rotated queries (the rope
@@ -1170,7 +1268,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // Coded: the coding launch, with no planner before it, is over when
             // the first item comes; an early start would only hold the query
             // copy back behind a ring of pages.
-            if constexpr (kCoded) resolve();
+            if constexpr (kStatic) resolve();
             while (ok && !aborted) {
                 if (!wait_for(bar_ifull + 8 * islot, iphase)) { ok = false; break; }
                 const uint8_t* slotp = item_q + islot * C::kItemBytes;
@@ -1180,8 +1278,8 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 const int npg = d1.y;
                 if (npg < 0) break;             // end of the work
                 const int row = d0.x, kvh = d0.y >> 16, chunk = d0.y & 0xffff, slot = d0.w;
-                const int nch = kCoded ? d0.z & kNchMask : d0.z;
-                const bool starts = !kCoded || !(d0.z & kCarriesOn), ends = !kCoded || !(d0.z & kCarriedOn);
+                const int nch = kStatic ? d0.z & kNchMask : d0.z;
+                const bool starts = !kStatic || !(d0.z & kCarriesOn), ends = !kStatic || !(d0.z & kCarriedOn);
                 const int first_page = d1.x, pos = d1.z, lo = d1.w;
                 const int y_kv = kvh * kPageSize;
                 const uint8_t* qsrc = static_cast<const uint8_t*>(a.q) + ((size_t)row * a.heads + kvh * g) * C::kQSrcRow;
@@ -1360,7 +1458,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 sinks = lay.sinks[l];
             }
             const bool has_sink = sinks != nullptr;
-            if (nch == 1) {
+            if (kShared ? slot < 0 : nch == 1) {
                 for (int u = lane; u < g * D / 8; u += 32) {
                     const int j = u / (D / 8), d0 = (u % (D / 8)) * 8;
                     float M, L, O[8];
@@ -1383,7 +1481,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 }
                 __syncwarp();
                 int last = 0;
-                if (lane == 0) {
+                if (!kShared && lane == 0) {
                     // Release this chunk's partial and, for the last chunk to
                     // arrive, acquire every other chunk's (one acq_rel atomic).
                     const int done = atomic_add_acq_rel_gpu(merge_cnt + (size_t)row * Hk + kvh, 1);
@@ -1396,7 +1494,7 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                     // out = sum_c e^(m_c - M) o_c / sum_c e^(m_c - M) l_c over the chunks
                     const int slot0 = slot - mt.chunk;
                     auto slot_of = [&](int c) {
-                        return kCoded ? 2 * ((int)blockIdx.x - mt.chunk + c) + (c == 0 ? 1 : 0) : slot0 + c;
+                        return kCoded ? 2 * (cta - mt.chunk + c) + (c == 0 ? 1 : 0) : slot0 + c;
                     };
                     for (int u = lane; u < g * D / 8; u += 32) {
                         const int j = u / (D / 8), d0 = (u % (D / 8)) * 8;
@@ -1523,6 +1621,13 @@ attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         }
         if (++eslot == C::kEpiSlots) { eslot = 0; ephase ^= 1; }
     }
+}
+
+template <typename T, int D, int G, typename Lay, typename Code = Uncoded>
+__global__ void __launch_bounds__(Cfg<T, D, G, Code>::kThreads, 1)
+attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+              const __grid_constant__ AttendArgs a, const __grid_constant__ Lay lay) {
+    attend_cta<T, D, G, Lay, Code>(k_map, v_map, a, lay, (int)blockIdx.x, (int)gridDim.x);
 }
 
 // ---------------------------------------------------------------------------

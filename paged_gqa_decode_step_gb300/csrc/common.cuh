@@ -18,8 +18,6 @@ constexpr int kItemsPerCta = 4;       // planner's target work items per persist
 constexpr uint32_t kPlanMagic = 0x70646174u;
 constexpr uint32_t kCodedPlanMagic = 0x70646163u;   // of a coded prefill: no other call runs it
 
-constexpr uint32_t kSharedPlanMagic = 0x70646173u;  // of a decode over shared prefixes: likewise
-
 // Status bits in the workspace's status word.
 constexpr int kErrBadPage = 1;
 constexpr int kErrBadPos = 2;
@@ -41,8 +39,9 @@ struct Ctrl {
     // attention kernel leaves the first stage of its first item unissued, so
     // that the consumers' bounded wait on it runs out (the timeout path).
     int test_hold;
-    // Shared prefixes: tiles, units (blocks of every tile and kv head) in all, and per CTA.
-    int sh_tiles, sh_blocks, sh_share;
+    // Shared prefixes: units per CTA of the shared pages; runs of the rows' own
+    // pages and the next one that no CTA has taken.
+    int sh_share, sh_runs, sh_next;
     int pad[47];
 };
 static_assert(sizeof(Ctrl) == 256, "control block is 256 bytes");
@@ -195,54 +194,6 @@ __host__ __device__ inline PfLayout pk_layout(int n_tokens, int heads, int kv_he
     L.blk = off; off = align256(off + sizeof(int4) * blocks);
     L.total = off;
     return L;
-}
-
-// ---------------------------------------------------------------------------
-// Decode over shared prefixes: tiles of a group's rows, in units of blocks of
-// 128 keys (two pages) that equal runs of CTAs share.
-// ---------------------------------------------------------------------------
-
-// Rows [t0, t0 + ntok) of a group over its npg shared pages, nb = ceil(npg / 2)
-// blocks; the units of kv head h start at start + h * nb.
-struct __align__(32) SharedTile {
-    int t0, ntok, start, nb;
-    int npg, pad[3];
-};
-static_assert(sizeof(SharedTile) == 32, "shared tile descriptor is 32 bytes");
-
-// Most CTAs that nb units in a row can belong to, at `share` units a CTA.
-__host__ __device__ __forceinline__ int shared_pieces(int nb, int share) { return (nb + share - 2) / share + 1; }
-
-// WsLayout of a decode step whose chunks' partials are joined by those of the
-// shared pages.  Units of (tile, kv head) pairs are cut into at most nb / share
-// + 2 pieces; summed over the pairs' rows that is at most tile_tokens per CTA
-// (nb * pairs / share <= CTAs) and 2 per (row, kv head).
-struct ShLayout {
-    WsLayout w;
-    size_t groups, row_pre, tiles, total;
-    long long max_slots;
-};
-
-inline ShLayout shared_layout(int rows, int heads, int kv_heads, int head_dim, int pages_per_row, int chunk_pages,
-                              int n_groups, int grid) {
-    ShLayout S;
-    WsLayout& L = S.w;
-    const int g = heads / kv_heads, tile_tokens = 2 * (kPfRows / g);
-    L.max_items = plan_max_items(rows, kv_heads, pages_per_row, chunk_pages, grid);
-    S.max_slots = (long long)L.max_items + (long long)tile_tokens * grid + 2ll * rows * kv_heads;
-    size_t off = 0;
-    L.ctrl = off; off += 256;
-    L.row_info = off; off = align256(off + sizeof(int4) * (size_t)rows);
-    L.items = off; off = align256(off + sizeof(ItemDesc) * (size_t)L.max_items);
-    L.merge_cnt = off; off = align256(off + sizeof(int) * (size_t)rows * kv_heads);
-    L.part_ml = off; off = align256(off + sizeof(float2) * (size_t)S.max_slots * g);
-    L.part_o = off; off = align256(off + sizeof(float) * (size_t)S.max_slots * g * head_dim);
-    L.q_rot = off; off = align256(off + (size_t)2 * rows * heads * head_dim);
-    S.groups = off; off = align256(off + sizeof(int4) * (size_t)n_groups);
-    S.row_pre = off; off = align256(off + sizeof(int2) * (size_t)rows);
-    S.tiles = off; off = align256(off + sizeof(SharedTile) * (size_t)rows);
-    L.total = S.total = off;
-    return S;
 }
 
 // ---------------------------------------------------------------------------

@@ -73,29 +73,61 @@ struct AttendArgs {
 };
 
 // Groups of rows whose tables begin with the same pages: rows [start[i],
-// start[i + 1]) share their first pages[i] pages.  The other fields are places
-// in the workspace.
-struct PrepShared {
-    int n_groups, tile_tokens, max_slots;
+// start[i + 1]) share their first pages[i] pages.
+struct SharedScan {
+    int n_groups, rows, kv_heads, tile_tokens, pages_per_row, window, max_pos;
     const int* start;       // [n_groups + 1]
     const int* pages;       // [n_groups]
-    size_t groups;          // int4 per group: first unit, first tile, hidden by a window
-    size_t row_pre;         // int2 per row: its tile's first unit and blocks (0: nothing shared)
-    size_t tiles;           // SharedTile
+    const int* positions;
 };
 
-// Decode attention of the rows' own pages, the shared ones being chunks too.
+// Workspace of a decode over shared prefixes.  Pieces of the shared pages need
+// at most tile_tokens partial slots per CTA and 2 per (row, kv head) and one
+// per group (csrc/shared.cuh: the units are at most `share` per CTA); the own
+// pages two per run, and one per (row, kv head) that no run cuts.
+constexpr int kSharedRuns = 8;           // runs of own pages per CTA, at most (a long one and up to 6 short ones)
+
+struct ShLayout {
+    WsLayout w;             // ctrl, row_info, part_ml and part_o (own pages), q_rot
+    size_t row_pre, pairs, pre_ml, pre_o, total;
+    long long pre_slots, own_slots;
+};
+
+inline ShLayout shared_layout(int rows, int heads, int kv_heads, int head_dim, int n_groups, int grid) {
+    ShLayout S = {};
+    WsLayout& L = S.w;
+    const int g = heads / kv_heads, tile_tokens = 2 * (kPfRows / g);
+    S.pre_slots = (long long)tile_tokens * grid + 2ll * rows * kv_heads + n_groups;
+    S.own_slots = 2ll * kSharedRuns * grid + (long long)rows * kv_heads;
+    size_t off = 0;
+    L.ctrl = off; off += 256;
+    L.row_info = off; off = align256(off + sizeof(int4) * (size_t)rows);
+    L.part_ml = off; off = align256(off + sizeof(float2) * (size_t)S.own_slots * g);
+    L.part_o = off; off = align256(off + sizeof(float) * (size_t)S.own_slots * g * head_dim);
+    L.q_rot = off; off = align256(off + (size_t)2 * rows * heads * head_dim);
+    S.row_pre = off; off = align256(off + sizeof(int4) * (size_t)rows);
+    S.pairs = off; off = align256(off + sizeof(int2) * (size_t)rows * kv_heads);
+    S.pre_ml = off; off = align256(off + sizeof(float2) * (size_t)S.pre_slots * g);
+    S.pre_o = off; off = align256(off + sizeof(float) * (size_t)S.pre_slots * g * head_dim);
+    L.total = S.total = off;
+    return S;
+}
+
+// Decode attention of the rows' own pages (row_info: position or -1, first own
+// page, shared pages).
 struct AttendShared {
-    int max_slots;
+    size_t pairs;           // int2 per (row, kv head): first run (-1: not cut, -2: output written) and pieces
 };
 
 struct SharedArgs {
-    int kv_heads, group, tile_tokens, head_dim, pages_per_row, num_pages;
+    SharedScan sc;
+    int heads, group, head_dim, num_pages, grid;
     float scale_log2;
     const int* table;
+    const void* sinks;
+    void* out;
     char* ws;
-    WsLayout L;
-    size_t tiles;
+    ShLayout S;
 };
 
 struct PrefillPrepArgs {
@@ -203,7 +235,7 @@ struct RotaryArgs {
 
 // Page bookkeeping (csrc/pages.cu).
 struct PagesLayout {
-    size_t info, table, rows, jobs, a, b, c, total;
+    size_t info, table, rows, jobs, a, b, c, d, total;
 };
 
 inline PagesLayout pages_layout(int rows, int pages_per_row, int num_pages) {
@@ -217,6 +249,7 @@ inline PagesLayout pages_layout(int rows, int pages_per_row, int num_pages) {
     L.a = off; off = align256(off + sizeof(int) * (size_t)num_pages);
     L.b = off; off = align256(off + sizeof(int) * (size_t)num_pages);
     L.c = off; off = align256(off + sizeof(int) * (size_t)num_pages);
+    L.d = off; off = align256(off + sizeof(int) * (size_t)num_pages);
     L.total = off;
     return L;
 }
@@ -263,15 +296,13 @@ cudaError_t launch_attend_layers(const AttendArgs& a, const AttendLayers& lay, i
 // The same over a coded cache (code 0: e4m3, 1: int8); maps over the codes.
 cudaError_t launch_attend_coded(const AttendArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
                                 int code, int grid, cudaStream_t stream);
-// The same where shared pages are chunks of the rows (csrc/attend_shared.cu; bf16).
-cudaError_t launch_attend_shared(const AttendArgs& a, const AttendShared& sh, const CUtensorMap& k_map,
-                                 const CUtensorMap& v_map, int grid, cudaStream_t stream);
-// Plan of a decode over shared prefixes (one block), then its rope + cache
-// write: two launches (bf16).
-cudaError_t launch_shared_prep(const PrepArgs& a, const PrepShared& sh, cudaStream_t stream);
-// Partial results of the shared pages (bf16), a programmatic dependent.
-cudaError_t launch_shared_prefix(const SharedArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map,
-                                 const CUtensorMap& v_map, int grid, cudaStream_t stream);
+// Decode over shared prefixes (bf16): the rope + cache write of its rows with
+// what each shares; the attention of shared and of own pages side by side; the
+// outputs from their partials.
+cudaError_t launch_shared_rope(const PrepArgs& a, const SharedScan& sc, size_t row_pre, cudaStream_t stream);
+cudaError_t launch_shared_attend(const SharedArgs& a, const AttendArgs& own, const CUtensorMap& q_map,
+                                 const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t stream);
 size_t attend_smem_bytes(int dtype, int head_dim);
 // The tile list (one block), then the rope + write of every token at its
 // slot (programmatic launch that ends after the tile list): two launches.

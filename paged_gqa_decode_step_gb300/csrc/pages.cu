@@ -1,9 +1,11 @@
 // Bookkeeping of a paged cache on the device: rows that continue, fork, start
 // anew, grow or give room back (update), and the pages in use moved to the
-// lowest ids (compact).  The table part runs as one cluster, so that its
-// phases are separated by cluster barriers (about a microsecond) and not by
-// launches; the page data is copied by a second launch that works through a
-// job list.
+// lowest ids (compact).  The table's part runs as one CTA that counts in shared
+// memory or, for more pages, as one cluster that counts in global memory, so
+// that its phases are separated by barriers and not by launches; what it costs
+// is latency, a global round trip (0.6 us) or a cluster barrier (0.7 us) after
+// another.  The page data is copied by a second launch that works through a job
+// list.
 //
 // update.  refs[x] counts the holders of page x: the rows whose first
 // ceil(length / 64) entries name it, and holders outside the table (pins).
@@ -30,28 +32,45 @@ namespace {
 
 constexpr int kPageCtas = 8;         // one cluster of the portable size
 constexpr int kPageThreads = 1024;
-constexpr int kAllThreads = kPageCtas * kPageThreads;
+constexpr int kRowsKept = 1024;      // rows whose numbers a CTA keeps in shared memory
+constexpr int kCountersPerPage = 4;  // ints of shared memory per page in one CTA
+constexpr int kAhead = 4;            // entries whose loads a thread has in flight
+constexpr int kPagesAhead = 8;
 
 // Counters at PagesArgs::L.info: the phases' totals.
 struct PagesInfo {
     int jobs;                  // page copies listed
-    int bad;                   // an error was found: nothing is written
     int live_below;            // compact: pages in use below the n-th id
-    int pad;
-    int count[kPageCtas];      // per CTA: free (update) or used (compact) pages of its range
+    int pad[2];
+    int tally[kPageCtas];      // per CTA: free (update) or used (compact) pages of its range, kBad if it found an error
 };
+constexpr int kBad = INT_MIN;  // nothing is written then
 
-__device__ __forceinline__ int cluster_rank() {
-    int r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// Every thread of the cluster; writes before it are visible after it (to loads
-// that pass L1 by: __ldcg).
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+// A CTA's place, its barrier and its view of what other CTAs write.
+template <int kCtas>
+struct Team {
+    static constexpr int kAll = kCtas * kPageThreads;
+    int cta, at;
+    __device__ Team() {
+        cta = 0;
+        if constexpr (kCtas > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(cta));
+        at = cta * kPageThreads + (int)threadIdx.x;
+    }
+    // Every thread; writes before it are visible after it, to load().
+    __device__ static void sync() {
+        if constexpr (kCtas > 1)
+            asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+        else
+            __syncthreads();
+    }
+    // A counter: in shared memory for one CTA, else past L1.
+    __device__ static int load(const int* p) {
+        if constexpr (kCtas > 1) return __ldcg(p);
+        else return *p;
+    }
+    // CTA c's pages are [from(c), from(c + 1)).
+    __device__ static int from(int n, int c) { return kCtas > 1 ? (int)((long long)n * c / kCtas) : c * n; }
+};
 
 __device__ __forceinline__ int pages_of(int positions) { return (positions + kPageSize - 1) / kPageSize; }
 
@@ -82,228 +101,329 @@ __device__ __forceinline__ int block_excl(int v, int* s_warp, int* total) {
     return before;
 }
 
-// CTA c's pages [page_from(c), page_from(c + 1)).
-__device__ __forceinline__ int page_from(int n, int c) { return (int)((long long)n * c / kPageCtas); }
-
-// What row r keeps: its parent, positions, and whether its tail will be
-// written into.  A bad row keeps nothing (the error stops the call).
-struct Kept {
-    int parent, keep, full, pages;
-    bool part, writes;
+// A row's parent, the positions it keeps, gets and held; parent -2: bad
+// numbers (the row then counts for nothing, and the error stops the call).
+struct __align__(16) Row {
+    int parent, keep, want, held;
+    __device__ int full() const { return keep / kPageSize; }
+    __device__ bool part() const { return keep % kPageSize > 0; }
+    __device__ bool writes() const { return want > keep; }
 };
 
-__device__ __forceinline__ bool row_kept(const PagesArgs& a, int r, Kept& k) {
+__device__ __forceinline__ Row read_row(const PagesArgs& a, int r) {
     const int cap = a.pages_per_row * kPageSize;
-    const int p = __ldg(a.parents + r), want = __ldg(a.new_lengths + r);
-    k = {-1, 0, 0, 0, false, false};
-    if (p < -1 || p >= a.rows || want < 0 || want > cap) return false;
-    const int held = p >= 0 ? __ldg(a.lengths + p) : 0;
-    if (held < 0 || held > cap) return false;
-    k.parent = p;
-    k.keep = min(held, want);
-    k.full = k.keep / kPageSize;
-    k.part = k.keep % kPageSize > 0;
-    k.writes = want > k.keep;
-    k.pages = pages_of(want);
-    return true;
+    const int p = __ldg(a.parents + r), want = __ldg(a.new_lengths + r), held = __ldg(a.lengths + r);
+    const int given = p >= 0 && p < a.rows ? __ldg(a.lengths + p) : 0;
+    if (p < -1 || p >= a.rows || want < 0 || want > cap || held < 0 || held > cap || given < 0 || given > cap)
+        return {-2, 0, 0, 0};
+    return {p, min(given, want), want, held};
 }
 
-__global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
+template <int kCtas>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
     pages_update_kernel(const __grid_constant__ PagesArgs a) {
-    __shared__ int s_warp[32];
+    using T = Team<kCtas>;
+    extern __shared__ int s_counters[];
+    __shared__ Row s_row[kRowsKept];
+    __shared__ int2 s_at[kRowsKept];            // entries a row keeps, and the rank of its first fresh page
+    __shared__ int s_warp[32], s_bad, s_tally;
     griddep_launch_dependents();
-    const int cta = cluster_rank(), tid = threadIdx.x, at = cta * kPageThreads + tid;
-    const int R = a.rows, W = a.pages_per_row, N = a.num_pages, cap = W * kPageSize;
+    const T team;
+    const int cta = team.cta, at = team.at, tid = threadIdx.x;
+    const int R = a.rows, W = a.pages_per_row, N = a.num_pages;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws);
     PagesInfo* info = reinterpret_cast<PagesInfo*>(a.ws + a.L.info);
-    int* old = reinterpret_cast<int*>(a.ws + a.L.table);
+    int* kept = reinterpret_cast<int*>(a.ws + a.L.table);   // [row][page]: the parent's entry
     int2* row_at = reinterpret_cast<int2*>(a.ws + a.L.rows);
     int4* jobs = reinterpret_cast<int4*>(a.ws + a.L.jobs);
-    int* held = reinterpret_cast<int*>(a.ws + a.L.a);       // rows that held the page; then its rank among free ones
-    int* others = reinterpret_cast<int*>(a.ws + a.L.b);     // holders that do not write into it
-    int* first = reinterpret_cast<int*>(a.ws + a.L.c);      // lowest row that does; then the list of free pages
+    // rows that held the page (then its rank among its CTA's free ones), holders
+    // that do not write into it, the lowest row that does, and each CTA's free
+    // pages at its range's start
+    int* held = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.a) : s_counters;
+    int* others = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.b) : s_counters + N;
+    int* first = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.c) : s_counters + 2 * N;
+    int* list = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.d) : s_counters + 3 * N;
 
-    for (int x = at; x < N; x += kAllThreads) {
+    for (int x = at; x < N; x += T::kAll) {
         held[x] = 0;
         others[x] = 0;
         first[x] = INT_MAX;
     }
-    if (at == 0) *info = PagesInfo{};
-    cluster_sync();
-
-    // Holders, old and new.  The table is copied because a row may take over
-    // the entries of one that is being written.
+    if (at == 0) info->jobs = 0;
+    if (tid == 0) s_bad = 0;
+    if (tid < min(R, kRowsKept)) s_row[tid] = read_row(a, tid);
+    auto row = [&](int r) { return r < kRowsKept ? s_row[r] : read_row(a, r); };
     auto bad = [&](int bits) {
         set_error(ctrl, bits);
-        info->bad = 1;
+        s_bad = 1;
     };
-    for (long long i = at; i < (long long)R * W; i += kAllThreads) {
-        const int r = (int)(i / W), c = (int)(i - (long long)r * W);
-        const int len = __ldg(a.lengths + r);
-        if (len < 0 || len > cap) {
-            if (c == 0) bad(kErrBadPos);
-        } else if (c < pages_of(len)) {
-            const int x = __ldcg(a.table + i);
-            old[i] = x;
-            if (x < 0 || x >= N) bad(kErrBadPage);
-            else atomicAdd(held + x, 1);
+    T::sync();
+
+    // Holders, old and new.  What a row keeps is copied, because its parent's
+    // entries may be overwritten before they are taken over.
+    const unsigned entries = (unsigned)R * W;
+    for (unsigned i0 = at; i0 < entries; i0 += kAhead * T::kAll) {
+        int x[kAhead], y[kAhead], r[kAhead];
+        bool old[kAhead], takes[kAhead], tail[kAhead];
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned i = i0 + k * T::kAll;
+            x[k] = y[k] = 0;
+            old[k] = takes[k] = tail[k] = false;
+            if (i >= entries) continue;
+            r[k] = i / W;
+            const int c = i - r[k] * W;
+            const Row w = row(r[k]);
+            if (w.parent == -2) {
+                if (c == 0) bad(kErrBadPos);
+                continue;
+            }
+            old[k] = c < pages_of(w.held);
+            tail[k] = c == w.full() && w.part();
+            takes[k] = c < w.full() || tail[k];
+            tail[k] = tail[k] && w.writes();
+            if (old[k]) x[k] = __ldcg(a.table + i);
+            if (takes[k]) y[k] = __ldcg(a.table + (size_t)w.parent * W + c);
         }
-        Kept k;
-        if (!row_kept(a, r, k)) {
-            if (c == 0) bad(kErrBadPos);
-        } else if (k.parent >= 0 && (c < k.full || (c == k.full && k.part))) {
-            const int x = __ldcg(a.table + (size_t)k.parent * W + c);
-            if (x < 0 || x >= N) bad(kErrBadPage);
-            else if (c == k.full && k.writes) atomicMin(first + x, r);
-            else atomicAdd(others + x, 1);
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (x[k] < 0 || x[k] >= N || y[k] < 0 || y[k] >= N) {
+                bad(kErrBadPage);
+                continue;
+            }
+            if (old[k]) atomicAdd(held + x[k], 1);
+            if (takes[k]) {
+                kept[i0 + k * T::kAll] = y[k];
+                if (tail[k]) atomicMin(first + y[k], r[k]);
+                else atomicAdd(others + y[k], 1);
+            }
         }
     }
-    cluster_sync();
+    T::sync();
 
-    // Pages: pins counted in, the free ones ranked within the CTA's range.
-    const int x0 = page_from(N, cta), x1 = page_from(N, cta + 1);
+    // Pages: pins counted in, the free ones ranked within the CTA's range, a
+    // few pages in a row per thread.
+    const int x0 = T::from(N, cta), x1 = T::from(N, cta + 1);
     int n_free = 0;
-    for (int b = x0; b < x1; b += kPageThreads) {
-        const int x = b + tid;
-        bool free = false;
-        if (x < x1) {
-            const int refs = __ldcg(a.refs + x), h = __ldcg(held + x), o = __ldcg(others + x);
-            if (refs < h || refs < 0) bad(kErrBadPage);
-            const int o2 = o + refs - h;
-            const bool owned = o2 == 0 && __ldcg(first + x) < INT_MAX;
-            free = o2 == 0 && !owned;
-            others[x] = o2;
+    for (int b = x0; b < x1;) {
+        const int P = min(kPagesAhead, (x1 - b + kPageThreads - 1) / kPageThreads), x = b + tid * P;
+        int refs[kPagesAhead];
+        #pragma unroll
+        for (int k = 0; k < kPagesAhead; ++k) refs[k] = k < P && x + k < x1 ? __ldcg(a.refs + x + k) : 1;
+        uint32_t free = 0;
+        #pragma unroll
+        for (int k = 0; k < kPagesAhead; ++k) {
+            if (k >= P || x + k >= x1) continue;
+            const int h = T::load(held + x + k);
+            if (refs[k] < h || refs[k] < 0) bad(kErrBadPage);
+            const int o = T::load(others + x + k) + refs[k] - h;
+            others[x + k] = o;
+            if (o == 0 && T::load(first + x + k) == INT_MAX) free |= 1u << k;
         }
         int total;
-        const int rank = n_free + block_excl(free ? 1 : 0, s_warp, &total);
-        if (x < x1) held[x] = free ? rank : -1;
+        int rank = n_free + block_excl(__popc(free), s_warp, &total);
+        #pragma unroll
+        for (int k = 0; k < kPagesAhead; ++k) {
+            if (k >= P || x + k >= x1) continue;
+            const bool f = free >> k & 1;
+            held[x + k] = f ? rank : -1;
+            if (f) list[x0 + rank++] = x + k;
+        }
         n_free += total;
+        b += P * kPageThreads;
     }
-    if (tid == 0) info->count[cta] = n_free;
-    cluster_sync();
+    // (the last barrier of a scan, or of the phase before, orders s_bad)
+    __syncthreads();
+    if (tid == 0) {
+        s_tally = s_bad ? kBad : n_free;
+        if (kCtas > 1) info->tally[cta] = s_tally;
+    }
+    T::sync();
 
+    int have[kCtas + 1];
+    bool stop = false;
+    have[0] = 0;
+    #pragma unroll
+    for (int c = 0; c < kCtas; ++c) {
+        const int n = kCtas > 1 ? __ldcg(&info->tally[c]) : s_tally;
+        stop = stop || n == kBad;
+        have[c + 1] = have[c] + n;
+    }
+    if (stop) return;                           // the same for every CTA; info->jobs is 0: nothing is copied either
     // Rows: which tails are copied, and where each row's fresh pages start.
-    // Every CTA scans all rows and keeps the ones it will write.
+    // Every CTA scans all rows.
     int need = 0;
     for (int b = 0; b < R; b += kPageThreads) {
         const int r = b + tid;
-        int mine = 0, kept = 0;
+        int mine = 0, keeps = 0;
         if (r < R) {
-            Kept k;
-            row_kept(a, r, k);
-            kept = k.full + (k.part ? 1 : 0);
-            if (k.part && k.writes) {
-                const int x = __ldcg(a.table + (size_t)k.parent * W + k.full);
-                const bool alone = x >= 0 && x < N && __ldcg(others + x) == 0 && __ldcg(first + x) == r;
-                if (!alone) kept = k.full;
+            const Row k = row(r);
+            keeps = k.full() + (k.part() ? 1 : 0);
+            if (k.part() && k.writes()) {
+                const int x = __ldcg(kept + (size_t)r * W + k.full());
+                if (T::load(others + x) != 0 || T::load(first + x) != r) keeps = k.full();
             }
-            mine = k.pages - kept;
+            mine = pages_of(k.want) - keeps;
         }
         int total;
         const int start = need + block_excl(mine, s_warp, &total);
-        if (r < R && r % kPageCtas == cta) row_at[r] = make_int2(kept, start);
+        // (rows past the first: all CTAs write the same)
+        if (r < kRowsKept) s_at[tid] = make_int2(keeps, start);
+        else if (r < R) row_at[r] = make_int2(keeps, start);
         need += total;
     }
-    int have[kPageCtas + 1];
-    have[0] = 0;
-    #pragma unroll
-    for (int c = 0; c < kPageCtas; ++c) have[c + 1] = have[c] + __ldcg(&info->count[c]);
-    const bool stop = __ldcg(&info->bad) != 0;
-    if (stop || need > have[kPageCtas]) {
-        // info->jobs is 0: nothing is copied either
-        if (!stop && at == 0) set_error(ctrl, kErrNoPages);
+    if (need > have[kCtas]) {
+        if (at == 0) set_error(ctrl, kErrNoPages);
         return;
     }
-    // No CTA reads first[] after this barrier, which then lists the free
-    // pages by rank; none has left, as all took the same branch.
-    cluster_sync();
+    __syncthreads();
+    int base = 0;
+    #pragma unroll
+    for (int c = 0; c < kCtas; ++c) base = cta == c ? have[c] : base;
+    #pragma unroll 4
     for (int x = x0 + tid; x < x1; x += kPageThreads) {
-        const int rank = held[x];                       // this CTA's own
-        if (rank < 0) {
-            const int o = others[x];
-            a.refs_out[x] = o == 0 ? 1 : o;             // not free at 0: one writer keeps it
-        } else {
-            first[have[cta] + rank] = x;
-            a.refs_out[x] = have[cta] + rank < need ? 1 : 0;
-        }
+        const int rank = T::load(held + x), o = T::load(others + x);
+        a.refs_out[x] = rank < 0 ? max(o, 1) : base + rank < need ? 1 : 0;      // not free at 0: one writer keeps it
     }
-    cluster_sync();
-    const int rows_here = (R - cta + kPageCtas - 1) / kPageCtas;
-    for (long long i = tid; i < (long long)rows_here * W; i += kPageThreads) {
-        const int q = (int)(i / W), c = (int)(i - (long long)q * W), r = q * kPageCtas + cta;
-        Kept k;
-        row_kept(a, r, k);
-        const int2 ra = row_at[r];
-        int x = -1;
-        if (c < ra.x) x = __ldcg(old + (size_t)k.parent * W + c);
-        else if (c < k.pages) x = __ldcg(first + ra.y + c - ra.x);
-        a.table_out[(size_t)r * W + c] = x;
-        if (k.part && c == k.full && c == ra.x)         // a copied tail
-            jobs[atomicAdd(&info->jobs, 1)] =
-                make_int4(__ldcg(old + (size_t)k.parent * W + c), x, k.keep % kPageSize, 0);
+    for (unsigned i0 = at; i0 < entries; i0 += kAhead * T::kAll) {
+        int y[kAhead], x[kAhead], tokens[kAhead];
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned i = i0 + k * T::kAll;
+            tokens[k] = 0;
+            x[k] = -1;
+            if (i >= entries) continue;
+            const int r = i / W, c = i - r * W;
+            const Row w = row(r);
+            const int2 ra = r < kRowsKept ? s_at[r] : __ldcg(row_at + r);
+            if (w.part() && c == w.full() && c == ra.x) tokens[k] = w.keep % kPageSize;     // a copied tail
+            if (c < ra.x || tokens[k]) y[k] = __ldcg(kept + i);
+            if (c < ra.x) {
+                x[k] = -2;                      // y
+            } else if (c < pages_of(w.want)) {
+                const int rank = ra.y + c - ra.x;
+                int from = 0, skip = 0;
+                #pragma unroll
+                for (int q = 1; q < kCtas; ++q)
+                    if (rank >= have[q]) {
+                        from = T::from(N, q);
+                        skip = have[q];
+                    }
+                x[k] = T::load(list + from + rank - skip);
+            }
+        }
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned i = i0 + k * T::kAll;
+            if (i >= entries) continue;
+            a.table_out[i] = x[k] == -2 ? y[k] : x[k];
+            if (tokens[k]) jobs[atomicAdd(&info->jobs, 1)] = make_int4(y[k], x[k], tokens[k], 0);
+        }
     }
 }
 
-__global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
+template <int kCtas>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
     pages_compact_kernel(const __grid_constant__ PagesArgs a) {
-    __shared__ int s_warp[32];
+    using T = Team<kCtas>;
+    extern __shared__ int s_counters[];
+    __shared__ int s_warp[32], s_bad, s_tally, s_below;
     griddep_launch_dependents();
-    const int cta = cluster_rank(), tid = threadIdx.x, at = cta * kPageThreads + tid;
+    const T team;
+    const int cta = team.cta, at = team.at, tid = threadIdx.x;
     const int R = a.rows, W = a.pages_per_row, N = a.num_pages, cap = W * kPageSize;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws);
     PagesInfo* info = reinterpret_cast<PagesInfo*>(a.ws + a.L.info);
     int4* jobs = reinterpret_cast<int4*>(a.ws + a.L.jobs);
-    int* rank = reinterpret_cast<int*>(a.ws + a.L.a);       // of a page in use among its CTA's; ~rank of a free one
-    int* holes = reinterpret_cast<int*>(a.ws + a.L.b);      // free ids below n, in order
+    // a page in use: its rank among its CTA's; a free one: ~rank
+    int* rank = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.a) : s_counters;
+    int* holes = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.b) : s_counters + N;      // free ids below n, in order
+    int* moved = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.c) : s_counters + 2 * N;  // new ids
 
-    if (at == 0) *info = PagesInfo{};
-    cluster_sync();
+    if (at == 0) info->jobs = 0;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
     auto bad = [&](int bits) {
         set_error(ctrl, bits);
-        info->bad = 1;
+        s_bad = 1;
     };
-    const int x0 = page_from(N, cta), x1 = page_from(N, cta + 1);
-    int n_live = 0;
-    for (int b = x0; b < x1; b += kPageThreads) {
-        const int x = b + tid, refs = x < x1 ? __ldcg(a.refs + x) : 0;
-        if (refs < 0) bad(kErrBadPage);
-        int total;
-        const int q = n_live + block_excl(refs > 0 ? 1 : 0, s_warp, &total);
-        if (x < x1) rank[x] = refs > 0 ? q : ~q;
-        n_live += total;
-    }
-    if (tid == 0) info->count[cta] = n_live;
-    for (long long i = at; i < (long long)R * W; i += kAllThreads) {
-        const int r = (int)(i / W), c = (int)(i - (long long)r * W);
-        const int len = __ldg(a.lengths + r);
-        if (len < 0 || len > cap) {
-            if (c == 0) bad(kErrBadPos);
-        } else if (c < pages_of(len)) {
-            const int x = __ldcg(a.table + i);
-            if (x < 0 || x >= N || __ldcg(a.refs + x) <= 0) bad(kErrBadPage);
+    // Held entries have to be in use.
+    const unsigned entries = (unsigned)R * W;
+    for (unsigned i0 = at; i0 < entries; i0 += kAhead * T::kAll) {
+        int x[kAhead], len[kAhead];
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned i = i0 + k * T::kAll;
+            x[k] = len[k] = 0;
+            if (i >= entries) continue;
+            len[k] = __ldg(a.lengths + i / W);
+            x[k] = __ldcg(a.table + i);
+        }
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned i = i0 + k * T::kAll;
+            const int c = i % W;
+            if (len[k] < 0 || len[k] > cap) {
+                if (c == 0) bad(kErrBadPos);
+            } else if (i < entries && c < pages_of(len[k])) {
+                if (x[k] < 0 || x[k] >= N || __ldcg(a.refs + x[k]) <= 0) bad(kErrBadPage);
+            }
         }
     }
-    cluster_sync();
-    if (__ldcg(&info->bad) != 0) return;                // the same for every CTA: no barrier is left waiting
+    const int x0 = T::from(N, cta), x1 = T::from(N, cta + 1);
+    int n_live = 0;
+    for (int b = x0; b < x1;) {
+        const int P = min(kPagesAhead, (x1 - b + kPageThreads - 1) / kPageThreads), x = b + tid * P;
+        int refs[kPagesAhead];
+        #pragma unroll
+        for (int k = 0; k < kPagesAhead; ++k) refs[k] = k < P && x + k < x1 ? __ldcg(a.refs + x + k) : 0;
+        int live = 0;
+        #pragma unroll
+        for (int k = 0; k < kPagesAhead; ++k) {
+            if (refs[k] < 0) bad(kErrBadPage);
+            live += refs[k] > 0;
+        }
+        int total;
+        int q = n_live + block_excl(live, s_warp, &total);
+        #pragma unroll
+        for (int k = 0; k < kPagesAhead; ++k) {
+            if (k >= P || x + k >= x1) continue;
+            rank[x + k] = refs[k] > 0 ? q++ : ~q;
+        }
+        n_live += total;
+        b += P * kPageThreads;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        s_tally = s_bad ? kBad : n_live;
+        if (kCtas > 1) info->tally[cta] = s_tally;
+    }
+    T::sync();
     int before = 0, n = 0;
+    bool stop = false;
     #pragma unroll
-    for (int c = 0; c < kPageCtas; ++c) {
-        const int k = __ldcg(&info->count[c]);
+    for (int c = 0; c < kCtas; ++c) {
+        const int k = kCtas > 1 ? __ldcg(&info->tally[c]) : s_tally;
+        stop = stop || k == kBad;
         before += c < cta ? k : 0;
         n += k;
     }
+    if (stop) return;                           // the same for every CTA: no barrier is left waiting
     for (int x = x0 + tid; x < x1; x += kPageThreads) {
-        const int q = rank[x], up = before + (q < 0 ? ~q : q);      // pages in use below x
-        if (x == n) info->live_below = up;
+        const int q = T::load(rank + x), up = before + (q < 0 ? ~q : q);        // pages in use below x
+        if (x == n) {
+            if (kCtas > 1) info->live_below = up;
+            else s_below = up;
+        }
         if (q < 0 && x < n) holes[x - up] = x;
     }
-    cluster_sync();
-    const int below = n < N ? __ldcg(&info->live_below) : n;
+    T::sync();
+    const int below = n == N ? n : kCtas > 1 ? __ldcg(&info->live_below) : s_below;
     for (int x = x0 + tid; x < x1; x += kPageThreads) {
-        const int q = rank[x], up = before + (q < 0 ? ~q : q);
+        const int q = T::load(rank + x), up = before + (q < 0 ? ~q : q);
         int to = q < 0 ? -1 : x;
         if (q >= 0 && x >= n) {
-            to = __ldcg(holes + up - below);
+            to = T::load(holes + up - below);
             jobs[up - below] = make_int4(x, to, kPageSize, 0);
             a.refs_out[to] = __ldcg(a.refs + x);
             a.refs_out[x] = 0;
@@ -312,14 +432,26 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
         } else if (x >= n) {
             a.refs_out[x] = 0;
         }
+        moved[x] = to;
         a.map[x] = to;
     }
     if (at == 0) info->jobs = n - below;
-    cluster_sync();
-    for (long long i = at; i < (long long)R * W; i += kAllThreads) {
-        const int r = (int)(i / W), c = (int)(i - (long long)r * W);
-        const int x = __ldcg(a.table + i);
-        a.table_out[i] = c < pages_of(__ldg(a.lengths + r)) ? __ldcg(a.map + x) : x;
+    T::sync();
+    for (unsigned i0 = at; i0 < entries; i0 += kAhead * T::kAll) {
+        int x[kAhead], held[kAhead];
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned i = i0 + k * T::kAll;
+            x[k] = held[k] = 0;
+            if (i >= entries) continue;
+            held[k] = pages_of(__ldg(a.lengths + i / W));
+            x[k] = __ldcg(a.table + i);
+        }
+        #pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned i = i0 + k * T::kAll;
+            if (i < entries) a.table_out[i] = (int)(i % W) < held[k] ? T::load(moved + x[k]) : x[k];
+        }
     }
 }
 
@@ -329,11 +461,13 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyAhead = 4;
 
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PoolList pools,
-                                                                  const PagesInfo* info, const int4* jobs) {
+                                                                  const PagesInfo* info, const int4* jobs, int most) {
     griddep_wait();
+    // the first job comes with the number of jobs (`most` places are there)
+    int4 job = __ldcg(jobs + min((int)blockIdx.x / pools.slabs, most - 1));
     const long long items = (long long)__ldcg(&info->jobs) * pools.slabs;
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-        const int4 job = __ldcg(jobs + item / pools.slabs);
+        if (item >= gridDim.x) job = __ldcg(jobs + item / pools.slabs);
         int slab = (int)(item % pools.slabs), lo = 0, hi = pools.n - 1;
         while (lo < hi) {                               // the pool that holds this slab
             const int mid = (lo + hi + 1) / 2;
@@ -362,10 +496,34 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 
 }  // namespace
 
-cudaError_t launch_pages(const PagesArgs& a, bool compact, cudaStream_t stream) {
-    if (compact) pages_compact_kernel<<<kPageCtas, kPageThreads, 0, stream>>>(a);
-    else pages_update_kernel<<<kPageCtas, kPageThreads, 0, stream>>>(a);
+// One CTA where its shared memory holds the counters and its threads have few
+// entries each; else the cluster.  (Measured: see kOneCtaEntries.)
+constexpr int kOneCtaPages = 12 * 1024;
+constexpr long long kOneCtaEntries = 32 * 1024;
+
+template <typename K>
+static cudaError_t launch_team(K one, K many, const PagesArgs& a, int* configured_mask, cudaStream_t stream) {
+    if (a.num_pages > kOneCtaPages || (long long)a.rows * a.pages_per_row > kOneCtaEntries) {
+        many<<<kPageCtas, kPageThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 31 || !(__atomic_load_n(configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
+        e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kOneCtaPages * kCountersPerPage * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+        if (dev < 31) __atomic_fetch_or(configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
+    }
+    one<<<1, kPageThreads, (size_t)a.num_pages * kCountersPerPage * sizeof(int), stream>>>(a);
     return cudaGetLastError();
+}
+
+cudaError_t launch_pages(const PagesArgs& a, bool compact, cudaStream_t stream) {
+    static int update_mask = 0, compact_mask = 0;   // bit per device id < 31
+    if (compact) return launch_team(pages_compact_kernel<1>, pages_compact_kernel<kPageCtas>, a, &compact_mask, stream);
+    return launch_team(pages_update_kernel<1>, pages_update_kernel<kPageCtas>, a, &update_mask, stream);
 }
 
 cudaError_t launch_pages_copy(const PagesArgs& a, const PoolList& pools, int grid, bool after_plan, cudaStream_t stream) {
@@ -379,7 +537,7 @@ cudaError_t launch_pages_copy(const PagesArgs& a, const PoolList& pools, int gri
     cfg.attrs = attr;
     cfg.numAttrs = after_plan ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, pages_copy_kernel, pools, reinterpret_cast<const PagesInfo*>(a.ws + a.L.info),
-                              reinterpret_cast<const int4*>(a.ws + a.L.jobs));
+                              reinterpret_cast<const int4*>(a.ws + a.L.jobs), max(a.rows, a.num_pages));
 }
 
 }  // namespace pdattn

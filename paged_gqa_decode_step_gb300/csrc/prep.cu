@@ -7,7 +7,7 @@
 #include <climits>
 #include <type_traits>
 
-#include "internal.h"
+#include "shared.cuh"
 
 namespace pdattn {
 
@@ -146,17 +146,6 @@ __device__ __forceinline__ int row_window(const PrepArgs& a, const Lay& lay, int
     else return a.window;
 }
 
-// The last group that starts at or before row r.
-__device__ __forceinline__ int group_of(const int* start, int n_groups, int r) {
-    int lo = 0, hi = n_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (start[mid] <= r) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 template <typename T, typename Lay>
 __device__ void rope_write_row(const PrepArgs& a, const Lay& lay, int row) {
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
@@ -178,15 +167,6 @@ __device__ void rope_write_row(const PrepArgs& a, const Lay& lay, int row) {
     if (pos < 0 || pos >= a.max_pos) {
         if (threadIdx.x == 0) set_error(ctrl, kErrBadPos);
         return;
-    }
-    if constexpr (std::is_same<Lay, PrepShared>::value) {
-        // a row whose position lies in its group's shared pages must not write there
-        const int gi = group_of(lay.start, lay.n_groups, r);
-        const int n = __ldg(lay.pages + gi);
-        if (__ldg(lay.start + gi) > r || __ldg(lay.start + gi + 1) <= r || n < 0 || n > pos / kPageSize) {
-            if (threadIdx.x == 0) set_error(ctrl, kErrBadPos);
-            return;
-        }
     }
     const int page = __ldg(a.table + (size_t)r * a.pages_per_row + pos / kPageSize);
     const bool page_ok = page >= 0 && page < a.num_pages;
@@ -507,210 +487,6 @@ __global__ void __launch_bounds__(512) plan_kernel(const __grid_constant__ PrepA
     build_plan(a, lay);
 }
 
-// ---------------------------------------------------------------------------
-// Decode over shared prefixes.  One block: which groups share, their tiles of
-// rows and the equal runs of their units (csrc/shared.cu), and the items of
-// the rows' own pages, as build_plan lists them.  The pieces of a row's tile
-// follow its own chunks in the row's merge slots: kv head h of a row has
-// nch + P places from base + h * (nch + P), P the most pieces a pair of the
-// tile can have, of which nch plus its number of pieces are used.
-// ---------------------------------------------------------------------------
-constexpr int kSharedGroupsCap = 1024;   // groups whose starts fit the planner's shared array
-constexpr int kSharedMinRows = 2;        // smaller groups and prefixes are attended row by row
-constexpr int kSharedMinPages = 4;
-
-__device__ void build_shared_plan(const PrepArgs& a, const PrepShared& sh) {
-    __shared__ int s_start[kSharedGroupsCap + 1];
-    __shared__ int2 s_at[kPlanRowsCap];
-    __shared__ int s_cnt[kChunkMax + 1];
-    __shared__ int s_cur[kChunkMax + 1];
-    __shared__ unsigned long long s_work;
-    __shared__ int s_longest, s_slots, s_chunk;
-    __shared__ int s_scan[32];
-    Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
-    int4* row_info = reinterpret_cast<int4*>(a.ws + a.L.row_info);
-    ItemDesc* items = reinterpret_cast<ItemDesc*>(a.ws + a.L.items);
-    int* merge_cnt = reinterpret_cast<int*>(a.ws + a.L.merge_cnt);
-    int4* groups = reinterpret_cast<int4*>(a.ws + sh.groups);
-    int2* row_pre = reinterpret_cast<int2*>(a.ws + sh.row_pre);
-    SharedTile* tiles = reinterpret_cast<SharedTile*>(a.ws + sh.tiles);
-    const int tid = threadIdx.x, R = a.rows, Hk = a.kv_heads, G = sh.n_groups, Tt = sh.tile_tokens;
-
-    if (tid == 0) { s_work = 0; s_slots = 0; s_longest = 0; }
-    for (int i = tid; i <= kChunkMax; i += blockDim.x) s_cnt[i] = 0;
-    bool bad = false;
-    for (int i = tid; i <= G; i += blockDim.x) {
-        const int s0 = __ldg(sh.start + i);
-        if (i <= kSharedGroupsCap) s_start[i] = s0;
-        if (i == 0) bad = bad || s0 != 0;
-        if (i == G) {
-            bad = bad || s0 != R;
-        } else {
-            bad = bad || s0 < 0 || __ldg(sh.start + i + 1) < s0 || __ldg(sh.pages + i) < 0;
-            groups[i] = make_int4(0, 0, 0, 0);
-        }
-    }
-    auto header = [&](int n_items, int C, int n_tiles, int total, int share) {
-        ctrl->n_items = n_items;
-        ctrl->chunk_pages = C;
-        ctrl->grid = a.grid_attend;
-        ctrl->next_item = a.grid_attend;   // CTA b takes item b first without an atomic
-        ctrl->done_ctas = 0;
-        ctrl->rows = R;
-        ctrl->kv_heads = Hk;
-        ctrl->pages_per_row = a.pages_per_row;
-        ctrl->max_items = a.L.max_items;
-        ctrl->group = a.heads / Hk;
-        ctrl->head_dim = a.head_dim;
-        ctrl->sh_tiles = n_tiles;
-        ctrl->sh_blocks = total;
-        ctrl->sh_share = share;
-        ctrl->magic = kSharedPlanMagic;
-    };
-    if (__syncthreads_or(bad)) {
-        // a list that is no partition of the rows: nothing is attended
-        if (tid == 0) {
-            set_error(ctrl, kErrBadPos);
-            header(0, 1, 0, 0, 1);
-        }
-        return;
-    }
-    const int* start = G <= kSharedGroupsCap ? s_start : sh.start;
-    if (a.window > 0) {
-        for (int r = tid; r < R; r += blockDim.x) {
-            const int pos = __ldg(a.positions + r);
-            if (pos >= 0 && pos < a.max_pos && row_lo(pos, a.window) > 0)
-                __stcg(&groups[group_of(start, G, r)].z, 1);
-        }
-        __syncthreads();
-    }
-    // A group shares if it has rows enough and its rows see every shared page.
-    auto shared_by = [&](int i) -> int {
-        const int n = __ldg(sh.pages + i);
-        if (start[i + 1] - start[i] < kSharedMinRows || n < kSharedMinPages || n > a.pages_per_row) return 0;
-        return a.window > 0 && __ldcg(&groups[i].z) ? 0 : n;
-    };
-
-    // Rows: their own pages [first, pos / 64].
-    unsigned long long w = 0;
-    int longest = 0;
-    for (int r = tid; r < R; r += blockDim.x) {
-        const int pos = __ldg(a.positions + r), gi = group_of(start, G, r);
-        const bool ok = pos >= 0 && pos < a.max_pos && __ldg(sh.pages + gi) <= pos / kPageSize;
-        if (!ok) set_error(ctrl, kErrBadPos);
-        const int first = ok ? max(row_lo(pos, a.window) / kPageSize, shared_by(gi)) : 0;
-        const int n = ok ? pos / kPageSize - first + 1 : 0;
-        w += n;
-        longest = max(longest, n);
-        row_info[r] = make_int4(ok ? pos : -1, first, gi, 0);
-    }
-    w = __reduce_add_sync(0xffffffffu, (unsigned)w);
-    longest = __reduce_max_sync(0xffffffffu, (unsigned)longest);
-    if ((tid & 31) == 0) {
-        if (w) atomicAdd(&s_work, w);
-        atomicMax(&s_longest, longest);
-    }
-    // Groups: their tiles and units.
-    int n_tiles = 0, total = 0;
-    for (int b = 0; b < G; b += blockDim.x) {
-        const int i = b + tid, npg = i < G ? shared_by(i) : 0;
-        const int k = npg ? (start[i + 1] - start[i] + Tt - 1) / Tt : 0, nb = (npg + 1) / 2;
-        int sum_t, sum_u;
-        const int t = n_tiles + block_scan_excl<false>(k, 0, s_scan, &sum_t);
-        const int u = total + block_scan_excl<false>(k * nb * Hk, 0, s_scan, &sum_u);
-        if (i < G) {
-            *reinterpret_cast<int2*>(&groups[i]) = make_int2(u, t);
-            for (int j = 0; j < k; ++j) {
-                const int t0 = start[i] + j * Tt;
-                int4* dst = reinterpret_cast<int4*>(tiles + t + j);
-                dst[0] = make_int4(t0, min(Tt, start[i + 1] - t0), u + j * nb * Hk, nb);
-                dst[1] = make_int4(npg, 0, 0, 0);
-            }
-        }
-        n_tiles += sum_t;
-        total += sum_u;
-    }
-    const int share = max((total + a.grid_attend - 1) / a.grid_attend, 1);
-    __syncthreads();
-    if (tid == 0) {
-        const int c = a.chunk_pages;
-        s_chunk = c > 0 ? c : choose_chunk(s_work, s_longest, R, Hk, a.grid_attend);
-    }
-    __syncthreads();
-    const int C = s_chunk;
-
-    for (int r = tid; r < R; r += blockDim.x) {
-        const int4 ri = row_info[r];
-        const int n = ri.x >= 0 ? ri.x / kPageSize - ri.y + 1 : 0, npg = shared_by(ri.z), nb = (npg + 1) / 2;
-        const int u = npg ? __ldcg(&groups[ri.z].x) + (r - start[ri.z]) / Tt * nb * Hk : 0;
-        const Chunking ch(n, C);
-        if (ch.big) atomicAdd(&s_cnt[ch.q + 1], ch.big * Hk);
-        if (n) atomicAdd(&s_cnt[ch.q], (ch.nch - ch.big) * Hk);
-        const int base = n ? atomicAdd(&s_slots, (ch.nch + (npg ? shared_pieces(nb, share) : 0)) * Hk) : 0;
-        row_info[r] = make_int4(ri.x, ri.y, ch.nch, base);
-        row_pre[r] = make_int2(u, nb);
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int off = 0;
-        for (int s = C; s >= 1; --s) { s_cur[s] = off; off += s_cnt[s]; }
-        s_cnt[0] = off;  // total items
-    }
-    __syncthreads();
-    const int n_items = s_cnt[0];
-    const bool fits = n_items <= a.L.max_items && s_slots <= sh.max_slots;
-    // Each row reserves its places; then the (row, kv head) pairs write their
-    // items in parallel.  Rows past the shared array's capacity write their
-    // own items.
-    auto write_pair = [&](int r, int h, int4 ri, int2 pre, int2 at) {
-        const Chunking ch(ri.x / kPageSize - ri.y + 1, C);
-        int pieces = 0, most = 0;
-        if (pre.y) {
-            const int s0 = pre.x + h * pre.y;
-            pieces = (s0 + pre.y - 1) / share - s0 / share + 1;
-            most = shared_pieces(pre.y, share);
-        }
-        merge_cnt[(size_t)r * Hk + h] = pieces;
-        const int lo = row_lo(ri.x, a.window);
-        for (int c = 0; c < ri.z; ++c) {
-            int4* dst = reinterpret_cast<int4*>(items + (c < ch.big ? at.x + c * Hk + h : at.y + (c - ch.big) * Hk + h));
-            dst[0] = make_int4(r, (h << 16) | c, ri.z + pieces, ri.w + h * (ri.z + most) + c);
-            dst[1] = make_int4(ri.y + ch.start(c), ch.size(c), ri.x, lo);
-        }
-    };
-    if (fits) {
-        for (int r = tid; r < R; r += blockDim.x) {
-            const int4 ri = row_info[r];
-            int2 at = make_int2(0, 0);
-            if (ri.x >= 0) {
-                const Chunking ch(ri.x / kPageSize - ri.y + 1, C);
-                at.x = ch.big ? atomicAdd(&s_cur[ch.q + 1], ch.big * Hk) : 0;
-                at.y = atomicAdd(&s_cur[ch.q], (ri.z - ch.big) * Hk);
-                if (r >= kPlanRowsCap)
-                    for (int h = 0; h < Hk; ++h) write_pair(r, h, ri, row_pre[r], at);
-            }
-            if (r < kPlanRowsCap) s_at[r] = at;
-        }
-        __syncthreads();
-        const int Rc = R < kPlanRowsCap ? R : kPlanRowsCap;
-        for (int pr = tid; pr < Rc * Hk; pr += blockDim.x) {
-            const int r = pr / Hk;
-            const int4 ri = row_info[r];
-            if (ri.x >= 0) write_pair(r, pr % Hk, ri, row_pre[r], s_at[r]);
-        }
-    }
-    if (tid == 0) {
-        if (!fits) set_error(ctrl, kErrBadPlan);
-        header(fits ? n_items : 0, C, fits ? n_tiles : 0, total, share);
-    }
-}
-
-__global__ void __launch_bounds__(512) shared_plan_kernel(const __grid_constant__ PrepArgs a,
-                                                         const __grid_constant__ PrepShared sh) {
-    griddep_launch_dependents();
-    build_shared_plan(a, sh);
-}
-
 // RoPE and cache write: one block per row, no shared memory, so that the
 // attention launch that follows (programmatic, one CTA per SM with most of
 // the SM's shared memory) can start its prologue beside these blocks.  When
@@ -725,6 +501,40 @@ __global__ void __launch_bounds__(kRopeRowThreads) rope_write_kernel(const __gri
     griddep_launch_dependents();
     rope_write_row<T>(a, lay, blockIdx.x);
     if (a.do_plan && blockIdx.x == gridDim.x - 1) griddep_wait();
+}
+
+// Decode over shared prefixes: one block per row rotates and writes it, and
+// leaves what the attention needs of it: in row_info its position (-1: the row
+// is skipped), its first own page and the pages it shares, and in row_pre where
+// the partials of those lie.
+__global__ void __launch_bounds__(kRopeRowThreads) shared_rope_kernel(const __grid_constant__ PrepArgs a,
+                                                                      const __grid_constant__ SharedScan sc,
+                                                                      size_t row_pre) {
+    __shared__ int s_ok;
+    griddep_launch_dependents();
+    Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws + a.L.ctrl);
+    const int r = blockIdx.x;
+    if (threadIdx.x < 32) {
+        const int pos = __ldg(a.positions + r);
+        const GroupAt f = find_group<false>(sc, r, threadIdx.x);
+        // a row whose position lies in its group's shared pages must not write there
+        const bool ok = pos >= 0 && pos < a.max_pos && !f.bad && __ldg(sc.pages + f.index) <= pos / kPageSize;
+        if (threadIdx.x == 0) {
+            s_ok = ok;
+            const int nb = (f.npg + 1) / 2, q = r - f.row0;
+            reinterpret_cast<int4*>(a.ws + a.L.row_info)[r] =
+                make_int4(ok ? pos : -1, ok ? max(row_lo(pos, a.window) / kPageSize, f.npg) : 0, f.npg, 0);
+            reinterpret_cast<int4*>(a.ws + row_pre)[r] =
+                make_int4(f.unit0 + q / sc.tile_tokens * sc.kv_heads * nb, f.s1, 2 * f.s2 + f.index, q);
+            if (!ok) set_error(ctrl, kErrBadPos);
+            if (r == 0) {
+                ctrl->sh_next = 0;
+                ctrl->magic = 0;        // a plan that was here is gone
+            }
+        }
+    }
+    __syncthreads();
+    if (s_ok) rope_write_row<__nv_bfloat16>(a, NoLayers{}, r);
 }
 
 // ---------------------------------------------------------------------------
@@ -1468,20 +1278,9 @@ cudaError_t launch_prep_layers(const PrepArgs& a, const PrepLayers& lay, int dty
     return launch_prep_any(a, lay, dtype, stream, launches);
 }
 
-cudaError_t launch_shared_prep(const PrepArgs& a, const PrepShared& sh, cudaStream_t stream) {
-    shared_plan_kernel<<<1, 512, 0, stream>>>(a, sh);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.rope_blocks);
-    cfg.blockDim = dim3(kRopeRowThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_write_kernel<__nv_bfloat16, PrepShared>, a, sh);
+cudaError_t launch_shared_rope(const PrepArgs& a, const SharedScan& sc, size_t row_pre, cudaStream_t stream) {
+    shared_rope_kernel<<<a.rows, kRopeRowThreads, 0, stream>>>(a, sc, row_pre);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_prefill_prep(const PrefillPrepArgs& a, int dtype, cudaStream_t stream) {

@@ -107,26 +107,36 @@ class Case:
         return out, bound + HALF * (out.abs() + bound) + 1e-30
 
 
-def shared_plan(groups, group_size, kv_heads, grid, min_rows=2, min_pages=4):
-    """(pieces of every (tile, kv head) per CTA, merge slots used) of the equal runs: for every tile (rows, blocks) and
-    kv head the CTAs that hold some of it, checked for being each block's once."""
+def shared_slots(groups, group_size, kv_heads, ctas, min_pages=6, min_saved=24):
+    """The partial slots that the pieces of every (tile, kv head) take, as the kernels place them, checked for being
+    each piece's own; returns (units, units per CTA, one past the last slot)."""
     per = 2 * (128 // group_size)
-    tiles, total = [], 0
-    for n, p in groups:
-        if n < min_rows or p < min_pages:
-            continue
-        nb = (p + 1) // 2
-        for t in range(-(-n // per)):
-            tiles.append((min(per, n - t * per), nb, total))
-            total += nb * kv_heads
-    share = max(-(-total // grid), 1)
-    slots, worst = 0, 0
-    for rows, nb, start in tiles:
+    shared = [(i, n, (p + 1) // 2) for i, (n, p) in enumerate(groups) if p >= min_pages and (n - 1) * p >= min_saved]
+    total = sum(-(-n // per) * nb * kv_heads for _, n, nb in shared)
+    share = max(-(-total // ctas), 1)
+    unit, s1, s2, end = 0, 0, 0, 0
+    for i, n, nb in shared:
+        slot0 = s1 // share + 2 * s2 + i
+        assert slot0 >= end
         most = (nb + share - 2) // share + 1
-        for h in range(kv_heads):
-            s0 = start + h * nb
-            pieces = (s0 + nb - 1) // share - s0 // share + 1
-            assert 1 <= pieces <= most and (s0 + nb - 1) // share < grid
-            worst = max(worst, pieces)
-        slots += rows * kv_heads * most
-    return total, share, slots
+        for t in range(-(-n // per)):
+            for h in range(kv_heads):
+                u = unit + (t * kv_heads + h) * nb
+                assert 1 <= (u + nb - 1) // share - u // share + 1 <= most and (u + nb - 1) // share < ctas
+        end = slot0 + n * kv_heads * most
+        unit += -(-n // per) * nb * kv_heads
+        s1 += n * kv_heads * nb
+        s2 += n * kv_heads
+    assert unit == total
+    return total, share, end
+
+
+def own_runs(units, ctas, start=3):
+    """(long, short) runs of the rows' own pages: how many, and their number in all."""
+    share = -(-units // ctas)
+    even = share <= 6 * (start + 1)
+    big = max(share, start + 1) if even else share // 4 * 3
+    small = big if even else max((share + 15) // 16, 5 * (start + 1))
+    x = min(units, big * ctas)
+    assert -(-x // big) <= ctas
+    return -(-x // big) + -(-(units - x) // small)

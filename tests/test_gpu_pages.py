@@ -82,7 +82,8 @@ def drawn(seed, rows, hi, grow, share):
 
 @pytest.mark.parametrize("seed,rows,hi,grow,share", [(1, 1, 50, 3, 1), (2, 2, 200, 100, 1), (3, 7, 300, 1, 1),
                                                      (4, 33, 500, 200, 3), (5, 64, 130, 64, 64), (6, 150, 900, 5, 5),
-                                                     (7, 40, 64, 1, 4), (8, 1100, 90, 30, 1), (9, 2500, 130, 2, 10)])
+                                                     (7, 40, 64, 1, 4), (8, 1100, 90, 30, 1), (9, 2500, 130, 2, 10),
+                                                     (10, 900, 3000, 40, 2), (11, 3000, 800, 9, 3)])
 def test_update(seed, rows, hi, grow, share):
     lengths, parents, new = drawn(seed, rows, hi, grow, share)
     width = max(pages(n) for n in lengths + new) + 1

@@ -16,13 +16,13 @@ pytestmark = [pytest.mark.gpu,
 class Run:
     """A case's tensors on the GPU and the call on them."""
 
-    def __init__(self, c, chunk_pages=0):
+    def __init__(self, c):
         self.b, self.c = binding(), c
         up = lambda t: None if t is None else t.cuda()
         self.q, self.k, self.v, self.pos, self.table = map(up, (c.q, c.k, c.v, c.positions, c.table))
         self.start, self.pages, self.kp, self.vp = map(up, (c.start, c.pages, c.k_pool, c.v_pool))
         self.p = self.b.make_params(c.rows, c.heads, c.kv_heads, c.D, c.width, c.num_pages, BF16, window=c.window,
-                                    rope_cos=up(c.cos), rope_sin=up(c.sin), sinks=up(c.sinks), chunk_pages=chunk_pages)
+                                    rope_cos=up(c.cos), rope_sin=up(c.sin), sinks=up(c.sinks))
         self.ws = self.b.new_shared_workspace(self.p, len(c.groups))
         self.out = torch.full_like(self.q, 7.0)
 
@@ -46,32 +46,32 @@ class Run:
     def check(self, skip=()):
         self.call()
         self.b.check_status(self.ws)
-        assert self.b.last_launch_count() == 4
+        assert self.b.last_launch_count() == 3
         self.hold(skip)
 
 
 CASES = {
     # name: (groups of (rows, shared pages), own lengths, heads, kv heads, D, kwargs)
     "one row": ([(1, 9)], [5], 4, 1, 64, {}),
-    "two rows": ([(2, 4)], [1, 64], 8, 1, 128, {}),
+    "two rows": ([(2, 24)], [1, 64], 8, 1, 128, {}),
     "five samples": ([(5, 7)], [1, 100, 63, 64, 65], 64, 8, 64, dict(sinks=True)),
-    "odd pages": ([(6, 5)], [3], 4, 4, 128, {}),
+    "odd pages": ([(6, 7)], [3], 4, 4, 128, {}),
     "full half": ([(32, 6)], [10, 70], 8, 2, 128, {}),
     "half and one": ([(33, 6)], [10, 70], 8, 2, 128, {}),
-    "tile and one": ([(65, 4)], [1, 130], 8, 2, 64, dict(sinks=True)),
+    "tile and one": ([(65, 6)], [1, 130], 8, 2, 64, dict(sinks=True)),
     "groups of three heads": ([(50, 9)], [20, 200], 6, 2, 64, {}),
     "groups of five heads": ([(30, 8)], [20, 200], 10, 2, 128, {}),
     "seven heads, two tiles": ([(37, 11)], [1, 2, 3], 7, 1, 64, {}),
-    "one head": ([(300, 5)], [1, 65], 2, 2, 64, {}),
-    "several groups": ([(3, 12), (1, 8), (0, 4), (20, 4), (2, 3), (9, 31), (4, 0)], [1, 63, 64, 65, 300], 8, 2, 64, {}),
-    "nothing shared": ([(4, 0), (3, 2)], [10, 100], 8, 8, 64, {}),
+    "one head": ([(300, 7)], [1, 65], 2, 2, 64, {}),
+    "several groups": ([(3, 12), (1, 8), (0, 4), (20, 6), (2, 11), (9, 31), (4, 0), (2, 25)], [1, 63, 64, 65, 300], 8, 2, 64, {}),
+    "nothing shared": ([(4, 0), (3, 5), (2, 12)], [10, 100], 8, 8, 64, {}),
     "long prefix, one kv head": ([(3, 333)], [7], 2, 1, 128, {}),
     "long prefix": ([(40, 120)], [7, 90], 8, 2, 64, {}),
-    "many kv heads": ([(2, 6)], [9], 48, 48, 64, {}),
-    "many groups": ([(2, 4)] * 70, [1, 66], 2, 1, 64, {}),
+    "many kv heads": ([(2, 24)], [9], 48, 48, 64, {}),
+    "many groups": ([(2, 24)] * 70, [1, 66], 2, 1, 64, {}),
     "no rotation": ([(7, 10)], [30], 8, 2, 128, dict(theta=0.0)),
     "wide window": ([(7, 10)], [30, 5], 8, 2, 64, dict(window=100000)),
-    "window hides": ([(7, 10), (3, 6)], [30, 5, 400], 8, 2, 64, dict(window=500, sinks=True)),
+    "window hides": ([(7, 10), (3, 13)], [30, 5, 400], 8, 2, 64, dict(window=500, sinks=True)),
     "window inside own": ([(7, 10)], [300], 8, 2, 128, dict(window=77)),
 }
 
@@ -82,14 +82,14 @@ def test_decode_shared(name):
     Run(Case(groups, own, heads, kv, D, seed=len(name), **kw)).check()
 
 
-@pytest.mark.parametrize("chunk_pages", [1, 3, 64])
-def test_own_pages_in_given_chunks(chunk_pages):
-    Run(Case([(9, 7), (4, 4)], [1, 200, 500], 8, 2, 64, seed=5), chunk_pages).check()
+def test_own_pages_past_one_queue_slot():
+    """Rows with more than 64 own pages, whose items are handed over in pieces."""
+    Run(Case([(3, 13), (2, 4)], [70 * PAGE + 1, 30, 140 * PAGE], 2, 1, 64, seed=5)).check()
 
 
 def test_more_rows_and_groups_than_the_planner_holds_at_once():
     rng = random.Random(3)
-    groups = [(rng.choice([1, 2, 3]), rng.choice([0, 4, 5])) for _ in range(1300)]
+    groups = [(rng.choice([1, 2, 3]), rng.choice([0, 6, 13, 24])) for _ in range(1300)]
     c = Case(groups, [1, 2, 65], 1, 1, 64, seed=3)
     assert c.rows > 2048 and len(groups) > 1024
     Run(c).check()
@@ -115,7 +115,7 @@ def test_large_scores_and_one_key_that_takes_all():
 
 
 def test_infinite_and_undefined_values_reach_only_those_that_see_them():
-    c = Case([(5, 6), (4, 5)], [10, 70], 8, 2, 64, seed=9)
+    c = Case([(5, 7), (4, 9)], [10, 70], 8, 2, 64, seed=9)
     x = int(c.table[0, 2])
     c.v_pool[x, 1, 5, 7] = float("nan")            # seen by group 0, kv head 1
     r = Run(c)
@@ -141,8 +141,8 @@ def test_the_same_call_gives_the_same_bits():
 
 def test_rows_that_are_skipped():
     """Positions outside the table, negative, or inside the shared pages: those rows are skipped and write nothing."""
-    c = Case([(6, 5), (3, 4)], [40, 2], 8, 2, 64, seed=6)
-    c.positions[1], c.positions[3], c.positions[7] = -1, c.width * PAGE, 4 * PAGE - 1
+    c = Case([(6, 7), (3, 12)], [40, 2], 8, 2, 64, seed=6)
+    c.positions[1], c.positions[3], c.positions[7] = -1, c.width * PAGE, 12 * PAGE - 1
     skip = (1, 3, 7)
     r = Run(c)
     r.call()
@@ -150,7 +150,7 @@ def test_rows_that_are_skipped():
         r.b.check_status(r.ws)
     assert e.value.status == r.b.EBADPOS
     r.hold(skip)
-    c2 = Case([(6, 5), (3, 4)], [40, 2], 8, 2, 64, seed=7)       # the workspace stays usable
+    c2 = Case([(6, 7), (3, 12)], [40, 2], 8, 2, 64, seed=7)       # the workspace stays usable
     r2 = Run(c2)
     r2.ws = r.ws
     r2.check()
@@ -158,7 +158,7 @@ def test_rows_that_are_skipped():
 
 @pytest.mark.parametrize("case", ["first", "last", "falls", "negative pages", "negative start", "past"])
 def test_groups_that_are_no_partition(case):
-    c = Case([(3, 4), (2, 5), (4, 4)], [10], 8, 2, 64, seed=8)
+    c = Case([(3, 12), (2, 25), (4, 8)], [10], 8, 2, 64, seed=8)
     r = Run(c)
     if case == "first":
         r.start[0] = 1
@@ -179,7 +179,7 @@ def test_groups_that_are_no_partition(case):
 
 
 def test_shared_pages_past_the_table():
-    c = Case([(3, 4), (2, 5)], [10], 8, 2, 64, seed=8)
+    c = Case([(3, 12), (2, 25)], [10], 8, 2, 64, seed=8)
     r = Run(c)
     r.pages[1] = 1 << 30
     r.call()
@@ -191,7 +191,7 @@ def test_shared_pages_past_the_table():
 
 @pytest.mark.parametrize("bad", [-1, 1 << 20])
 def test_bad_shared_page(bad):
-    c = Case([(3, 6), (2, 5)], [10], 8, 2, 64, seed=8)
+    c = Case([(3, 13), (2, 25)], [10], 8, 2, 64, seed=8)
     r = Run(c)
     r.table[:3, 2] = bad
     r.call()
@@ -205,7 +205,7 @@ def test_bad_shared_page(bad):
 
 
 def test_in_graphs_that_share_a_workspace_with_groups_that_change():
-    c = [Case([(6, 8), (5, 4)], [30, 100], 8, 2, 64, seed=1), Case([(3, 9), (8, 5)], [77, 3], 8, 2, 64, seed=2)]
+    c = [Case([(6, 8), (5, 7)], [30, 100], 8, 2, 64, seed=1), Case([(3, 13), (8, 6)], [77, 3], 8, 2, 64, seed=2)]
     c[1].width = c[0].width = max(x.width for x in c)
     for x in c:
         pad = torch.full((x.rows, x.width - x.table.shape[1]), -1, dtype=torch.int32)
@@ -233,7 +233,7 @@ def test_in_graphs_that_share_a_workspace_with_groups_that_change():
             r.hold()
         # the same rows, grouped otherwise, through the first graph: only its device arrays change
         runs[0].start.copy_(torch.tensor([0, 6, 11], dtype=torch.int32))
-        runs[0].pages.copy_(torch.tensor([5, 0], dtype=torch.int32))
+        runs[0].pages.copy_(torch.tensor([7, 0], dtype=torch.int32))
         runs[0].out.fill_(7.0)
         graphs[0].replay()
         runs[0].b.check_status(ws, stream)
@@ -242,7 +242,7 @@ def test_in_graphs_that_share_a_workspace_with_groups_that_change():
 
 
 def test_two_calls_at_once_on_two_streams():
-    runs = [Run(Case([(20, 20), (3, 4)], [30, 100], 8, 2, 128, seed=s)) for s in (1, 2)]
+    runs = [Run(Case([(20, 20), (3, 14)], [30, 100], 8, 2, 128, seed=s)) for s in (1, 2)]
     streams = [torch.cuda.Stream() for _ in runs]
     torch.cuda.synchronize()
     for _ in range(3):

@@ -180,19 +180,22 @@ def test_pools_are_checked(b):
         b.pages_update(p, None, *[None] * 6)
 
 
-def test_equal_runs_of_shared_units_fit_their_slots():
-    """The bound the workspace is sized by: merge slots of the pieces of every (tile, kv head)."""
+def test_partials_fit_their_slots():
+    """The bounds that the workspace is sized by, whatever number of the CTAs takes the shared pages."""
     import random
-    from shared_util import shared_plan
+    from shared_util import own_runs, shared_slots
     rng = random.Random(1)
-    for _ in range(400):
+    for _ in range(300):
         kv, g = rng.choice([1, 2, 3, 8, 12, 48]), rng.choice([1, 2, 3, 4, 5, 6, 7, 8])
         groups = [(rng.choice([0, 1, 2, 3, 30, 64, 65, 300]), rng.choice([0, 3, 4, 5, 9, 100, 2000]))
                   for _ in range(rng.choice([1, 2, 9, 40]))]
         rows = sum(n for n, _ in groups)
-        for grid in (1, 2, 148, 152):
-            total, share, slots = shared_plan(groups, g, kv, grid)
-            assert slots <= 2 * (128 // g) * grid + 2 * rows * kv and share * grid >= total
+        grid = rng.choice([2, 148, 152])
+        for ctas in (1, rng.randint(1, grid), grid):
+            total, share, end = shared_slots(groups, g, kv, ctas)
+            assert end <= 2 * (128 // g) * grid + 2 * rows * kv + len(groups) and share * ctas >= total
+            for units in (0, 1, rng.randint(1, 1000), rng.randint(1, 10 ** 6)):
+                assert own_runs(units, ctas) <= 8 * grid
 
 
 def test_shared_decode_is_checked(b):
