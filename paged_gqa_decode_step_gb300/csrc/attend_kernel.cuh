@@ -72,13 +72,14 @@ constexpr int kValidShift = 16;
 template <typename T, int D>
 __host__ __device__ constexpr int q_row_bytes() { return sizeof(T) == 2 ? D * 2 + 16 : D * (int)sizeof(T); }
 
-template <typename T, int D, int G, typename Code = Uncoded>
+template <typename T, int D, int G, typename Code = Uncoded, bool kWide = false>
 struct Cfg {
     static constexpr bool kCoded = !std::is_same<Code, Uncoded>::value;
     // warp roles: consumers 0 .. kCW - 1, producer, scheduler, two epilogue warps
     // (a coded page is half the bytes of a bf16 one and the same work, so two
-    // warps per scheduler share it)
-    static constexpr int kCW = kCoded ? 2 * kConsumerWarps : kConsumerWarps;
+    // warps per scheduler share it; kWide does the same for pages of T, two of
+    // them per stage)
+    static constexpr int kCW = kCoded || kWide ? 2 * kConsumerWarps : kConsumerWarps;
     static constexpr int kProducer = kCW, kScheduler = kCW + 1, kEpilogue = kCW + 2;
     static constexpr int kThreads = (kCW + 2 + kEpilogueWarps) * 32;
     static constexpr int kElem = sizeof(T);
@@ -117,7 +118,7 @@ struct Cfg {
     // Epilogue slots: Meta, then each consumer warp's (m, l) per head and
     // its O[head][kORow] (fp32, unnormalised); the epilogue warps merge
     // them.  Two slots per epilogue warp at head dim 64, one at 128.
-    static constexpr int kEpiSlots = D == 128 ? 2 : 4;
+    static constexpr int kEpiSlots = D == 128 || kWide ? 2 : 4;
     static constexpr int kEpiHeads = kElem == 2 ? kMaxGroup : G;   // heads each warp stashes
     static constexpr int kEpiOffO = (int)sizeof(Meta) + kCW * kEpiHeads * 8;
     static constexpr int kEpiBytes = kEpiOffO + kCW * kEpiHeads * kORow * 4;
@@ -131,6 +132,7 @@ struct Cfg {
     static constexpr int kPageBytes = 2 * kTileBytes;                 // K and V of one page
     static constexpr int kBacklogPages = kBacklogBytes / kPageBytes > 2 ? kBacklogBytes / kPageBytes : 2;
     static_assert(kSmem <= 232448, "shared memory per CTA");
+    static_assert(!kWide || (kPagesPerStage == 2 && kElem == 2), "two groups of warps, a page each");
     static_assert(kOffBar % 8 == 0, "mbarrier alignment");
     static_assert(kEpiOffO % 16 == 0 && kEpiBytes % 16 == 0 && kOffEpi % 16 == 0, "16-byte stash rows");
 };
@@ -792,21 +794,27 @@ __device__ bool first_wave_item(const AttendArgs& a, const Lay& lay, int b, int 
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
+// Own pages beside shared ones (bf16): at head dim 64 four consumer warps are
+// bound by their own latency at 36 GB/s a CTA, and not all CTAs take own pages.
+template <int D>
+constexpr bool kWideOwn = D == 64;
+
 // CTA `cta` of `n_ctas` (the whole grid, but for launches with other CTAs too).
 template <typename T, int D, int G, typename Lay, typename Code = Uncoded>
 __device__ __forceinline__ void attend_cta(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs& a,
                                            const Lay& lay, const int cta, const int n_ctas) {
-    using C = Cfg<T, D, G, Code>;
+    // Rows that share pages: the items are the rows' own pages, whose partials
+    // a later launch joins with those of the shared ones (which other CTAs of
+    // this launch attend).
+    constexpr bool kShared = std::is_same<Lay, AttendShared>::value;
+    // Fewer CTAs have to keep up with HBM then.
+    using C = Cfg<T, D, G, Code, kShared && kWideOwn<D>>;
     constexpr bool kCoded = C::kCoded;
     constexpr int kThreads = C::kThreads, kCW = C::kCW;
     constexpr int kProducerWarp = C::kProducer, kSchedulerWarp = C::kScheduler, kEpilogueWarp = C::kEpilogue;
     // Multi-layer launch: item row v is row v % layer_rows of layer
     // v / layer_rows, whose pools, output and sinks come from `lay`.
     constexpr bool kMulti = std::is_same<Lay, AttendLayers>::value;
-    // Rows that share pages: the items are the rows' own pages, whose partials
-    // a later launch joins with those of the shared ones (which other CTAs of
-    // this launch attend).
-    constexpr bool kShared = std::is_same<Lay, AttendShared>::value;
     // No plan: every CTA finds its own share of the work.
     constexpr bool kStatic = kCoded || kShared;
     constexpr int S = C::kStages;
@@ -1571,6 +1579,15 @@ __device__ __forceinline__ void attend_cta(const CUtensorMap& k_map, const CUten
                     cs.page(kbase + p * C::kTileBytes, kbase + (P + p) * C::kTileBytes,
                             sbase + C::kOffScale + (stage * P + p) * C::kScaleBytes, 16 * (warp & 3), lane, lo_p, hi_p,
                             lo_p > 0 || hi_p < kPageSize);
+                }
+            } else if constexpr (kCW > kConsumerWarps) {
+                // four warps per page, every other page
+                #pragma unroll 1
+                for (int p = warp >> 2; p < np; p += kCW / 4) {
+                    if (!(mt.flags & (1 << (kValidShift + p)))) continue;
+                    const int lo_p = mt.t_lo - p * kPageSize, hi_p = mt.t_hi - p * kPageSize;
+                    cs.page(kbase + p * C::kTileBytes, kbase + (P + p) * C::kTileBytes, warp & 3, lane, lo_p, hi_p,
+                            lo_p > 0 || hi_p < kPageSize, a.scale_log2);
                 }
             } else {
                 #pragma unroll

@@ -35,6 +35,7 @@ constexpr int kPageThreads = 1024;
 constexpr int kRowsKept = 1024;      // rows whose numbers a CTA keeps in shared memory
 constexpr int kCountersPerPage = 4;  // ints of shared memory per page in one CTA
 constexpr int kAhead = 4;            // entries whose loads a thread has in flight
+constexpr int kTwo = 2;              // the same as rows x columns
 constexpr int kPagesAhead = 8;
 
 // Counters at PagesArgs::L.info: the phases' totals.
@@ -159,43 +160,53 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
     };
     T::sync();
 
+    // Lanes of a row: the power of two that its entries fill, at most a warp.
+    const int lanes = W > 16 ? 32 : W > 8 ? 16 : 8, teams = T::kAll / lanes, l = at % lanes;
+
     // Holders, old and new.  What a row keeps is copied, because its parent's
     // entries may be overwritten before they are taken over.
-    const unsigned entries = (unsigned)R * W;
-    for (unsigned i0 = at; i0 < entries; i0 += kAhead * T::kAll) {
-        int x[kAhead], y[kAhead], r[kAhead];
-        bool old[kAhead], takes[kAhead], tail[kAhead];
+    for (int r0 = at / lanes; r0 < R; r0 += kTwo * teams) {
+        int full[kTwo], n_old[kTwo], n_takes[kTwo], parent[kTwo], most = 0;
+        bool writes[kTwo];
         #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const unsigned i = i0 + k * T::kAll;
-            x[k] = y[k] = 0;
-            old[k] = takes[k] = tail[k] = false;
-            if (i >= entries) continue;
-            r[k] = i / W;
-            const int c = i - r[k] * W;
-            const Row w = row(r[k]);
-            if (w.parent == -2) {
-                if (c == 0) bad(kErrBadPos);
-                continue;
-            }
-            old[k] = c < pages_of(w.held);
-            tail[k] = c == w.full() && w.part();
-            takes[k] = c < w.full() || tail[k];
-            tail[k] = tail[k] && w.writes();
-            if (old[k]) x[k] = __ldcg(a.table + i);
-            if (takes[k]) y[k] = __ldcg(a.table + (size_t)w.parent * W + c);
+        for (int q = 0; q < kTwo; ++q) {
+            const int r = r0 + q * teams;
+            const Row w = r < R ? row(r) : Row{-1, 0, 0, 0};
+            if (w.parent == -2 && l == 0) bad(kErrBadPos);
+            parent[q] = w.parent;
+            full[q] = w.full();
+            writes[q] = w.writes();
+            n_old[q] = pages_of(w.held);
+            n_takes[q] = full[q] + (w.part() ? 1 : 0);
+            most = max(most, max(n_old[q], n_takes[q]));
         }
-        #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (x[k] < 0 || x[k] >= N || y[k] < 0 || y[k] >= N) {
-                bad(kErrBadPage);
-                continue;
+        for (int c0 = l; c0 < most; c0 += kTwo * lanes) {
+            int x[kTwo][kTwo], y[kTwo][kTwo];
+            #pragma unroll
+            for (int q = 0; q < kTwo; ++q) {
+                #pragma unroll
+                for (int k = 0; k < kTwo; ++k) {
+                    const int c = c0 + k * lanes;
+                    x[q][k] = c < n_old[q] ? __ldcg(a.table + (size_t)(r0 + q * teams) * W + c) : 0;
+                    y[q][k] = c < n_takes[q] ? __ldcg(a.table + (size_t)parent[q] * W + c) : 0;
+                }
             }
-            if (old[k]) atomicAdd(held + x[k], 1);
-            if (takes[k]) {
-                kept[i0 + k * T::kAll] = y[k];
-                if (tail[k]) atomicMin(first + y[k], r[k]);
-                else atomicAdd(others + y[k], 1);
+            #pragma unroll
+            for (int q = 0; q < kTwo; ++q) {
+                #pragma unroll
+                for (int k = 0; k < kTwo; ++k) {
+                    const int r = r0 + q * teams, c = c0 + k * lanes, xx = x[q][k], yy = y[q][k];
+                    if (xx < 0 || xx >= N || yy < 0 || yy >= N) {
+                        bad(kErrBadPage);
+                        continue;
+                    }
+                    if (c < n_old[q]) atomicAdd(held + xx, 1);
+                    if (c < n_takes[q]) {
+                        kept[(size_t)r * W + c] = yy;
+                        if (c == full[q] && writes[q]) atomicMin(first + yy, r);
+                        else atomicAdd(others + yy, 1);
+                    }
+                }
             }
         }
     }
@@ -285,39 +296,55 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
         const int rank = T::load(held + x), o = T::load(others + x);
         a.refs_out[x] = rank < 0 ? max(o, 1) : base + rank < need ? 1 : 0;      // not free at 0: one writer keeps it
     }
-    for (unsigned i0 = at; i0 < entries; i0 += kAhead * T::kAll) {
-        int y[kAhead], x[kAhead], tokens[kAhead];
+    for (int r0 = at / lanes; r0 < R; r0 += kTwo * teams) {
+        int2 ra[kTwo];
+        int n[kTwo], tail[kTwo], tokens[kTwo];
         #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const unsigned i = i0 + k * T::kAll;
-            tokens[k] = 0;
-            x[k] = -1;
-            if (i >= entries) continue;
-            const int r = i / W, c = i - r * W;
+        for (int q = 0; q < kTwo; ++q) {
+            const int r = r0 + q * teams;
+            ra[q] = make_int2(0, 0);
+            n[q] = 0;
+            tail[q] = -1;
+            if (r >= R) continue;
             const Row w = row(r);
-            const int2 ra = r < kRowsKept ? s_at[r] : __ldcg(row_at + r);
-            if (w.part() && c == w.full() && c == ra.x) tokens[k] = w.keep % kPageSize;     // a copied tail
-            if (c < ra.x || tokens[k]) y[k] = __ldcg(kept + i);
-            if (c < ra.x) {
-                x[k] = -2;                      // y
-            } else if (c < pages_of(w.want)) {
-                const int rank = ra.y + c - ra.x;
-                int from = 0, skip = 0;
-                #pragma unroll
-                for (int q = 1; q < kCtas; ++q)
-                    if (rank >= have[q]) {
-                        from = T::from(N, q);
-                        skip = have[q];
-                    }
-                x[k] = T::load(list + from + rank - skip);
-            }
+            ra[q] = r < kRowsKept ? s_at[r] : __ldcg(row_at + r);
+            n[q] = pages_of(w.want);
+            tokens[q] = w.keep % kPageSize;
+            // a tail that is not kept is copied to the first fresh page
+            if (w.part() && w.full() == ra[q].x) tail[q] = ra[q].x;
         }
-        #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const unsigned i = i0 + k * T::kAll;
-            if (i >= entries) continue;
-            a.table_out[i] = x[k] == -2 ? y[k] : x[k];
-            if (tokens[k]) jobs[atomicAdd(&info->jobs, 1)] = make_int4(y[k], x[k], tokens[k], 0);
+        for (int c0 = l; c0 < W; c0 += kTwo * lanes) {
+            int x[kTwo][kTwo], y[kTwo][kTwo];
+            #pragma unroll
+            for (int q = 0; q < kTwo; ++q) {
+                #pragma unroll
+                for (int k = 0; k < kTwo; ++k) {
+                    const int c = c0 + k * lanes;
+                    x[q][k] = -1;
+                    if (c < ra[q].x || c == tail[q]) y[q][k] = __ldcg(kept + (size_t)(r0 + q * teams) * W + c);
+                    if (c >= ra[q].x && c < n[q]) {
+                        const int rank = ra[q].y + c - ra[q].x;
+                        int at0 = 0, skip = 0;
+                        #pragma unroll
+                        for (int h = 1; h < kCtas; ++h)
+                            if (rank >= have[h]) {
+                                at0 = T::from(N, h);
+                                skip = have[h];
+                            }
+                        x[q][k] = T::load(list + at0 + rank - skip);
+                    }
+                }
+            }
+            #pragma unroll
+            for (int q = 0; q < kTwo; ++q) {
+                #pragma unroll
+                for (int k = 0; k < kTwo; ++k) {
+                    const int r = r0 + q * teams, c = c0 + k * lanes;
+                    if (r >= R || c >= W) continue;
+                    a.table_out[(size_t)r * W + c] = c < ra[q].x ? y[q][k] : x[q][k];
+                    if (c == tail[q]) jobs[atomicAdd(&info->jobs, 1)] = make_int4(y[q][k], x[q][k], tokens[q], 0);
+                }
+            }
         }
     }
 }
@@ -496,10 +523,12 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 
 }  // namespace
 
-// One CTA where its shared memory holds the counters and its threads have few
-// entries each; else the cluster.  (Measured: see kOneCtaEntries.)
-constexpr int kOneCtaPages = 12 * 1024;
-constexpr long long kOneCtaEntries = 32 * 1024;
+// One CTA for small tables, else the cluster.  update, one CTA against the
+// cluster, us: 64 x 65 entries and 4360 pages 11.5, 16.1; 16 x 512 and 4000 14.0,
+// 18.5; 256 x 40 and 4000 18.9, 14.1; 90 x 130 and 12200 24.1, 18.9; 1000 x 32 and
+// 12200 53.5, 19.5.  compact: 9 x 7 and 60 8.2, 11.8; 256 x 40 16.9, 13.1.
+constexpr int kOneCtaPages = 4608;
+constexpr long long kOneCtaEntries = 8192;
 
 template <typename K>
 static cudaError_t launch_team(K one, K many, const PagesArgs& a, int* configured_mask, cudaStream_t stream) {

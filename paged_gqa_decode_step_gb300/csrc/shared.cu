@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? kJoinWide : 9)
 template <int D>
 cudaError_t launch_d(const SharedArgs& a, const AttendArgs& own, const CUtensorMap& q_map, const CUtensorMap& k_map,
                      const CUtensorMap& v_map, cudaStream_t stream) {
-    constexpr int own_smem = Cfg<__nv_bfloat16, D, kMaxGroup>::kSmem;
+    constexpr int own_smem = Cfg<__nv_bfloat16, D, kMaxGroup, Uncoded, kWideOwn<D>>::kSmem;
     constexpr int smem = ShCfg<D>::kSmem > own_smem ? ShCfg<D>::kSmem : own_smem;
     auto kern = shared_attend_kernel<D>;
     static int configured_mask = 0;   // bit per device id < 31
