@@ -339,3 +339,30 @@ def test_samples_of_one_prompt_step_by_step():
     b.decode_shared(p, qr, kr, v, positions, table, start, count, kp, vp, again, sws)
     b.check_status(sws)
     assert torch.equal(again, outs[0])
+
+
+def test_calls_that_follow_one_another_on_a_stream():
+    """Each call's launches start while those before them end: inputs that the work just before writes (positions, the
+    table, pages, groups, queries) are read only afterwards, and a step's outputs are whole for what comes next."""
+    c = Case([(20, 20), (9, 12)], [1, 64, 130], 8, 2, 64, seed=11)
+    r = Run(c)
+    clean = [t.clone() for t in (r.q, r.k, r.v, r.pos, r.table, r.start, r.pages, r.kp, r.vp)]
+    mine = (r.q, r.k, r.v, r.pos, r.table, r.start, r.pages, r.kp, r.vp)
+    rot, rws = r.b.make_rotary(64, 1e4), r.b.new_status()
+    big = torch.zeros(200000, 8, 64, device="cuda", dtype=BF16)
+    at = torch.zeros(200000, dtype=torch.int32, device="cuda")
+    outs = []
+    for i in range(6):
+        for t in mine:
+            t.zero_()
+        if i % 2:
+            r.b.rotary_apply(rot, big, None, at, big, None, rws)      # a long kernel just before
+        for t, good in zip(mine, clean):
+            t.copy_(good)
+        r.call()
+        outs.append(r.out.clone())
+        r.out.fill_(7.0)
+    r.b.check_status(r.ws)
+    assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs)
+    r.out.copy_(outs[0])
+    r.hold()
