@@ -262,10 +262,12 @@ size_t pdattn_shared_workspace_size(const pdattn_params* p, int32_t n_groups);
  * group_start [n_groups + 1] and group_pages [n_groups] are DEVICE arrays of
  * int32, read when the call runs; group_start begins with 0, ends with rows
  * and does not fall.  A group may be empty, hold one row or share no page
- * (group_pages 0).  Shared pages are full: a row whose new position lies
- * in them (positions[r] / 64 < group_pages) is recorded as PDATTN_EBADPOS and
- * skipped, as is one whose position is outside the table or the rope table;
- * a list that is not a partition of the rows is PDATTN_EBADPOS too, and the
+ * (group_pages 0).  Shared pages are full, and no row of the call writes into
+ * a page that other rows share (the pages of pdattn_pages_update are like
+ * that): shared pages are read while the new positions are written.  A row
+ * whose new position lies in the pages its group shares (positions[r] / 64 <
+ * group_pages) is recorded as PDATTN_EBADPOS and skipped, as is one whose
+ * position is outside the table or the rope table; a list that is not a partition of the rows is PDATTN_EBADPOS too, and the
  * call then writes nothing.  The entries of any row of a group may be read for
  * its shared pages, and a bad one is PDATTN_EBADPAGE.  Groups that share little
  * (fewer than 6 pages, or 24 page reads saved in all) and groups of which a
@@ -505,7 +507,7 @@ typedef struct {
     double theta;           /* > 1 */
     double factor;          /* >= 1 */
     double low, high;       /* WAVELENGTH and RAMP: 0 < low < high */
-    double gain;            /* 0: by the scaling; else > 0 */
+    double gain;            /* 0: by the scaling; else > 0, an f32 */
 } pdattn_rotary_spec;
 
 /* Frequencies: a HOST block that pdattn_rotary_make fills and the calls read. */
@@ -563,8 +565,10 @@ pdattn_status pdattn_rotary_apply(const pdattn_rotary* rotary, int32_t n_tokens,
  * T, and the codes and the scales (row_bytes 4) of a coded cache, of every
  * layer that shares the table.  Pools are 16-byte aligned and must not
  * overlap.  `pools` is a HOST array, read during the call.  Of p only rows,
- * pages_per_row, num_pages and page_size are read.  Errors found on the
- * device (below) leave the outputs and the pools as they were.
+ * pages_per_row, num_pages and page_size are read; rows may be 0 (the arrays
+ * of rows are not read then, the pages and their counts are).  num_pages and
+ * rows * pages_per_row are below 2^30 (PDATTN_EUNSUPPORTED otherwise).  Errors
+ * found on the device (below) leave the outputs and the pools as they were.
  */
 typedef struct {
     void* data;
@@ -607,9 +611,9 @@ pdattn_status pdattn_pages_update(const pdattn_params* p, int32_t n_pools, const
  * free id below n, the others stay.  page_map [num_pages] gets each page's new
  * id, -1 for a free one (for holders outside the table).  Held table entries
  * are renamed, entries after them copied.  table_out may be table and
- * refs_out may be refs.  Errors, which change nothing: a held entry that is
- * outside the pool or free, or a negative count, is PDATTN_EBADPAGE; a bad
- * length PDATTN_EBADPOS.
+ * refs_out may be refs; page_map is none of the four.  Errors, which change
+ * nothing: a held entry that is outside the pool or free, or a negative
+ * count, is PDATTN_EBADPAGE; a bad length PDATTN_EBADPOS.
  */
 pdattn_status pdattn_pages_compact(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools,
                                    const int32_t* table, const int32_t* lengths, const int32_t* refs,

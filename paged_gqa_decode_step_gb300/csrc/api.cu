@@ -1215,7 +1215,8 @@ pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* 
         return fail(PDATTN_EINVAL, "unknown scaling %d", c.scaling);
     if (!(c.theta > 1.0) || !std::isfinite(c.theta)) return fail(PDATTN_EINVAL, "theta must be > 1");
     if (!(c.factor >= 1.0) || !std::isfinite(c.factor)) return fail(PDATTN_EINVAL, "factor must be >= 1");
-    if (!(c.gain >= 0.0) || !std::isfinite(c.gain)) return fail(PDATTN_EINVAL, "gain must be >= 0");
+    if (!(c.gain >= 0.0) || !std::isfinite((float)c.gain) || (c.gain > 0.0 && (float)c.gain == 0.f))
+        return fail(PDATTN_EINVAL, "gain must be 0 or a positive f32");
     if (c.scaling >= PDATTN_ROTARY_WAVELENGTH) {
         if (!(c.low > 0.0) || !(c.high > c.low) || !std::isfinite(c.high))
             return fail(PDATTN_EINVAL, "low and high must be 0 < low < high");
@@ -1349,8 +1350,9 @@ static pdattn_status check_pages_params(const pdattn_params* p) {
     if (p->pages_per_row <= 0 || p->num_pages <= 0) return fail(PDATTN_EINVAL, "pages_per_row and num_pages must be > 0");
     if (p->page_size != kPageSize) return fail(PDATTN_EUNSUPPORTED, "page_size must be 64");
     if ((long long)p->pages_per_row * kPageSize >= (1ll << 30)) return fail(PDATTN_EUNSUPPORTED, "pages_per_row too large");
-    // the pages wanted are counted in 32 bits
-    if ((long long)p->rows * p->pages_per_row >= (1ll << 31)) return fail(PDATTN_EUNSUPPORTED, "the table is too large");
+    // entries, pages and the pages wanted are counted in 32 bits
+    if ((long long)p->rows * p->pages_per_row >= (1ll << 30)) return fail(PDATTN_EUNSUPPORTED, "the table is too large");
+    if (p->num_pages >= (1 << 30)) return fail(PDATTN_EUNSUPPORTED, "num_pages too large");
     return PDATTN_OK;
 }
 
@@ -1371,9 +1373,9 @@ static pdattn_status pages_impl(const pdattn_params* p, int32_t n_pools, const p
         if (pools[i].heads <= 0 || pools[i].heads > 32767 || pools[i].row_bytes <= 0 || pools[i].row_bytes > 4096)
             return fail(PDATTN_EINVAL, "pool %d: heads must be in [1, 32767], row_bytes in [1, 4096]", i);
     }
-    if (p->rows == 0) return PDATTN_OK;
-    if (!a.table || !a.lengths || !a.refs || !a.table_out || !a.refs_out ||
-        (compact ? !a.map : !a.parents || !a.new_lengths))
+    // (without rows there are still pages that holders outside the table keep)
+    if (!a.refs || !a.refs_out || (compact && !a.map) ||
+        (p->rows > 0 && (!a.table || !a.lengths || !a.table_out || (!compact && (!a.parents || !a.new_lengths)))))
         return fail(PDATTN_EINVAL, "NULL data pointer");
     if (!workspace) return fail(PDATTN_EINVAL, "workspace is NULL");
     if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
@@ -1381,6 +1383,8 @@ static pdattn_status pages_impl(const pdattn_params* p, int32_t n_pools, const p
     a.L = pages_layout(p->rows, p->pages_per_row, p->num_pages);
     if (workspace_bytes < a.L.total)
         return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, a.L.total);
+    if (compact && (a.map == a.refs || a.map == a.refs_out || a.map == a.table || a.map == a.table_out))
+        return fail(PDATTN_EINVAL, "page_map must not be another argument");
     const int sms = sm_count();
     if (sms <= 0) return fail(PDATTN_ECUDA, "no CUDA device");
     a.rows = p->rows;

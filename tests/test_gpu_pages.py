@@ -37,7 +37,7 @@ class Cache:
 
     def load(self):
         s = self.s
-        self.table, self.lengths, self.refs = ints(s.table), ints(s.lengths), ints(s.refs)
+        self.table, self.lengths, self.refs = ints(s.table).view(len(s.table), s.width), ints(s.lengths), ints(s.refs)
 
     def update(self, parents, new, **kw):
         self.b.pages_update(self.p, self.pages, self.table, self.lengths, self.refs, ints(parents), ints(new), self.ws, **kw)
@@ -227,6 +227,26 @@ def test_compact(seed, rows, hi, share, spare, low):
     c.same(table, refs, copies)
     n = sum(x > 0 for x in refs)
     assert (c.refs[:n] > 0).all() and (c.refs[n:] == 0).all()
+
+
+@pytest.mark.parametrize("num_pages", [1, 40, 6000])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_pages_without_rows(num_pages, inplace):
+    # no row, but holders outside the table: counts are passed on, pages still move
+    pins = tuple(range(0, num_pages, 3)) + (0,)
+    s = State(0, 4, num_pages, [], seed=2, pins=pins)
+    c = Cache(s)
+    out = {} if inplace else dict(refs_out=torch.full_like(c.refs, 5))
+    c.update([], [], **out)
+    c.check()
+    assert torch.equal(out.get("refs_out", c.refs), ints(s.refs)) and torch.equal(c.refs, ints(s.refs))
+    _, refs, to = s.compact()
+    page_map = torch.full((num_pages,), 99, dtype=torch.int32, device="cuda")
+    c.compact(page_map, **out)
+    c.check()
+    assert torch.equal(page_map, ints(to)) and torch.equal(out.get("refs_out", c.refs), ints(refs))
+    for got, want in zip(c.pools, c.want_pools([(x, y, PAGE) for x, y in enumerate(to) if y >= 0 and y != x])):
+        assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("case", ["page high", "page free", "negative refs", "length long"])

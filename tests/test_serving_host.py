@@ -80,7 +80,7 @@ def test_frequencies_on_a_ramp(b, whole, rot, theta, factor, low, high, original
 @pytest.mark.parametrize("kw,status", [
     (dict(head_dim=96), 2), (dict(rot_dim=0), 1), (dict(rot_dim=24), 1), (dict(rot_dim=80), 1), (dict(theta=1.0), 1),
     (dict(theta=math.inf), 1), (dict(theta=math.nan), 1), (dict(factor=0.5), 1), (dict(factor=math.nan), 1),
-    (dict(gain=-1.0), 1), (dict(gain=math.inf), 1), (dict(scaling="wavelength", low=0.0, high=4.0, original_len=8), 1),
+    (dict(gain=-1.0), 1), (dict(gain=math.inf), 1), (dict(gain=1e300), 1), (dict(gain=1e-60), 1), (dict(scaling="wavelength", low=0.0, high=4.0, original_len=8), 1),
     (dict(scaling="wavelength", low=4.0, high=4.0, original_len=8), 1), (dict(scaling="ramp", low=1.0, high=4.0), 1),
     (dict(scaling="ramp", low=1.0, high=math.inf, original_len=8), 1)])
 def test_specs_are_checked(b, kw, status):
@@ -165,7 +165,22 @@ def test_page_calls_are_checked(b, call):
     assert _pages_calls(b, p(), [good], ws=ctypes.c_void_p(4096 + 128))[call]() == b.EINVAL
     assert _pages_calls(b, p(), [good], nb=b.lib.pdattn_pages_workspace_size(p()) - 1)[call]() == b.EINVAL
     assert b"workspace" in b.lib.pdattn_last_error() and b.last_launch_count() == 0
-    assert _pages_calls(b, p(rows=0), [good], at=NULL, ws=NULL)[call]() == b.OK
+    # without rows the pages and their counts are still there
+    assert _pages_calls(b, p(rows=0), [good], at=NULL)[call]() == b.EINVAL
+    assert _pages_calls(b, p(rows=0), [good], ws=NULL)[call]() == b.EINVAL
+    for kw in (dict(num_pages=2 ** 30), dict(rows=2 ** 20, pages_per_row=2 ** 10)):     # counted in 32 bits
+        assert _pages_calls(b, p(**kw), [good])[call]() == b.EUNSUPPORTED
+        assert b.lib.pdattn_pages_workspace_size(p(**kw)) == 0
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_page_map_is_its_own(b, which):
+    p = b.make_params(2, 8, 2, 64, 4, 8, torch.bfloat16)
+    pool = (b.Pool * 1)(b.Pool(4096, 2, 128))
+    at = [ctypes.c_void_p(4096 * (i + 2)) for i in range(6)]         # table, lengths, refs, table_out, refs_out, page_map
+    at[5] = at[(0, 2, 3, 4)[which]]
+    assert b.lib.pdattn_pages_compact(p, 1, pool, *at, AT, 1 << 40, NULL) == b.EINVAL
+    assert b"page_map" in b.lib.pdattn_last_error()
 
 
 def test_pools_are_checked(b):
