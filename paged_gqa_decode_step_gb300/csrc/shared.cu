@@ -618,15 +618,24 @@ __global__ void __launch_bounds__(kShThreads, 1)
 // The outputs of rows that share pages, and of pairs that were cut, from their
 // partials: four dimensions of one query head per thread.  It is bound by
 // latency: the loads of a batch of kBatch partials go out together, and where
-// there are more blocks than fit at once, batches are small and more do.
+// there are more blocks than fit at once, batches are small and more do.  Few
+// rows are cut into many pieces, which kLanes lanes then share (24 rows of 19
+// pieces and two own ones: the call 66.4 us with four, 67.5 with two, 68.6 with
+// one; batches of 12 to 24 instead: 68.9 to 72.6).
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWide = 6;         // blocks per SM that fit with batches of 8
+constexpr int kJoinFew = 2;          // blocks per SM that leave room for four times as many
+constexpr int kJoinLanes = 4;
 
-template <int kBatch>
-__global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? kJoinWide : 9)
+template <int kBatch, int kLanes>
+__global__ void __launch_bounds__(kJoinThreads, kBatch == 4 ? 9 : kJoinWide)
     shared_join_kernel(const __grid_constant__ SharedArgs a) {
     const int D = a.head_dim, g = a.group, Hk = a.sc.kv_heads, per = D / 4, r = blockIdx.x;
-    const int u = blockIdx.y * kJoinThreads + threadIdx.x, hq = u / per, h = hq / g, j = hq - h * g, d0 = (u - hq * per) * 4;
+    // (a warp's units are dimensions of one head)
+    constexpr int kUnits = 32 / kLanes;
+    const int part = threadIdx.x % 32 / kUnits;
+    const int u = (blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32) * kUnits + threadIdx.x % kUnits;
+    const int hq = u / per, h = hq / g, j = hq - h * g, d0 = (u - hq * per) * 4;
     griddep_wait();
     if (hq >= a.heads) return;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws);
@@ -647,12 +656,12 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? kJoinWide : 9)
     }
     float M = -1.0e30f, L = 0.f, O[4] = {};
     #pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += kBatch) {
+    for (int c0 = part; c0 < n; c0 += kBatch * kLanes) {
         float2 x[kBatch];
         float4 p[kBatch];
         #pragma unroll
         for (int c = 0; c < kBatch; ++c) {
-            const int i = c0 + c, o = i - n_pre;
+            const int i = c0 + c * kLanes, o = i - n_pre;
             x[c] = make_float2(-1.0e30f, 0.f);
             if (i >= n) continue;
             // a cut pair's first piece is its run's second slot, the others are the first ones of the runs that follow
@@ -671,7 +680,7 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? kJoinWide : 9)
         for (int e = 0; e < 4; ++e) O[e] *= fa;
         #pragma unroll
         for (int c = 0; c < kBatch; ++c) {
-            if (c0 + c >= n) break;
+            if (c0 + c * kLanes >= n) break;
             const float f = exp2_approx(x[c].x - M);
             L += f * x[c].y;
             O[0] += f * p[c].x;
@@ -679,6 +688,18 @@ __global__ void __launch_bounds__(kJoinThreads, kBatch == 8 ? kJoinWide : 9)
             O[2] += f * p[c].z;
             O[3] += f * p[c].w;
         }
+    }
+    if constexpr (kLanes > 1) {
+        #pragma unroll
+        for (int d = kUnits; d < 32; d *= 2) {
+            const float Mo = __shfl_xor_sync(0xffffffffu, M, d), Lo = __shfl_xor_sync(0xffffffffu, L, d);
+            const float Mn = fmaxf(M, Mo), f = exp2_approx(M - Mn), fo = exp2_approx(Mo - Mn);
+            M = Mn;
+            L = L * f + Lo * fo;
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) O[e] = O[e] * f + __shfl_xor_sync(0xffffffffu, O[e], d) * fo;
+        }
+        if (part != 0) return;
     }
     const bool has_sink = a.sinks != nullptr;
     const float sk = has_sink ? load_f32<__nv_bfloat16>(a.sinks, hq) * 1.4426950408889634f : 0.f;
@@ -726,8 +747,10 @@ cudaError_t launch_shared_attend(const SharedArgs& a, const AttendArgs& own, con
 
 cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t stream) {
     const int per_row = (a.heads * (a.head_dim / 4) + kJoinThreads - 1) / kJoinThreads;
+    const long long blocks = (long long)a.sc.rows * per_row;
+    const bool few = blocks <= (long long)a.grid * kJoinFew;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.sc.rows, per_row);
+    cfg.gridDim = dim3(a.sc.rows, few ? kJoinLanes * per_row : per_row);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -735,9 +758,9 @@ cudaError_t launch_shared_join(const SharedArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return (long long)a.sc.rows * per_row <= (long long)a.grid * kJoinWide
-               ? cudaLaunchKernelEx(&cfg, shared_join_kernel<8>, a)
-               : cudaLaunchKernelEx(&cfg, shared_join_kernel<4>, a);
+    if (few) return cudaLaunchKernelEx(&cfg, shared_join_kernel<8, kJoinLanes>, a);
+    return blocks <= (long long)a.grid * kJoinWide ? cudaLaunchKernelEx(&cfg, shared_join_kernel<8, 1>, a)
+                                                   : cudaLaunchKernelEx(&cfg, shared_join_kernel<4, 1>, a);
 }
 
 }  // namespace pdattn
