@@ -93,99 +93,160 @@ __global__ void __launch_bounds__(256) rotary_tables_kernel(const __grid_constan
 }
 
 // One token per block: its pairs' cos and sin go to shared memory once for all
-// heads while the first vectors of the token load.  A unit is the two 16-byte
-// vectors of N half pairs, or one vector of interleaved pairs or of dimensions
-// past rot_dim.
+// heads while the first vectors of the token load.
 constexpr int kRotaryThreads = 128;
-template <bool kInterleaved>
-constexpr int kRotaryAhead = kInterleaved ? 4 : 3;     // units a thread loads before it needs the angles
 
-template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-    using V = Vec16<T>;
-    constexpr int N = V::N;
-    __shared__ float s_cos[kRotaryPairs], s_sin[kRotaryPairs];
-    const int tok = blockIdx.x, tid = threadIdx.x;
-    const int D = a.head_dim, rot = a.rot_dim, half = rot / 2;
-    const int turned = kInterleaved ? rot / N : half / N;              // units of a head that turn
-    const int per = turned + (D - rot) / N, units = per * (a.heads + a.kv_heads);
-    const T* qi = static_cast<const T*>(a.q) + (size_t)tok * a.q_stride;
-    const T* ki = static_cast<const T*>(a.k) + (size_t)tok * a.k_stride;
-    T* qo = static_cast<T*>(a.q_out) + (size_t)tok * a.q_out_stride;
-    T* ko = static_cast<T*>(a.k_out) + (size_t)tok * a.k_out_stride;
-    // unit u: its head's vector and first element
-    auto place = [&](int u, const T*& src, T*& dst, int& e) {
-        const int h = u / per, v = u - h * per;
-        e = v < turned ? v * N : rot + (v - turned) * N;
-        const bool is_q = h < a.heads;
-        const size_t at = (size_t)(is_q ? h : h - a.heads) * D + e;
-        src = (is_q ? qi : ki) + at;
-        dst = (is_q ? qo : ko) + at;
-    };
-    constexpr int kAhead = kRotaryAhead<kInterleaved>;
-    uint4 x[kAhead][2];
-    auto load = [&](int u, uint4 (&r)[2]) {
-        const T* src;
-        T* dst;
-        int e;
-        place(u, src, dst, e);
-        r[0] = *reinterpret_cast<const uint4*>(src);
-        if (!kInterleaved && e < rot) r[1] = *reinterpret_cast<const uint4*>(src + half);
-    };
-    #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-        if (tid + k * kRotaryThreads < units) load(tid + k * kRotaryThreads, x[k]);
-    const int pos = __ldg(a.positions + tok);
+// The angles of the block's token into shared memory; false if it has none.
+__device__ __forceinline__ bool token_angles(const RotaryArgs& a, float* s_cos, float* s_sin) {
+    const int pos = __ldg(a.positions + blockIdx.x);
     if (pos < 0) {
-        if (tid == 0) set_error(reinterpret_cast<Ctrl*>(a.ws), kErrBadPos);
-        return;
+        if (threadIdx.x == 0) set_error(reinterpret_cast<Ctrl*>(a.ws), kErrBadPos);
+        return false;
     }
-    for (int i = tid; i < half; i += kRotaryThreads) {
+    for (int i = threadIdx.x; i < a.rot_dim / 2; i += kRotaryThreads) {
         float c, s;
         cos_sin((uint64_t)pos * a.turns[i], a.gain, c, s);
         s_cos[i] = c;
         s_sin[i] = a.inverse ? -s : s;
     }
     __syncthreads();
+    return true;
+}
+
+// Half pairs.  A unit is the two vectors of N pairs, or one vector of
+// dimensions past rot_dim.  (A division by `per` and 2 N shared reads of 4 bytes
+// a unit: 8192 tokens of 40 heads of 128 26.5 us, half of each turned 31.4;
+// now 26.2 and 27.5.  A thread that keeps to one unit of every head, as below,
+// has too few heads of 8 vectors: 31.5 and 38.5.)
+constexpr int kHalfAhead = 3;            // units a thread loads before it needs the angles (2: 26.7, 28.1)
+
+template <typename T>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_half_kernel(const __grid_constant__ RotaryArgs a) {
+    using V = Vec16<T>;
+    constexpr int N = V::N;
+    __shared__ __align__(16) float s_cos[kRotaryPairs], s_sin[kRotaryPairs];
+    const int tok = blockIdx.x, tid = threadIdx.x;
+    const int D = a.head_dim, rot = a.rot_dim, half = rot / 2, turned = half / N;
+    const int per = turned + (D - rot) / N, units = per * (a.heads + a.kv_heads);
+    const uint32_t magic = 0xffffffffu / per + 1;                      // u / per for u < 2^27
+    const T* qi = static_cast<const T*>(a.q) + (size_t)tok * a.q_stride;
+    const T* ki = static_cast<const T*>(a.k) + (size_t)tok * a.k_stride;
+    T* qo = static_cast<T*>(a.q_out) + (size_t)tok * a.q_out_stride;
+    T* ko = static_cast<T*>(a.k_out) + (size_t)tok * a.k_out_stride;
+    // unit u: whether it is q's, its vector's place in a token and its first element
+    auto place = [&](int u, bool& is_q, int& at, int& e) {
+        const int h = (int)__umulhi((uint32_t)u, magic), v = u - h * per;
+        e = v < turned ? v * N : rot + (v - turned) * N;
+        is_q = h < a.heads;
+        at = (is_q ? h : h - a.heads) * D + e;
+    };
+    uint4 x[kHalfAhead][2];
+    auto load = [&](int u, uint4 (&r)[2]) {
+        bool is_q;
+        int at, e;
+        place(u, is_q, at, e);
+        const T* src = (is_q ? qi : ki) + at;
+        r[0] = *reinterpret_cast<const uint4*>(src);
+        if (e < rot) r[1] = *reinterpret_cast<const uint4*>(src + half);
+    };
+    #pragma unroll
+    for (int k = 0; k < kHalfAhead; ++k)
+        if (tid + k * kRotaryThreads < units) load(tid + k * kRotaryThreads, x[k]);
+    if (!token_angles(a, s_cos, s_sin)) return;
     auto turn = [&](int u, const uint4 (&r)[2]) {
-        const T* src;
-        T* dst;
-        int e;
-        place(u, src, dst, e);
+        bool is_q;
+        int at, e;
+        place(u, is_q, at, e);
+        T* dst = (is_q ? qo : ko) + at;
         if (e >= rot) {
             *reinterpret_cast<uint4*>(dst) = r[0];
             return;
         }
-        float f[N], y[N];
+        float f[N], g[N], y[N], z[N];
         V::to_f32(r[0], f);
-        if constexpr (kInterleaved) {
-            #pragma unroll
-            for (int k = 0; k < N; k += 2) {
-                const float c = s_cos[(e + k) / 2], s = s_sin[(e + k) / 2];
-                y[k] = f[k] * c - f[k + 1] * s;
-                y[k + 1] = f[k + 1] * c + f[k] * s;
-            }
-            *reinterpret_cast<uint4*>(dst) = V::from_f32(y);
-        } else {
-            float g[N], z[N];
-            V::to_f32(r[1], g);
-            #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const float c = s_cos[e + k], s = s_sin[e + k];
-                y[k] = f[k] * c - g[k] * s;
-                z[k] = g[k] * c + f[k] * s;
-            }
-            *reinterpret_cast<uint4*>(dst) = V::from_f32(y);
-            *reinterpret_cast<uint4*>(dst + half) = V::from_f32(z);
+        V::to_f32(r[1], g);
+        float cc[N], ss[N];
+        #pragma unroll
+        for (int k = 0; k < N; k += 4) {
+            *reinterpret_cast<float4*>(cc + k) = *reinterpret_cast<const float4*>(s_cos + e + k);
+            *reinterpret_cast<float4*>(ss + k) = *reinterpret_cast<const float4*>(s_sin + e + k);
         }
+        #pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float c = cc[k], s = ss[k];
+            y[k] = f[k] * c - g[k] * s;
+            z[k] = g[k] * c + f[k] * s;
+        }
+        *reinterpret_cast<uint4*>(dst) = V::from_f32(y);
+        *reinterpret_cast<uint4*>(dst + half) = V::from_f32(z);
     };
     #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
+    for (int k = 0; k < kHalfAhead; ++k)
         if (tid + k * kRotaryThreads < units) turn(tid + k * kRotaryThreads, x[k]);
-    for (int u = tid + kAhead * kRotaryThreads; u < units; u += kRotaryThreads) {
+    for (int u = tid + kHalfAhead * kRotaryThreads; u < units; u += kRotaryThreads) {
         uint4 r[2];
         load(u, r);
         turn(u, r);
+    }
+}
+
+// Interleaved pairs.  A thread takes the same vector of every H-th head (D / N
+// divides the threads), so that it keeps its cos and sin in registers: with
+// vectors in order and 2 N shared reads for each the schedulers were 80 % busy
+// (8192 tokens of 40 heads of 128, half of each turned, 31.2 us; so 26.5).
+constexpr int kPairAhead = 5;            // heads a thread has in flight (4: 28.4 us, 6: 27.9)
+
+template <typename T>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_pair_kernel(const __grid_constant__ RotaryArgs a) {
+    using V = Vec16<T>;
+    constexpr int N = V::N;
+    __shared__ __align__(16) float s_cos[kRotaryPairs], s_sin[kRotaryPairs];
+    const int tok = blockIdx.x, tid = threadIdx.x, D = a.head_dim;
+    const int per = D / N, H = kRotaryThreads / per, h0 = tid / per, e = (tid - h0 * per) * N;
+    const int heads = a.heads + a.kv_heads;
+    const T* qi = static_cast<const T*>(a.q) + (size_t)tok * a.q_stride + e;
+    const T* ki = static_cast<const T*>(a.k) + (size_t)tok * a.k_stride + e;
+    T* qo = static_cast<T*>(a.q_out) + (size_t)tok * a.q_out_stride + e;
+    T* ko = static_cast<T*>(a.k_out) + (size_t)tok * a.k_out_stride + e;
+    uint4 x[kPairAhead];
+    auto load = [&](int hb) {
+        #pragma unroll
+        for (int k = 0; k < kPairAhead; ++k) {
+            const int h = hb + k * H;
+            if (h < heads) x[k] = *reinterpret_cast<const uint4*>(h < a.heads ? qi + h * D : ki + (h - a.heads) * D);
+        }
+    };
+    load(h0);
+    if (!token_angles(a, s_cos, s_sin)) return;
+    const bool turns = e < a.rot_dim;
+    float c[N / 2] = {}, s[N / 2] = {};
+    if (turns) {
+        #pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            c[k] = s_cos[e / 2 + k];
+            s[k] = s_sin[e / 2 + k];
+        }
+    }
+    for (int hb = h0; hb < heads;) {
+        #pragma unroll
+        for (int k = 0; k < kPairAhead; ++k) {
+            const int h = hb + k * H;
+            if (h >= heads) continue;
+            uint4 out = x[k];
+            if (turns) {
+                float f[N], y[N];
+                V::to_f32(x[k], f);
+                #pragma unroll
+                for (int t = 0; t < N; t += 2) {
+                    y[t] = f[t] * c[t / 2] - f[t + 1] * s[t / 2];
+                    y[t + 1] = f[t + 1] * c[t / 2] + f[t] * s[t / 2];
+                }
+                out = V::from_f32(y);
+            }
+            *reinterpret_cast<uint4*>(h < a.heads ? qo + h * D : ko + (h - a.heads) * D) = out;
+        }
+        hb += kPairAhead * H;
+        load(hb);
     }
 }
 
@@ -211,11 +272,11 @@ cudaError_t launch_rotary_tables(const RotaryArgs& a, int length, int dtype, voi
 
 cudaError_t launch_rotary(const RotaryArgs& a, int n_tokens, int dtype, cudaStream_t stream) {
     if (dtype == 0) {
-        if (a.interleaved) rotary_kernel<__nv_bfloat16, true><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
-        else rotary_kernel<__nv_bfloat16, false><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
+        if (a.interleaved) rotary_pair_kernel<__nv_bfloat16><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
+        else rotary_half_kernel<__nv_bfloat16><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
     } else {
-        if (a.interleaved) rotary_kernel<float, true><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
-        else rotary_kernel<float, false><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
+        if (a.interleaved) rotary_pair_kernel<float><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
+        else rotary_half_kernel<float><<<n_tokens, kRotaryThreads, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
