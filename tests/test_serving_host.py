@@ -2,6 +2,10 @@
 bookkeeping): CPU only, before any launch."""
 import ctypes
 import math
+import os
+import re
+import subprocess
+import tempfile
 
 import pytest
 import torch
@@ -234,3 +238,14 @@ def test_shared_decode_is_checked(b):
     assert call(p(rows=0), at=NULL, groups=NULL, ws=NULL) == b.OK
     if torch.cuda.is_available():
         assert call(p(), nb=b.lib.pdattn_shared_workspace_size(p(), 1) - 1) == b.EINVAL
+
+
+@pytest.mark.parametrize("source", ["rotary.cu", "pages.cu", "shared.cu"])
+def test_kernels_compile_without_spills(source):
+    from paged_gqa_decode_step_gb300 import build
+    with tempfile.TemporaryDirectory() as d:
+        r = subprocess.run([build.nvcc(), "-c", os.path.join(build.CSRC, source), "-o", os.path.join(d, "k.o"), "-Xptxas",
+                            "-v"] + build._flags(), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-4000:]
+    spills = re.findall(r"(\d+) bytes spill stores, (\d+) bytes spill loads", r.stdout + r.stderr)
+    assert spills and all(x == ("0", "0") for x in spills), f"{source}: register spills {spills}"
