@@ -134,19 +134,24 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
     const int R = a.rows, W = a.pages_per_row, N = a.num_pages;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(a.ws);
     PagesInfo* info = reinterpret_cast<PagesInfo*>(a.ws + a.L.info);
-    int* kept = reinterpret_cast<int*>(a.ws + a.L.table);   // [row][page]: the parent's entry
     int2* row_at = reinterpret_cast<int2*>(a.ws + a.L.rows);
     int4* jobs = reinterpret_cast<int4*>(a.ws + a.L.jobs);
-    // rows that held the page (then its rank among its CTA's free ones), holders
-    // that do not write into it, the lowest row that does, and each CTA's free
-    // pages at its range's start
+    // rows that held the page less its count (then its rank among its CTA's free
+    // ones), rows that do not write into it (then with holders outside), the
+    // lowest row that does, each CTA's free pages at its range's start, and
+    // [row][page] the parent's entry
     int* held = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.a) : s_counters;
     int* others = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.b) : s_counters + N;
     int* first = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.c) : s_counters + 2 * N;
     int* list = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.d) : s_counters + 3 * N;
+    int* kept = kCtas > 1 ? reinterpret_cast<int*>(a.ws + a.L.table) : s_counters + kCountersPerPage * N;
 
+    bool negative = false;
+    #pragma unroll 4
     for (int x = at; x < N; x += T::kAll) {
-        held[x] = 0;
+        const int refs = __ldcg(a.refs + x);
+        negative = negative || refs < 0;
+        held[x] = -refs;
         others[x] = 0;
         first[x] = INT_MAX;
     }
@@ -159,6 +164,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
         s_bad = 1;
     };
     T::sync();
+    if (negative) bad(kErrBadPage);
 
     // Lanes of a row: the power of two that its entries fill, at most a warp.
     const int lanes = W > 16 ? 32 : W > 8 ? 16 : 8, teams = T::kAll / lanes, l = at % lanes;
@@ -218,16 +224,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
     int n_free = 0;
     for (int b = x0; b < x1;) {
         const int P = min(kPagesAhead, (x1 - b + kPageThreads - 1) / kPageThreads), x = b + tid * P;
-        int refs[kPagesAhead];
-        #pragma unroll
-        for (int k = 0; k < kPagesAhead; ++k) refs[k] = k < P && x + k < x1 ? __ldcg(a.refs + x + k) : 1;
         uint32_t free = 0;
         #pragma unroll
         for (int k = 0; k < kPagesAhead; ++k) {
             if (k >= P || x + k >= x1) continue;
-            const int h = T::load(held + x + k);
-            if (refs[k] < h || refs[k] < 0) bad(kErrBadPage);
-            const int o = T::load(others + x + k) + refs[k] - h;
+            const int h = T::load(held + x + k), o = T::load(others + x + k) - h;
+            if (h > 0) bad(kErrBadPage);
             others[x + k] = o;
             if (o == 0 && T::load(first + x + k) == INT_MAX) free |= 1u << k;
         }
@@ -271,7 +273,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
             const Row k = row(r);
             keeps = k.full() + (k.part() ? 1 : 0);
             if (k.part() && k.writes()) {
-                const int x = __ldcg(kept + (size_t)r * W + k.full());
+                const int x = T::load(kept + (size_t)r * W + k.full());
                 if (T::load(others + x) != 0 || T::load(first + x) != r) keeps = k.full();
             }
             mine = pages_of(k.want) - keeps;
@@ -321,7 +323,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
                 for (int k = 0; k < kTwo; ++k) {
                     const int c = c0 + k * lanes;
                     x[q][k] = -1;
-                    if (c < ra[q].x || c == tail[q]) y[q][k] = __ldcg(kept + (size_t)(r0 + q * teams) * W + c);
+                    if (c < ra[q].x || c == tail[q]) y[q][k] = T::load(kept + (size_t)(r0 + q * teams) * W + c);
                     if (c >= ra[q].x && c < n[q]) {
                         const int rank = ra[q].y + c - ra[q].x;
                         int at0 = 0, skip = 0;
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 // 18.5; 256 x 40 and 4000 18.9, 14.1; 90 x 130 and 12200 24.1, 18.9; 1000 x 32 and
 // 12200 53.5, 19.5.  compact: 9 x 7 and 60 8.2, 11.8; 256 x 40 16.9, 13.1.
 constexpr int kOneCtaPages = 4608;
-constexpr long long kOneCtaEntries = 8192;
+constexpr int kOneCtaEntries = 8192;
 
 template <typename K>
 static cudaError_t launch_team(K one, K many, const PagesArgs& a, int* configured_mask, cudaStream_t stream) {
@@ -541,11 +543,11 @@ static cudaError_t launch_team(K one, K many, const PagesArgs& a, int* configure
     if (e != cudaSuccess) return e;
     if (dev >= 31 || !(__atomic_load_n(configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
         e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kOneCtaPages * kCountersPerPage * (int)sizeof(int));
+                                 (kOneCtaPages * kCountersPerPage + kOneCtaEntries) * (int)sizeof(int));
         if (e != cudaSuccess) return e;
         if (dev < 31) __atomic_fetch_or(configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
-    one<<<1, kPageThreads, (size_t)a.num_pages * kCountersPerPage * sizeof(int), stream>>>(a);
+    one<<<1, kPageThreads, ((size_t)a.num_pages * kCountersPerPage + (size_t)a.rows * a.pages_per_row) * sizeof(int), stream>>>(a);
     return cudaGetLastError();
 }
 
