@@ -73,6 +73,12 @@ struct Team {
     __device__ static int from(int n, int c) { return kCtas > 1 ? (int)((long long)n * c / kCtas) : c * n; }
 };
 
+// Lanes that take a row of an update: the power of two that its entries fill, at
+// most a warp.
+__host__ __device__ __forceinline__ int row_lanes(int pages_per_row) {
+    return pages_per_row > 16 ? 32 : pages_per_row > 8 ? 16 : 8;
+}
+
 __device__ __forceinline__ int pages_of(int positions) { return (positions + kPageSize - 1) / kPageSize; }
 
 // Exclusive sum over the block (1024 threads); *total gets the sum.
@@ -166,8 +172,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
     T::sync();
     if (negative) bad(kErrBadPage);
 
-    // Lanes of a row: the power of two that its entries fill, at most a warp.
-    const int lanes = W > 16 ? 32 : W > 8 ? 16 : 8, teams = T::kAll / lanes, l = at % lanes;
+    const int lanes = row_lanes(W), teams = T::kAll / lanes, l = at % lanes;
 
     // Holders, old and new.  What a row keeps is copied, because its parent's
     // entries may be overwritten before they are taken over.
@@ -525,16 +530,21 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 
 }  // namespace
 
-// One CTA for small tables, else the cluster.  update, one CTA against the
-// cluster, us: 64 x 65 entries and 4360 pages 11.5, 16.1; 16 x 512 and 4000 14.0,
-// 18.5; 256 x 40 and 4000 18.9, 14.1; 90 x 130 and 12200 24.1, 18.9; 1000 x 32 and
-// 12200 53.5, 19.5.  compact: 9 x 7 and 60 8.2, 11.8; 256 x 40 16.9, 13.1.
+// One CTA for small tables, else the cluster.  An update's rows are taken by
+// teams of lanes (row_lanes), a compaction's entries one per thread.  One CTA
+// against the cluster, rows x pages_per_row and num_pages, us: update 64 x 65 and
+// 4360 10.8, 15.0; 16 x 512 and 4000 13.4, 18.1; 128 x 64 and 4000 13.0, 14.3;
+// 256 x 13 and 2100 12.5, 13.6; 256 x 32 and 4000 17.6, 13.7.  compact 9 x 7 and
+// 60 7.1, 11.1; 256 x 13 and 2100 10.8, 11.9; 64 x 65 and 4360 13.1, 12.7;
+// 128 x 64 and 4000 15.4, 13.0.
 constexpr int kOneCtaPages = 4608;
-constexpr int kOneCtaEntries = 8192;
+constexpr int kOneCtaEntries = 8192;         // of an update: in shared memory
+constexpr int kOneCtaWork = 4096;
 
 template <typename K>
-static cudaError_t launch_team(K one, K many, const PagesArgs& a, int* configured_mask, cudaStream_t stream) {
-    if (a.num_pages > kOneCtaPages || (long long)a.rows * a.pages_per_row > kOneCtaEntries) {
+static cudaError_t launch_team(K one, K many, const PagesArgs& a, bool small, size_t smem, size_t most, int* configured_mask,
+                               cudaStream_t stream) {
+    if (!small) {
         many<<<kPageCtas, kPageThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
@@ -542,19 +552,26 @@ static cudaError_t launch_team(K one, K many, const PagesArgs& a, int* configure
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 31 || !(__atomic_load_n(configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
-        e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kOneCtaPages * kCountersPerPage + kOneCtaEntries) * (int)sizeof(int));
+        e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
         if (dev < 31) __atomic_fetch_or(configured_mask, 1 << dev, __ATOMIC_ACQ_REL);
     }
-    one<<<1, kPageThreads, ((size_t)a.num_pages * kCountersPerPage + (size_t)a.rows * a.pages_per_row) * sizeof(int), stream>>>(a);
+    one<<<1, kPageThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_pages(const PagesArgs& a, bool compact, cudaStream_t stream) {
     static int update_mask = 0, compact_mask = 0;   // bit per device id < 31
-    if (compact) return launch_team(pages_compact_kernel<1>, pages_compact_kernel<kPageCtas>, a, &compact_mask, stream);
-    return launch_team(pages_update_kernel<1>, pages_update_kernel<kPageCtas>, a, &update_mask, stream);
+    const long long entries = (long long)a.rows * a.pages_per_row;
+    const size_t counters = (size_t)a.num_pages * kCountersPerPage * sizeof(int);
+    const size_t most = (size_t)kOneCtaPages * kCountersPerPage * sizeof(int);
+    if (compact)
+        return launch_team(pages_compact_kernel<1>, pages_compact_kernel<kPageCtas>, a,
+                           a.num_pages <= kOneCtaPages && entries <= kOneCtaWork, counters, most, &compact_mask, stream);
+    const bool small = a.num_pages <= kOneCtaPages && entries <= kOneCtaEntries &&
+                       (long long)a.rows * row_lanes(a.pages_per_row) <= kOneCtaWork;
+    return launch_team(pages_update_kernel<1>, pages_update_kernel<kPageCtas>, a, small, counters + entries * sizeof(int),
+                       most + kOneCtaEntries * sizeof(int), &update_mask, stream);
 }
 
 cudaError_t launch_pages_copy(const PagesArgs& a, const PoolList& pools, int grid, bool after_plan, cudaStream_t stream) {
