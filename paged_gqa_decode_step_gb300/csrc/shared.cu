@@ -563,8 +563,10 @@ __device__ __forceinline__ void prefix_cta(const CUtensorMap& q_map, const CUten
 // tensor cores and their softmax, the rows' own ones by HBM, so that side by
 // side each takes what the other leaves.  The number of CTAs of each kind goes
 // by what a block of 128 keys for one half of a tile and an own page take on an
-// SM (10 ns).
-constexpr int kUnitCost[2] = {90, 135};     // head dim 64, 128
+// SM (10 ns).  (A unit at 105 and 135: 256 rows in six groups 159.6 and 155.6 us,
+// 153.8 between; 40 rows under 200 pages 36.5 and 41.0.  Head dim 64, 80 and 90:
+// 64 rows under 32 pages 49.0 and 41.1; 128 under 100 79.2 and 76.2, at 100 73.8.)
+constexpr int kUnitCost[2] = {100, 118};    // head dim 64, 128
 constexpr int kPageCost[2] = {40, 36};
 constexpr int kItemPages = 3;               // what a pair's start and end cost, in pages
 
