@@ -515,15 +515,15 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
         const char* src = base + ((size_t)job.x * heads + slab) * kPageSize * row;
         char* dst = base + ((size_t)job.y * heads + slab) * kPageSize * row;
         const int bytes = job.z * row, vecs = bytes / 16;
-        int v = threadIdx.x;
-        for (; v + (kCopyAhead - 1) * kCopyThreads < vecs; v += kCopyAhead * kCopyThreads) {
+        for (int v0 = threadIdx.x; v0 < vecs; v0 += kCopyAhead * kCopyThreads) {
             uint4 x[kCopyAhead];
             #pragma unroll
-            for (int k = 0; k < kCopyAhead; ++k) x[k] = __ldcs(reinterpret_cast<const uint4*>(src) + v + k * kCopyThreads);
+            for (int k = 0; k < kCopyAhead; ++k)
+                if (v0 + k * kCopyThreads < vecs) x[k] = __ldcs(reinterpret_cast<const uint4*>(src) + v0 + k * kCopyThreads);
             #pragma unroll
-            for (int k = 0; k < kCopyAhead; ++k) reinterpret_cast<uint4*>(dst)[v + k * kCopyThreads] = x[k];
+            for (int k = 0; k < kCopyAhead; ++k)
+                if (v0 + k * kCopyThreads < vecs) reinterpret_cast<uint4*>(dst)[v0 + k * kCopyThreads] = x[k];
         }
-        for (; v < vecs; v += kCopyThreads) reinterpret_cast<uint4*>(dst)[v] = reinterpret_cast<const uint4*>(src)[v];
         for (int t = vecs * 16 + threadIdx.x; t < bytes; t += kCopyThreads) dst[t] = src[t];
     }
 }
