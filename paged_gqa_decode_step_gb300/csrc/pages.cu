@@ -1,7 +1,7 @@
 // Bookkeeping of a paged cache on the device: rows that continue, fork, start
 // anew, grow or give room back (update), and the pages in use moved to the
 // lowest ids (compact).  The table's part runs as one CTA that counts in shared
-// memory or, for more pages, as one cluster that counts in global memory, so
+// memory or, for larger tables, as one cluster that counts in global memory, so
 // that its phases are separated by barriers and not by launches; what it costs
 // is latency, a global round trip (0.6 us) or a cluster barrier (0.7 us) after
 // another.  The page data is copied by a second launch that works through a job
