@@ -593,7 +593,8 @@ size_t pdattn_pages_workspace_size(const pdattn_params* p);
  * New pages are the lowest free ids, in order of row and position; pages that
  * this call frees count as free.  table_out gets the pages, -1 after them;
  * refs_out the counts, holders outside the table included.  table_out may be
- * table and refs_out may be refs.  new_lengths is the next call's `lengths`.
+ * table and refs_out may be refs; otherwise neither overlaps another array
+ * (PDATTN_EINVAL).  new_lengths is the next call's `lengths`.
  * Errors, which change nothing: a parent outside [-1, rows) or a length
  * outside [0, 64 * pages_per_row] is PDATTN_EBADPOS; a held entry outside the
  * pool, or fewer refs than rows that hold the page, PDATTN_EBADPAGE; too few
@@ -611,9 +612,10 @@ pdattn_status pdattn_pages_update(const pdattn_params* p, int32_t n_pools, const
  * free id below n, the others stay.  page_map [num_pages] gets each page's new
  * id, -1 for a free one (for holders outside the table).  Held table entries
  * are renamed, entries after them copied.  table_out may be table and
- * refs_out may be refs; page_map is none of the four.  Errors, which change
- * nothing: a held entry that is outside the pool or free, or a negative
- * count, is PDATTN_EBADPAGE; a bad length PDATTN_EBADPOS.
+ * refs_out may be refs; otherwise neither, nor page_map, overlaps another array
+ * (PDATTN_EINVAL).  Errors, which change nothing: a held entry that is outside
+ * the pool or free, or a negative count, is PDATTN_EBADPAGE; a bad length
+ * PDATTN_EBADPOS.
  */
 pdattn_status pdattn_pages_compact(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools,
                                    const int32_t* table, const int32_t* lengths, const int32_t* refs,

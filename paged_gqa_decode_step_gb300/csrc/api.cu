@@ -1361,6 +1361,34 @@ size_t pdattn_pages_workspace_size(const pdattn_params* p) {
     return pages_layout(p->rows, p->pages_per_row, p->num_pages).total;
 }
 
+// What the call writes is no other array of it: the kernels write table, counts
+// and map before they have read lengths for the last time.  The table and the
+// counts may be updated in place.
+static pdattn_status check_pages_overlap(const pdattn_params* p, const PagesArgs& a, bool compact) {
+    const size_t tab = sizeof(int32_t) * (size_t)p->rows * p->pages_per_row, row = sizeof(int32_t) * (size_t)p->rows;
+    const size_t num = sizeof(int32_t) * (size_t)p->num_pages;
+    const struct {
+        const char* name;
+        const int* at;
+        size_t bytes;
+        int in_place;                       // outputs: the input that they may be
+    } arrays[] = {{"table", a.table, tab, -1},     {"lengths", a.lengths, row, -1},
+                  {"refs", a.refs, num, -1},       {"parents", a.parents, compact ? 0 : row, -1},
+                  {"new_lengths", a.new_lengths, compact ? 0 : row, -1},
+                  {"table_out", a.table_out, tab, 0}, {"refs_out", a.refs_out, num, 2},
+                  {"page_map", a.map, compact ? num : 0, -1}};
+    constexpr int kInputs = 5, kArrays = 8;
+    for (int o = kInputs; o < kArrays; ++o)
+        for (int i = 0; i < o; ++i) {
+            const auto &x = arrays[o], &y = arrays[i];
+            const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.at), y0 = reinterpret_cast<uintptr_t>(y.at);
+            if (x.bytes == 0 || y.bytes == 0 || x0 + x.bytes <= y0 || y0 + y.bytes <= x0) continue;
+            if (i == x.in_place && x0 == y0) continue;
+            return fail(PDATTN_EINVAL, "%s must not overlap %s", x.name, y.name);
+        }
+    return PDATTN_OK;
+}
+
 static pdattn_status pages_impl(const pdattn_params* p, int32_t n_pools, const pdattn_pool* pools, PagesArgs a,
                                 bool compact, void* workspace, size_t workspace_bytes, pdattn_stream stream) {
     g_launches = 0;
@@ -1383,8 +1411,7 @@ static pdattn_status pages_impl(const pdattn_params* p, int32_t n_pools, const p
     a.L = pages_layout(p->rows, p->pages_per_row, p->num_pages);
     if (workspace_bytes < a.L.total)
         return fail(PDATTN_EINVAL, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, a.L.total);
-    if (compact && (a.map == a.refs || a.map == a.refs_out || a.map == a.table || a.map == a.table_out))
-        return fail(PDATTN_EINVAL, "page_map must not be another argument");
+    if ((s = check_pages_overlap(p, a, compact)) != PDATTN_OK) return s;
     const int sms = sm_count();
     if (sms <= 0) return fail(PDATTN_ECUDA, "no CUDA device");
     a.rows = p->rows;
