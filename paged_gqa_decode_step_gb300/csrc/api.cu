@@ -1200,7 +1200,7 @@ pdattn_status pdattn_coded_prefill(const pdattn_params* p, const pdattn_coded_ca
 // ---------------------------------------------------------------------------
 namespace {
 constexpr uint32_t kRotaryMade = 0x70647274u;
-constexpr double kTwoPi = 6.283185307179586476925;
+constexpr long double kTwoPi = 6.28318530717958647692528676655900577L;
 }  // namespace
 
 pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* out) {
@@ -1223,17 +1223,22 @@ pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* 
         if (c.original_len <= 0) return fail(PDATTN_EINVAL, "original_len must be > 0");
         if (c.whole_pairs != 0 && c.whole_pairs != 1) return fail(PDATTN_EINVAL, "whole_pairs must be 0 or 1");
     }
-    const double pairs = c.rot_dim / 2, log_theta = std::log(c.theta);
+    // Positions of up to 2^31 multiply what a frequency is off by, which in
+    // double (2^-55 turns) would be 2^-24 turns there; long double has 64 bits
+    // of precision or more.
+    using real = long double;
+    const real pairs = c.rot_dim / 2, log_theta = std::log((real)c.theta);
     // the ramp's ends, in pairs
-    double a = 0.0, b = 0.0;
+    real a = 0, b = 0;
     if (c.scaling == PDATTN_ROTARY_RAMP) {
         a = pairs * std::log(c.original_len / (kTwoPi * c.high)) / log_theta;
         b = pairs * std::log(c.original_len / (kTwoPi * c.low)) / log_theta;
         if (c.whole_pairs) {
-            a = std::fmin(std::fmax(std::floor(a), 0.0), c.rot_dim - 1);
-            b = std::fmin(std::fmax(std::ceil(b), 0.0), c.rot_dim - 1);
+            const real last = c.rot_dim - 1;
+            a = std::fmin(std::fmax(std::floor(a), (real)0), last);
+            b = std::fmin(std::fmax(std::ceil(b), (real)0), last);
         }
-        b = std::fmax(b, a + 1e-3);
+        b = std::fmax(b, a + (real)1e-3L);
     }
     pdattn_rotary r = {};
     r.head_dim = c.head_dim;
@@ -1242,14 +1247,15 @@ pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* 
     r.gain = (float)(c.gain > 0.0 ? c.gain : c.scaling == PDATTN_ROTARY_RAMP ? 0.1 * std::log(c.factor) + 1.0 : 1.0);
     r.made = kRotaryMade;
     for (int i = 0; i < c.rot_dim / 2; ++i) {
-        const double f = std::exp(-(double)i / pairs * log_theta);
-        double s = 1.0;                                 // share of f, the rest of f / factor
-        if (c.scaling == PDATTN_ROTARY_LINEAR) s = 0.0;
-        if (c.scaling == PDATTN_ROTARY_WAVELENGTH) s = (c.original_len * f / kTwoPi - c.low) / (c.high - c.low);
-        if (c.scaling == PDATTN_ROTARY_RAMP) s = 1.0 - (i - a) / (b - a);
-        s = std::fmin(std::fmax(s, 0.0), 1.0);
+        const real f = std::exp(-(real)i * log_theta / pairs);
+        real s = 1;                                     // share of f, the rest of f / factor
+        if (c.scaling == PDATTN_ROTARY_LINEAR) s = 0;
+        if (c.scaling == PDATTN_ROTARY_WAVELENGTH)
+            s = (c.original_len * f / kTwoPi - c.low) / ((real)c.high - c.low);
+        if (c.scaling == PDATTN_ROTARY_RAMP) s = 1 - (i - a) / (b - a);
+        s = std::fmin(std::fmax(s, (real)0), (real)1);
         // at most 1 / (2 pi) turn: below 2^62
-        r.turns[i] = (uint64_t)std::llrint(std::ldexp((f * s + f / c.factor * (1.0 - s)) / kTwoPi, 64));
+        r.turns[i] = (uint64_t)std::llrint(std::ldexp((f * s + f / c.factor * (1 - s)) / kTwoPi, 64));
     }
     *out = r;
     return PDATTN_OK;

@@ -7,9 +7,10 @@
 // transpose, so the inverse call on an output's gradient is the input's.
 //
 // Angles.  The host holds w_i / (2 pi) in turns as a fraction of 2^64
-// (pdattn_rotary.turns).  pos * turns mod 2^64 is the angle's exact place in
-// its turn: one integer product, whose overflow drops the whole turns, where a
-// product in f32 is off by 2^-24 of the angle (0.004 rad at position 131072).
+// (pdattn_rotary.turns), to half a unit or a little more, which is 2^-33 turns at
+// position 2^31.  pos * turns mod 2^64 is then the angle's place in its turn:
+// one integer product, whose overflow drops the whole turns, where a product
+// in f32 is off by 2^-24 of the angle (0.004 rad at position 131072).
 // The top 32 bits are cut into a quarter turn and a signed rest of at most an
 // eighth of a turn, so that the rest is an f32 to 2^-25 of an eighth of a turn.
 #include "internal.h"
