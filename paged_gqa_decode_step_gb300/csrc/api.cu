@@ -1292,7 +1292,9 @@ pdattn_status pdattn_rotary_tables(const pdattn_rotary* rotary, int32_t length, 
     if (length == 0) return PDATTN_OK;
     if (!cos_out || !sin_out) return fail(PDATTN_EINVAL, "NULL table pointer");
     if (!aligned16(cos_out) || !aligned16(sin_out)) return fail(PDATTN_EINVAL, "rope tables must be 16-byte aligned");
-    cudaError_t e = launch_rotary_tables(rotary_args(rotary), length, dtype, cos_out, sin_out, (cudaStream_t)stream);
+    const int sms = sm_count();
+    if (sms <= 0) return fail(PDATTN_ECUDA, "no CUDA device");
+    cudaError_t e = launch_rotary_tables(rotary_args(rotary), length, dtype, cos_out, sin_out, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "rotary table launch");
     g_launches = 1;
     return PDATTN_OK;

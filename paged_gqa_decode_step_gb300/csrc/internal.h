@@ -324,8 +324,8 @@ cudaError_t launch_prefill_plan(const PrefillPrepArgs& a, cudaStream_t stream);
 // Attention of the units, then, where tiles may be split, their merge.
 cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& q_map, int code, int grid, bool merge,
                                  cudaStream_t stream);
-// Rotary tables of `length` positions; rotation of n_tokens tokens.
-cudaError_t launch_rotary_tables(const RotaryArgs& a, int length, int dtype, void* cos_out, void* sin_out,
+// Rotary tables of `length` positions (on a device of `sms` SMs); rotation of n_tokens tokens.
+cudaError_t launch_rotary_tables(const RotaryArgs& a, int length, int dtype, void* cos_out, void* sin_out, int sms,
                                  cudaStream_t stream);
 cudaError_t launch_rotary(const RotaryArgs& a, int n_tokens, int dtype, cudaStream_t stream);
 // The table's part of an update or a compaction (one cluster), then the page

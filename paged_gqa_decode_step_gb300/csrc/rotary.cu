@@ -253,11 +253,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_pair_kernel(const __gri
 
 }  // namespace
 
-cudaError_t launch_rotary_tables(const RotaryArgs& a, int length, int dtype, void* cos_out, void* sin_out,
+cudaError_t launch_rotary_tables(const RotaryArgs& a, int length, int dtype, void* cos_out, void* sin_out, int sms,
                                  cudaStream_t stream) {
     // sums: when the runs make a block for every SM
     const int runs = kRun * 256 / (a.head_dim / 16), each = 256 / (a.head_dim / (dtype == 0 ? 16 : 8));
-    const bool sums = dtype == 0 && length >= 148 * runs;
+    const bool sums = dtype == 0 && length >= (long long)sms * runs;
     const long long blocks = ((long long)length + (sums ? runs : each) - 1) / (sums ? runs : each);
     const int grid = (int)(blocks < 8192 ? blocks : 8192);
     __nv_bfloat16 *cb = static_cast<__nv_bfloat16*>(cos_out), *sb = static_cast<__nv_bfloat16*>(sin_out);
