@@ -462,15 +462,24 @@ def _check_coded(p, cache, ws, n, heads, ints, table, **named):
         _same_device(cache._tensors[0], ws)
 
 
+# Torch's own short ways to the current device and to a stream's handle (the
+# public ones take three times as long, and 3 us for a Stream object); where a
+# version of torch lacks them, the public ones.
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _here():
-    """The current device, -1 without a GPU (torch.cuda.current_device takes three times as long)."""
-    if torch.cuda._initialized:
-        return torch._C._cuda_getDevice()
+    """The current device, -1 without a GPU."""
+    if _get_device is not None and torch.cuda.is_initialized():
+        return _get_device()
     return torch.cuda.current_device() if torch.cuda.is_available() else -1
 
 
 def _stream_of(stream, here):
-    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _get_raw_stream(here) if _get_raw_stream is not None else torch.cuda.current_stream(here).cuda_stream
 
 
 def _tokens(t):
@@ -478,11 +487,7 @@ def _tokens(t):
 
 
 def _raw_stream(stream):
-    # the current stream's handle without the Stream object, whose making takes
-    # longer (3 us) than the rest of a call's checks
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+    return stream.cuda_stream if stream is not None else _stream_of(None, torch.cuda.current_device())
 
 
 def coded_write(p, cache, k_new, v_new, positions, slots, ws, stream=None):
