@@ -328,7 +328,7 @@ cudaError_t launch_prefill_coded(const CodedPrefillArgs& ca, const CUtensorMap& 
 cudaError_t launch_rotary_tables(const RotaryArgs& a, int length, int dtype, void* cos_out, void* sin_out, int sms,
                                  cudaStream_t stream);
 cudaError_t launch_rotary(const RotaryArgs& a, int n_tokens, int dtype, cudaStream_t stream);
-// The table's part of an update or a compaction (one cluster), then the page
+// The table's part of an update or a compaction (one CTA or one cluster), then the page
 // copies it listed (after_plan: a programmatic dependent of it).
 cudaError_t launch_pages(const PagesArgs& a, bool compact, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PagesArgs& a, const PoolList& pools, int grid, bool after_plan, cudaStream_t stream);

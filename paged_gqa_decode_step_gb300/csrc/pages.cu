@@ -1,11 +1,12 @@
 // Bookkeeping of a paged cache on the device: rows that continue, fork, start
 // anew, grow or give room back (update), and the pages in use moved to the
 // lowest ids (compact).  The table's part runs as one CTA that counts in shared
-// memory or, for larger tables, as one cluster that counts in global memory, so
-// that its phases are separated by barriers and not by launches; what it costs
-// is latency, a global round trip (0.6 us) or a cluster barrier (0.7 us) after
-// another.  The page data is copied by a second launch that works through a job
-// list.
+// memory or, for larger tables and pools, as one cluster that counts in global
+// memory, so that its phases are separated by barriers and not by launches.
+// What it costs is half latency, a global round trip (0.6 us) or a cluster
+// barrier (0.7 us) after another, and half issue (256 beams of 13 entries: slots
+// 50 % busy; part of that is lanes without an entry).  The page data is copied
+// by a second launch that works through a job list.
 //
 // update.  refs[x] counts the holders of page x: the rows whose first
 // ceil(length / 64) entries name it, and holders outside the table (pins).
@@ -530,16 +531,27 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 
 }  // namespace
 
-// One CTA for small tables, else the cluster.  An update's rows are taken by
-// teams of lanes (row_lanes), a compaction's entries one per thread.  One CTA
-// against the cluster, rows x pages_per_row and num_pages, us: update 64 x 65 and
-// 4360 10.8, 15.0; 16 x 512 and 4000 13.4, 18.1; 128 x 64 and 4000 13.0, 14.3;
-// 256 x 13 and 2100 12.5, 13.6; 256 x 32 and 4000 17.6, 13.7.  compact 9 x 7 and
-// 60 7.1, 11.1; 256 x 13 and 2100 10.8, 11.9; 64 x 65 and 4360 13.1, 12.7;
-// 128 x 64 and 4000 15.4, 13.0.
-constexpr int kOneCtaPages = 4608;
+// One CTA for small tables and pools, else the cluster.  An update's rows are
+// taken by teams of lanes (row_lanes), a compaction's entries one per thread; up
+// to kOneCtaPages its threads count and rank all pages in one pass.  One CTA
+// against the cluster, us of a graph replay, by num_pages:
+//   rows x pages_per_row     4360         6000         8000        10000
+//   update   16 x 64      8.9, 13.4    9.8, 13.4   13.7, 13.6   15.5, 14.8
+//            64 x 65     11.1, 15.9   11.7, 15.9   15.4, 15.5   17.4, 17.0
+//            64 x 128    11.2, 15.8   12.2, 16.5   15.8, 17.3   17.6, 18.4
+//           128 x 64     12.4, 13.9   13.2, 14.5   16.9, 15.6   18.6, 16.1
+//            24 x 340    12.6, 19.1   13.8, 19.9   18.3, 22.7   20.6, 24.7
+//   compact  16 x 64      9.6, 12.3   10.6, 12.6   12.5, 12.9   14.6, 13.7
+//            64 x 65     13.3, 12.8   14.2, 13.2   16.7, 13.3   18.8, 14.8
+//           128 x 64     15.2, 12.0   16.1, 12.9   18.8, 13.4   21.8, 14.7
+// An update of 256 x 32 in 4000 pages 17.6, 13.7; compact 256 x 13 in 2100 10.8,
+// 11.9, 64 x 65 in 1000 10.5, 10.8: an entry of it counts as two pages.  The
+// cluster in 32768 and 131072 pages: update of 64 x 65 21.6, 53.8, compact 18.0,
+// 35.8.
+constexpr int kOneCtaPages = kPagesAhead * kPageThreads;
 constexpr int kOneCtaEntries = 8192;         // of an update: in shared memory
-constexpr int kOneCtaWork = 4096;
+constexpr int kOneCtaLanes = 4096;           // of an update
+constexpr int kOneCtaCompact = 10240;        // pages and twice the entries
 
 template <typename K>
 static cudaError_t launch_team(K one, K many, const PagesArgs& a, bool small, size_t smem, size_t most, int* configured_mask,
@@ -567,9 +579,10 @@ cudaError_t launch_pages(const PagesArgs& a, bool compact, cudaStream_t stream) 
     const size_t most = (size_t)kOneCtaPages * kCountersPerPage * sizeof(int);
     if (compact)
         return launch_team(pages_compact_kernel<1>, pages_compact_kernel<kPageCtas>, a,
-                           a.num_pages <= kOneCtaPages && entries <= kOneCtaWork, counters, most, &compact_mask, stream);
+                           a.num_pages <= kOneCtaPages && a.num_pages + 2 * entries <= kOneCtaCompact, counters, most,
+                           &compact_mask, stream);
     const bool small = a.num_pages <= kOneCtaPages && entries <= kOneCtaEntries &&
-                       (long long)a.rows * row_lanes(a.pages_per_row) <= kOneCtaWork;
+                       (long long)a.rows * row_lanes(a.pages_per_row) <= kOneCtaLanes;
     return launch_team(pages_update_kernel<1>, pages_update_kernel<kPageCtas>, a, small, counters + entries * sizeof(int),
                        most + kOneCtaEntries * sizeof(int), &update_mask, stream);
 }
