@@ -271,7 +271,8 @@ size_t pdattn_shared_workspace_size(const pdattn_params* p, int32_t n_groups);
  * call then writes nothing.  The entries of any row of a group may be read for
  * its shared pages, and a bad one is PDATTN_EBADPAGE.  Groups that share little
  * (fewer than 6 pages, or 24 page reads saved in all) and groups of which a
- * window hides some position from some row are attended row by row.
+ * window hides some position from some row are attended row by row, which
+ * pdattn_decode_fused does faster where it is so for most rows.
  * dtype bf16 (PDATTN_EUNSUPPORTED otherwise; f32 rows may share pages in
  * pdattn_decode_fused).  chunk_pages is not used.  n_groups is at most the one
  * the workspace was sized for; a plan that the workspace held is withdrawn

@@ -54,8 +54,9 @@ constexpr float kRescaleLog2 = 8.0f;    // lazy rescale threshold (log2 units)
 // 2^31 a weight of 2^128 or of nothing, and beside the own pages' weights, whose
 // products are rounded, a factor of 2^(2^-24 |score|).  Past kFar, where that
 // factor reaches 2^-12, products are rounded here too.  (That the case is looked
-// for takes 64 rows 44.6 instead of 43.8 us and 256 rows 156.7 instead of 156.2;
-// as a loop of its own over S in tensor memory 45.7 and 156.4.)
+// for takes a call of 64 rows 44.6 instead of 43.8 us and one of 256 rows 156.7
+// instead of 156.2, graph replays 41.4 and 41.3, 154.0 and 153.8; as a loop of its
+// own over S in tensor memory calls took 45.7 and 156.4.)
 constexpr float kFar = 4096.f;
 constexpr int kPieceSlots = 4;
 constexpr int kPieceReaders = 9;        // the issuing warp and the eight softmax warps
@@ -589,9 +590,12 @@ __device__ __forceinline__ void prefix_cta(const CUtensorMap& q_map, const CUten
 // tensor cores and their softmax, the rows' own ones by HBM, so that side by
 // side each takes what the other leaves.  The number of CTAs of each kind goes
 // by what a block of 128 keys for one half of a tile and an own page take on an
-// SM (10 ns).  (A unit at 105 and 135: 256 rows in six groups 159.6 and 155.6 us,
-// 153.8 between; 40 rows under 200 pages 36.5 and 41.0.  Head dim 64, 80 and 90:
-// 64 rows under 32 pages 49.0 and 41.1; 128 under 100 79.2 and 76.2, at 100 73.8.)
+// SM (10 ns).  Graph replays, us: at head dim 128 a unit at 105, 118, 130 and 135,
+// 256 rows in six groups 155.1, 152.3, 153.7 and 154.5; 40 rows under 200 pages
+// 35.8, 37.1, 39.5 and 39.4.  Head dim 64 at 80, 90, 100 and 120, 64 rows under 32
+// pages 50.0, 41.9, 42.0 and 46.3; 128 rows under 100 69.6, 68.5, 67.3 and 64.8.
+// (The costs differ by what else the launch does; the shared pages have no
+// cursor that would make up for it.)
 constexpr int kUnitCost[2] = {100, 118};    // head dim 64, 128
 constexpr int kPageCost[2] = {40, 36};
 constexpr int kItemPages = 3;               // what a pair's start and end cost, in pages
@@ -648,8 +652,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
 // latency: the loads of a batch of kBatch partials go out together, and where
 // there are more blocks than fit at once, batches are small and more do.  Few
 // rows are cut into many pieces, which kLanes lanes then share (24 rows of 19
-// pieces and two own ones: the call 66.4 us with four, 67.5 with two, 68.6 with
-// one; batches of 12 to 24 instead: 68.9 to 72.6).
+// pieces and two own ones: a graph replay 63.4 us with four, 64.2 with two, 66.3
+// with one; batches of 12 and 24 instead: 65.8, 69.7).
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWide = 6;         // blocks per SM that fit with batches of 8
 constexpr int kJoinFew = 2;          // blocks per SM that leave room for four times as many
