@@ -1225,7 +1225,8 @@ pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* 
     }
     // Positions of up to 2^31 multiply what a frequency is off by, which in
     // double (2^-55 turns) would be 2^-24 turns there; long double has 64 bits
-    // of precision or more.
+    // of precision or more.  (It is done by software on Arm, so pair i's power
+    // is the product of two out of sixteen.)
     using real = long double;
     const real pairs = c.rot_dim / 2, log_theta = std::log((real)c.theta);
     // the ramp's ends, in pairs
@@ -1246,8 +1247,13 @@ pdattn_status pdattn_rotary_make(const pdattn_rotary_spec* spec, pdattn_rotary* 
     r.interleaved = c.interleaved;
     r.gain = (float)(c.gain > 0.0 ? c.gain : c.scaling == PDATTN_ROTARY_RAMP ? 0.1 * std::log(c.factor) + 1.0 : 1.0);
     r.made = kRotaryMade;
+    real ones[8], eights[8];
+    for (int i = 0; i < 8; ++i) {
+        ones[i] = std::exp(-(real)i * log_theta / pairs);
+        eights[i] = std::exp(-(real)(8 * i) * log_theta / pairs);
+    }
     for (int i = 0; i < c.rot_dim / 2; ++i) {
-        const real f = std::exp(-(real)i * log_theta / pairs);
+        const real f = eights[i / 8] * ones[i % 8];
         real s = 1;                                     // share of f, the rest of f / factor
         if (c.scaling == PDATTN_ROTARY_LINEAR) s = 0;
         if (c.scaling == PDATTN_ROTARY_WAVELENGTH)

@@ -50,15 +50,15 @@ def turns(theta, rot, scaling="none", factor=1.0, low=1.0, high=1.0, original_le
 @pytest.mark.parametrize("theta,rot", [(10000.0, 64), (500000.0, 128), (150000.0, 64), (1e7, 48), (1.5, 16)])
 def test_frequencies_have_64_bits(b, theta, rot, spec):
     """In a format of 64 bits (rounding 2^-64 of a value): the logarithm, its product with i / pairs and the power are
-    each off by 2^-64, the first two of an exponent of at most x = log(theta), so a frequency by (2 x + 1) 2^-64 of itself,
-    and e^-x (2 x + 1) <= 1.22; five more products and sums and 2 pi.  The share of a scaled one is off by as much times
+    each off by 2^-64, the first two of an exponent of x <= log(theta), so a frequency, the product of two powers, by
+    (2 x + 3) 2^-64 of itself, and e^-x (2 x + 3) <= 3; five more products and sums and 2 pi.  The share of a scaled one is off by as much times
     how steep it is: f by high / (high - low) on the wavelengths', and on the ramp's, whose ends (up to 128 pairs)
     are off by 6 roundings, by 128 * 6 over a width of two pairs at least, or by none where its ends are whole pairs.  The
     result is a whole number of 2^-64 turns, f at most 1 / (2 pi)."""
     r = b.make_rotary(128, theta, rot_dim=rot, **SPECS[spec])
     want = turns(theta, rot, **SPECS[spec])
     steep = {"wavelength": 4.0 * 4 / 3, "ramp": 384.0, "whole": 0.0}.get(spec, 0.0)
-    off = (1.22 + 6 + steep) / (2 * math.pi) + 0.5
+    off = (3 + 6 + steep) / (2 * math.pi) + 0.5
     worst = max(abs(Decimal(t) - w * 2 ** 64) for t, w in zip(r.turns, want))
     assert worst <= off, float(worst)
 
